@@ -395,3 +395,8 @@ def pack_weights(w_gate, w_up, w_down):
     out = torch.empty(n, dtype=torch.uint8, device=w_gate.device)
     lc_moe_pack_weights(shape, w_gate, w_up, w_down, out)
     return out
+
+
+# ---- training operators (include/lc_moe_train.h) ----------------------------------------
+from .train import (AdamW, adamw_state, balance_loss, forward_saved, gate_backward,  # noqa: E402,F401
+                    layer_backward, router_backward)
