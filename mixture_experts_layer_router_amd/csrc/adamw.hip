@@ -13,8 +13,7 @@ namespace lcm {
 
 namespace aw {
 
-constexpr int kMaxTensors = 32;  // descriptors per launch (kernel arguments stay below 4 KB)
-constexpr int kChunk = 2048;     // elements per workgroup: 256 threads x 8
+constexpr int kStrip = 2048;  // elements a workgroup takes at a time: 256 threads x 8
 
 struct Desc {
   void* param;
@@ -26,21 +25,48 @@ struct Desc {
   uint8_t* vs;
   int64_t n;
   float wd, lrs;
-  int64_t at;      // first element of this launch's piece (a multiple of kChunk)
-  uint32_t first;  // first workgroup of the piece
+  uint32_t at;     // first strip of this launch's piece of the tensor
   uint32_t flags;  // 1: param bf16, 2: grad bf16; place in the caller's list << 2
 };
-struct Args {
-  Desc t[kMaxTensors];
-  int count;  // pieces of this launch
+struct Hyper {
   float lr, beta1, omb1, beta2, omb2, eps;
-  double ln1, ln2;  // log(beta1), log(beta2); -infinity for 0
-  int step;
+  double p1, p2;  // beta1^step, beta2^step
+  uint32_t seed;
+  int step, strips;  // strips of a workgroup
   const int32_t* step_dev;
   const float* grad_scale;
-  uint32_t seed;
 };
-static_assert(sizeof(Args) <= 4000, "kernel arguments");
+// Descriptors per launch: as many as fit in 4000 bytes of kernel arguments with the first
+// workgroup of each piece beside them.
+constexpr int kMaxTensors = int((4000 - sizeof(Hyper) - 8) / (sizeof(Desc) + 4));
+struct Args {
+  Hyper h;
+  int count;
+  uint32_t first[kMaxTensors];
+  Desc t[kMaxTensors];
+};
+static_assert(sizeof(Args) <= 4096, "kernel arguments");
+
+// beta^t by squaring, products only: the same bits on the host and on the device.
+__host__ __device__ inline double power(double b, int t) {
+#pragma clang fp contract(off)
+  double r = 1.;
+  for (; t; t >>= 1) {
+    if (t & 1) r = r * b;
+    b = b * b;
+  }
+  return r;
+}
+// The step's scalars of a tensor: the rate over 1 - beta1^t, 1 / sqrt(1 - beta2^t), the decay.
+struct Scalars {
+  float rate, root, keep;
+};
+__device__ __forceinline__ Scalars scalars(const Hyper& h, float lrs, float wd, double p1, double p2) {
+#pragma clang fp contract(off)
+  const double lr = double(h.lr) * lrs;
+  return Scalars{static_cast<float>(lr / (1. - p1)), static_cast<float>(1. / sqrt(1. - p2)),
+                 static_cast<float>(1. - lr * wd)};
+}
 
 // a * b and a + b, each rounded by itself: the compiler may not join them into one
 // multiply-add, so the states (and the codes taken from them) are the formula's to the bit.
@@ -64,21 +90,27 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 }
 
 // E4M3 code of |y| <= 448 rounded down or up by the 20-bit fraction r: the digits below the
-// code's last place plus r carry into it with probability (their size) / (one step).
+// code's last place plus r carry into it with probability (their size) / (one step).  SMALL:
+// y may be below 2^-6, where the code's steps are 2^-9 whatever the exponent.
+template <bool SMALL>
 __device__ __forceinline__ uint32_t e4m3_random(float y, uint32_t r) {
   const float a = fabsf(y);
-  uint32_t q;
-  if (a < 0.015625f) q = static_cast<uint32_t>(add(a * 512.f, static_cast<float>(r) * 9.5367431640625e-07f));
-  else q = ((__float_as_uint(a) + r) >> 20) - 960u;
+  uint32_t q = (__float_as_uint(a) + (r - (960u << 20))) >> 20;
+  if constexpr (SMALL) {
+    const uint32_t s = static_cast<uint32_t>(add(a * 512.f, static_cast<float>(r) * 9.5367431640625e-07f));
+    q = a < 0.015625f ? s : q;
+  }
   q = q < 126u ? q : 126u;
-  return q | (y < 0.f ? 128u : 0u);
+  return q | ((__float_as_uint(y) >> 24) & 128u);
 }
 
-// Value of an E4M3 code (finite codes only).
-__device__ __forceinline__ float e4m3_value(uint32_t c) {
-  const uint32_t e = (c >> 3) & 15u, f = c & 7u;
-  const float a = e ? __uint_as_float(((e + 120u) << 23) | (f << 20)) : static_cast<float>(f) * 0.001953125f;
-  return c & 128u ? -a : a;
+// The square root rounded to nearest for 2^-100 <= v < infinity: v / sqrt(v) from the
+// hardware's reciprocal root (one ulp) and one correction by the exact residual, which leaves
+// about 2^-46 before the last rounding.
+__device__ __forceinline__ float root_of(float v) {
+  const float y = __builtin_amdgcn_rsqf(v);
+  const float s = v * y;
+  return fmaf(fmaf(-s, s, v), 0.5f * y, s);
 }
 
 __device__ __forceinline__ float pow2(int k) {  // 2^k, k in -127..127
@@ -118,7 +150,10 @@ __device__ __forceinline__ void store8(void* p, bool bf, int64_t i, int cnt, con
     if (cnt == 8) {
       uint32_t u[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) u[c] = f2bf(o[2 * c]) | (uint32_t(f2bf(o[2 * c + 1])) << 16);
+      for (int c = 0; c < 4; ++c) {  // v_cvt_pk_bf16_f32, nearest even
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        u[c] = __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(o[2 * c]), static_cast<__bf16>(o[2 * c + 1])});
+      }
       *reinterpret_cast<uint4*>(q) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
 #pragma unroll
@@ -158,22 +193,45 @@ __device__ __forceinline__ void store_codes(void* p, int64_t i, int cnt, uint2 v
     if (c < cnt) q[c] = uint8_t((c < 4 ? v.x : v.y) >> (8 * (c & 3)));
 }
 
-// Block exponent (at least -127) of 16 lanes x 8 values.
+// Block exponent (at least -127) of the 8 values of each of a row of 16 lanes.
+template <int CTRL>
+__device__ __forceinline__ float row_max(float v) {
+  return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 15, 15, true)));
+}
 __device__ __forceinline__ int block_k(const float (&val)[8]) {
   float amax = 0.f;
 #pragma unroll
   for (int c = 0; c < 8; ++c) amax = fmaxf(amax, fabsf(val[c]));
-#pragma unroll
-  for (int o = 8; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+  // rotations of the row by 8, 4, 2, 1 lanes
+  amax = row_max<0x121>(row_max<0x122>(row_max<0x124>(row_max<0x128>(amax))));
   const int k = block_exp(amax);
   return k < -127 ? -127 : k;
 }
 
+template <bool SMALL>
+__device__ __forceinline__ void encode(const float (&m)[8], const float (&r)[8], float im, float iv, uint32_t first,
+                                       uint2& cm, uint2& cv) {
+  uint32_t qm[2] = {0, 0}, qv[2] = {0, 0};
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t u = mix(first + c);
+    qm[c >> 2] |= e4m3_random<SMALL>(m[c] * im, ((u & 0xFFFFu) << 4) + 8u) << (8 * (c & 3));
+    uint32_t q = e4m3_random<SMALL>(r[c] * iv, ((u >> 16) << 4) + 8u);
+    if (SMALL) q = r[c] > 0.f && q == 0u ? 1u : q;  // (a code of 8 or more else)
+    qv[c >> 2] |= q << (8 * (c & 3));
+  }
+  cm = make_uint2(qm[0], qm[1]);
+  cv = make_uint2(qv[0], qv[1]);
+}
+
 }  // namespace aw
 
+// One workgroup takes h.strips strips of one tensor, one after another; a thread has 8
+// consecutive elements of a strip, a row of 16 lanes one block of the 8-bit states.
 template <int BITS>
 __global__ __launch_bounds__(256) void adamw_kernel(aw::Args a) {
   using namespace aw;
+  const Hyper& h = a.h;
   // 8 bits: 2^-k of every exponent byte, from the math library's powf.  It may be an ulp off
   // the power of two, 2^-20 of a code's step; tensor libraries scale by it too, so the codes
   // equal those of a program that computes the step with elementary tensor operations.
@@ -183,70 +241,91 @@ __global__ __launch_bounds__(256) void adamw_kernel(aw::Args a) {
     __syncthreads();
   }
   int ti = 0;
-  for (int i = 1; i < a.count; ++i) ti = a.t[i].first <= blockIdx.x ? i : ti;
+  for (int i = 1; i < a.count; ++i) ti = a.first[i] <= blockIdx.x ? i : ti;
   const Desc& t = a.t[ti];
   float gs = 1.f;
-  if (a.grad_scale) {
-    gs = *a.grad_scale;
+  if (h.grad_scale) {
+    gs = *h.grad_scale;
     if (!(fabsf(gs) < INFINITY)) return;
   }
-  int step = a.step_dev ? *a.step_dev : a.step;
-  step = step < 1 ? 1 : step;
-  // 1 - beta^step = -expm1(step log beta)
-  const float rate = static_cast<float>(double(a.lr) * t.lrs / -expm1(step * a.ln1));
-  const float root = static_cast<float>(1. / sqrt(-expm1(step * a.ln2)));
-  const float keep = static_cast<float>(1. - double(a.lr) * t.lrs * t.wd);
-  const int64_t i = t.at + int64_t(blockIdx.x - t.first) * kChunk + threadIdx.x * 8;
-  const int cnt = t.n - i >= 8 ? 8 : t.n > i ? int(t.n - i) : 0;
-  float g[8], w[8], m[8], v[8], r[8];
-  load8(t.grad, t.flags & 2, i, cnt, g);
-  if (t.master) load8(t.master, false, i, cnt, w);
-  else load8(t.param, t.flags & 1, i, cnt, w);
-  if constexpr (BITS == 32) {
-    load8(t.m, false, i, cnt, m);
-    load8(t.v, false, i, cnt, v);
-  } else {
-    const uint2 cm = load_codes(t.m, i, cnt), cv = load_codes(t.v, i, cnt);
-    const float sm = cnt ? pow2(int(t.ms[i >> 7]) - 127) : 0.f, sv = cnt ? pow2(int(t.vs[i >> 7]) - 127) : 0.f;
+  int step = h.step;
+  double p1 = h.p1, p2 = h.p2;
+  if (h.step_dev) {
+    step = *h.step_dev;
+    step = step < 1 ? 1 : step;
+    p1 = power(double(h.beta1), step);
+    p2 = power(double(h.beta2), step);
+  }
+  const Scalars sc = scalars(h, t.lrs, t.wd, p1, p2);
+  const uint32_t key0 = mix(h.seed + 0x9E3779B9u * uint32_t(step)) + 0x3C6EF373u * ((t.flags >> 2) + 1u);
+  const int64_t strip0 = int64_t(t.at) + int64_t(blockIdx.x - a.first[ti]) * h.strips;
+  for (int s = 0; s < h.strips; ++s) {
+    if ((strip0 + s) * kStrip >= t.n) break;
+    const int64_t i = (strip0 + s) * kStrip + threadIdx.x * 8;
+    const int cnt = t.n - i >= 8 ? 8 : t.n > i ? int(t.n - i) : 0;
+    float g[8], w[8], m[8], v[8], r[8];
+    load8(t.grad, t.flags & 2, i, cnt, g);
+    if (t.master) load8(t.master, false, i, cnt, w);
+    else load8(t.param, t.flags & 1, i, cnt, w);
+    if constexpr (BITS == 32) {
+      load8(t.m, false, i, cnt, m);
+      load8(t.v, false, i, cnt, v);
+    } else {
+      const uint2 cm = load_codes(t.m, i, cnt), cv = load_codes(t.v, i, cnt);
+      const float sm = cnt ? pow2(int(t.ms[i >> 7]) - 127) : 0.f, sv = cnt ? pow2(int(t.vs[i >> 7]) - 127) : 0.f;
+      const uint32_t um[2] = {cm.x, cm.y}, uv[2] = {cv.x, cv.y};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {  // two codes at a time (v_cvt_pk_f32_fp8: E4M3 on gfx950)
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+        const f32x2 dm = c & 1 ? __builtin_amdgcn_cvt_pk_f32_fp8(um[c >> 1], true) : __builtin_amdgcn_cvt_pk_f32_fp8(um[c >> 1], false);
+        const f32x2 dv = c & 1 ? __builtin_amdgcn_cvt_pk_f32_fp8(uv[c >> 1], true) : __builtin_amdgcn_cvt_pk_f32_fp8(uv[c >> 1], false);
+        m[2 * c] = dm[0] * sm;
+        m[2 * c + 1] = dm[1] * sm;
+        const float r0 = dv[0] * sv, r1 = dv[1] * sv;
+        v[2 * c] = mul(r0, r0);
+        v[2 * c + 1] = mul(r1, r1);
+      }
+    }
+    float least = INFINITY;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      m[c] = e4m3_value(((c < 4 ? cm.x : cm.y) >> (8 * (c & 3))) & 255u) * sm;
-      const float q = e4m3_value(((c < 4 ? cv.x : cv.y) >> (8 * (c & 3))) & 255u) * sv;
-      v[c] = mul(q, q);
+      const float gr = mul(g[c], gs);
+      m[c] = add(mul(h.beta1, m[c]), mul(h.omb1, gr));
+      v[c] = add(mul(h.beta2, v[c]), mul(mul(h.omb2, gr), gr));
+      least = fminf(least, v[c]);
     }
-  }
+    if (__any(least < 7.888609052210118e-31f)) {  // 2^-100
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const float gr = mul(g[c], gs);
-    m[c] = add(mul(a.beta1, m[c]), mul(a.omb1, gr));
-    v[c] = add(mul(a.beta2, v[c]), mul(mul(a.omb2, gr), gr));
-    r[c] = sqrtf(v[c]);  // rounded to nearest (the default of this compiler)
-    w[c] = w[c] * keep - rate * (m[c] / (r[c] * root + a.eps));
-  }
-  if (t.master) store8(t.master, false, i, cnt, w);
-  store8(t.param, t.flags & 1, i, cnt, w);
-  if constexpr (BITS == 32) {
-    store8(t.m, false, i, cnt, m);
-    store8(t.v, false, i, cnt, v);
-  } else {
-    const uint32_t key = mix(mix(a.seed + 0x9E3779B9u * uint32_t(step)) + 0x3C6EF373u * ((t.flags >> 2) + 1u) +
-                             0x85A308D3u * uint32_t(uint64_t(i) >> 32));
-    const int km = block_k(m), kv = block_k(r);
-    const float im = inverse[km + 127], iv = inverse[kv + 127];
-    uint32_t qm[2] = {0, 0}, qv[2] = {0, 0};
+      for (int c = 0; c < 8; ++c) r[c] = sqrtf(v[c]);
+    } else {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const uint32_t u = mix(uint32_t(i) + c + key);
-      qm[c >> 2] |= e4m3_random(m[c] * im, ((u & 0xFFFFu) << 4) + 8u) << (8 * (c & 3));
-      uint32_t q = e4m3_random(r[c] * iv, ((u >> 16) << 4) + 8u);
-      q = r[c] > 0.f && q == 0u ? 1u : q;
-      qv[c >> 2] |= q << (8 * (c & 3));
+      for (int c = 0; c < 8; ++c) r[c] = root_of(v[c]);
     }
-    store_codes(t.m, i, cnt, make_uint2(qm[0], qm[1]));
-    store_codes(t.v, i, cnt, make_uint2(qv[0], qv[1]));
-    if ((threadIdx.x & 15) == 0 && cnt) {
-      t.ms[i >> 7] = uint8_t(km + 127);
-      t.vs[i >> 7] = uint8_t(kv + 127);
+    // the quotient by the hardware's reciprocal: within two ulps of the update
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      w[c] = w[c] * sc.keep - sc.rate * (m[c] * __builtin_amdgcn_rcpf(fmaf(r[c], sc.root, h.eps)));
+    if (t.master) store8(t.master, false, i, cnt, w);
+    store8(t.param, t.flags & 1, i, cnt, w);
+    if constexpr (BITS == 32) {
+      store8(t.m, false, i, cnt, m);
+      store8(t.v, false, i, cnt, v);
+    } else {
+      const uint32_t key = mix(key0 + 0x85A308D3u * uint32_t(uint64_t(i) >> 32));
+      const int km = block_k(m), kv = block_k(r);
+      const float im = inverse[km + 127], iv = inverse[kv + 127];
+      float low = INFINITY;  // the smallest quotient of the thread
+#pragma unroll
+      for (int c = 0; c < 8; ++c) low = fminf(low, fminf(fabsf(m[c]) * im, r[c] * iv));
+      uint2 cm, cv;
+      if (__any(low < 0.015625f)) encode<true>(m, r, im, iv, uint32_t(i) + key, cm, cv);
+      else encode<false>(m, r, im, iv, uint32_t(i) + key, cm, cv);
+      store_codes(t.m, i, cnt, cm);
+      store_codes(t.v, i, cnt, cv);
+      if ((threadIdx.x & 15) == 0 && cnt) {
+        t.ms[i >> 7] = uint8_t(km + 127);
+        t.vs[i >> 7] = uint8_t(kv + 127);
+      }
     }
   }
 }
@@ -254,20 +333,25 @@ __global__ __launch_bounds__(256) void adamw_kernel(aw::Args a) {
 hipError_t launch_adamw(const lc_moe_adamw_tensor* tensors, int count, const lc_moe_adamw_hyper& h, hipStream_t st) {
   using namespace aw;
   Args a{};
-  a.lr = h.lr;
-  a.beta1 = h.beta1;
-  a.omb1 = static_cast<float>(1. - double(h.beta1));
-  a.beta2 = h.beta2;
-  a.omb2 = static_cast<float>(1. - double(h.beta2));
-  a.eps = h.eps;
-  a.ln1 = std::log(double(h.beta1));
-  a.ln2 = std::log(double(h.beta2));
-  a.step = h.step;
-  a.step_dev = h.step_dev;
-  a.grad_scale = h.grad_scale;
-  a.seed = h.seed;
+  a.h.lr = h.lr;
+  a.h.beta1 = h.beta1;
+  a.h.omb1 = static_cast<float>(1. - double(h.beta1));
+  a.h.beta2 = h.beta2;
+  a.h.omb2 = static_cast<float>(1. - double(h.beta2));
+  a.h.eps = h.eps;
+  a.h.seed = h.seed;
+  a.h.step = h.step;
+  a.h.step_dev = h.step_dev;
+  a.h.grad_scale = h.grad_scale;
+  a.h.p1 = power(double(h.beta1), h.step_dev ? 1 : h.step);
+  a.h.p2 = power(double(h.beta2), h.step_dev ? 1 : h.step);
+  // strips of a workgroup: one where the step is small (its latency counts), else four, which
+  // share the workgroup's start
+  int64_t total = 0;
+  for (int i = 0; i < count; ++i) total += (tensors[i].n + kStrip - 1) / kStrip;
+  a.h.strips = total >= 8192 ? 4 : 1;
   // One launch covers up to kMaxTensors pieces and kMaxBlocks workgroups (the grid holds
-  // 2^32 - 1 work-items); a tensor that needs more is cut at a multiple of its blocks.
+  // 2^32 - 1 work-items); a tensor that needs more is cut at a multiple of its strips.
   constexpr int64_t kMaxBlocks = int64_t(1) << 23;
   int64_t blocks = 0;
   auto flush = [&]() -> hipError_t {
@@ -280,13 +364,15 @@ hipError_t launch_adamw(const lc_moe_adamw_tensor* tensors, int count, const lc_
   };
   for (int i = 0; i < count; ++i) {
     const lc_moe_adamw_tensor& t = tensors[i];
-    for (int64_t at = 0; at < t.n;) {
+    const int64_t strips = (t.n + kStrip - 1) / kStrip;
+    for (int64_t at = 0; at < strips;) {
       if (a.count == kMaxTensors || blocks == kMaxBlocks) {
         const hipError_t err = flush();
         if (err != hipSuccess) return err;
       }
-      int64_t take = (t.n - at + kChunk - 1) / kChunk;
+      int64_t take = (strips - at + a.h.strips - 1) / a.h.strips;
       if (take > kMaxBlocks - blocks) take = kMaxBlocks - blocks;
+      a.first[a.count] = uint32_t(blocks);
       Desc& d = a.t[a.count++];
       d.param = t.param;
       d.master = t.master;
@@ -298,11 +384,10 @@ hipError_t launch_adamw(const lc_moe_adamw_tensor* tensors, int count, const lc_
       d.n = t.n;
       d.wd = t.weight_decay;
       d.lrs = t.lr_scale;
-      d.at = at;
-      d.first = uint32_t(blocks);
+      d.at = uint32_t(at);
       d.flags = (t.param_dtype == LC_MOE_BF16 ? 1u : 0u) | (t.grad_dtype == LC_MOE_BF16 ? 2u : 0u) | (uint32_t(i) << 2);
       blocks += take;
-      at += take * kChunk;
+      at += take * a.h.strips;
     }
   }
   return flush();
