@@ -4,6 +4,7 @@
 // kMaxTensors a launch, so a step of a few dozen tensors is one launch and needs no device
 // table.
 #include <cmath>
+#include <type_traits>
 
 #include "fp8.h"
 #include "topk.h"
@@ -117,60 +118,80 @@ __device__ __forceinline__ float pow2(int k) {  // 2^k, k in -127..127
   return k >= -126 ? __uint_as_float(uint32_t(k + 127) << 23) : __uint_as_float(1u << 22);
 }
 
-// 8 elements of a tensor as fp32; cnt < 8 only at its end.
-__device__ __forceinline__ void load8(const void* p, bool bf, int64_t i, int cnt, float (&o)[8]) {
+// 4 elements of a tensor as fp32; cnt < 4 only at its end.
+__device__ __forceinline__ void load4(const void* p, bool bf, int64_t i, int cnt, float* o) {
   if (bf) {
     const bf16_t* q = static_cast<const bf16_t*>(p) + i;
-    if (cnt == 8) {
-      const uint4 w = *reinterpret_cast<const uint4*>(q);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        o[2 * c] = __uint_as_float(u[c] << 16);
-        o[2 * c + 1] = __uint_as_float(u[c] & 0xFFFF0000u);
-      }
+    if (cnt >= 4) {
+      const uint2 w = *reinterpret_cast<const uint2*>(q);
+      o[0] = __uint_as_float(w.x << 16), o[1] = __uint_as_float(w.x & 0xFFFF0000u);
+      o[2] = __uint_as_float(w.y << 16), o[3] = __uint_as_float(w.y & 0xFFFF0000u);
     } else {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) o[c] = c < cnt ? bf2f(q[c]) : 0.f;
+      for (int c = 0; c < 4; ++c) o[c] = c < cnt ? bf2f(q[c]) : 0.f;
     }
   } else {
     const float* q = static_cast<const float*>(p) + i;
-    if (cnt == 8) {
-      const float4 a = *reinterpret_cast<const float4*>(q), b = *reinterpret_cast<const float4*>(q + 4);
-      o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+    if (cnt >= 4) {
+      const float4 a = *reinterpret_cast<const float4*>(q);
+      o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w;
     } else {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) o[c] = c < cnt ? q[c] : 0.f;
+      for (int c = 0; c < 4; ++c) o[c] = c < cnt ? q[c] : 0.f;
     }
   }
 }
-__device__ __forceinline__ void store8(void* p, bool bf, int64_t i, int cnt, const float (&o)[8]) {
+// Two values to bf16, nearest even (v_cvt_pk_bf16_f32).
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
+}
+__device__ __forceinline__ void store4(void* p, bool bf, int64_t i, int cnt, const float* o) {
   if (bf) {
     bf16_t* q = static_cast<bf16_t*>(p) + i;
-    if (cnt == 8) {
-      uint32_t u[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {  // v_cvt_pk_bf16_f32, nearest even
-        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-        u[c] = __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(o[2 * c]), static_cast<__bf16>(o[2 * c + 1])});
-      }
-      *reinterpret_cast<uint4*>(q) = make_uint4(u[0], u[1], u[2], u[3]);
+    if (cnt >= 4) {
+      *reinterpret_cast<uint2*>(q) = make_uint2(pack2(o[0], o[1]), pack2(o[2], o[3]));
     } else {
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
+      for (int c = 0; c < 4; ++c)
         if (c < cnt) q[c] = f2bf(o[c]);
     }
   } else {
     float* q = static_cast<float*>(p) + i;
-    if (cnt == 8) {
+    if (cnt >= 4) {
       *reinterpret_cast<float4*>(q) = make_float4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<float4*>(q + 4) = make_float4(o[4], o[5], o[6], o[7]);
     } else {
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
+      for (int c = 0; c < 4; ++c)
         if (c < cnt) q[c] = o[c];
     }
   }
+}
+// A thread's 8 elements of a strip, in two groups of 4 that are GAP elements apart.
+template <int GAP>
+__device__ __forceinline__ void load8(const void* p, bool bf, int64_t i, const int (&cnt)[2], float (&o)[8]) {
+  if (GAP == 4 && bf && cnt[1] == 4) {  // 16 bytes
+    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const bf16_t*>(p) + i);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      o[2 * c] = __uint_as_float(u[c] << 16);
+      o[2 * c + 1] = __uint_as_float(u[c] & 0xFFFF0000u);
+    }
+    return;
+  }
+  load4(p, bf, i, cnt[0], o);
+  load4(p, bf, i + GAP, cnt[1], o + 4);
+}
+template <int GAP>
+__device__ __forceinline__ void store8(void* p, bool bf, int64_t i, const int (&cnt)[2], const float (&o)[8]) {
+  if (GAP == 4 && bf && cnt[1] == 4) {
+    *reinterpret_cast<uint4*>(static_cast<bf16_t*>(p) + i) =
+        make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
+    return;
+  }
+  store4(p, bf, i, cnt[0], o);
+  store4(p, bf, i + GAP, cnt[1], o + 4);
 }
 
 __device__ __forceinline__ uint2 load_codes(const void* p, int64_t i, int cnt) {
@@ -229,7 +250,7 @@ __device__ __forceinline__ void encode(const float (&m)[8], const float (&r)[8],
 // One workgroup takes h.strips strips of one tensor, one after another; a thread has 8
 // consecutive elements of a strip, a row of 16 lanes one block of the 8-bit states.
 template <int BITS>
-__global__ __launch_bounds__(256) void adamw_kernel(aw::Args a) {
+__global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args a) {
   using namespace aw;
   const Hyper& h = a.h;
   // 8 bits: 2^-k of every exponent byte, from the math library's powf.  It may be an ulp off
@@ -259,17 +280,23 @@ __global__ __launch_bounds__(256) void adamw_kernel(aw::Args a) {
   const Scalars sc = scalars(h, t.lrs, t.wd, p1, p2);
   const uint32_t key0 = mix(h.seed + 0x9E3779B9u * uint32_t(step)) + 0x3C6EF373u * ((t.flags >> 2) + 1u);
   const int64_t strip0 = int64_t(t.at) + int64_t(blockIdx.x - a.first[ti]) * h.strips;
-  for (int s = 0; s < h.strips; ++s) {
-    if ((strip0 + s) * kStrip >= t.n) break;
-    const int64_t i = (strip0 + s) * kStrip + threadIdx.x * 8;
-    const int cnt = t.n - i >= 8 ? 8 : t.n > i ? int(t.n - i) : 0;
+  // FULL: the strip lies inside the tensor, so no element's place is asked for
+  auto strip = [&](int64_t at, auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    // 32 bits: groups of 4 with a strip's half between them, so that every load and store of
+    // fp32 values is one contiguous piece of a wave; 8 bits: 8 consecutive elements
+    constexpr int GAP = BITS == 32 ? kStrip / 2 : 4;
+    const int64_t i = at + threadIdx.x * (BITS == 32 ? 4 : 8);
+    auto left = [&](int64_t e) { return FULL || t.n - e >= 4 ? 4 : t.n > e ? int(t.n - e) : 0; };
+    const int two[2] = {left(i), left(i + GAP)};
+    const int cnt = two[0] + two[1];  // (8 bits: the thread's elements)
     float g[8], w[8], m[8], v[8], r[8];
-    load8(t.grad, t.flags & 2, i, cnt, g);
-    if (t.master) load8(t.master, false, i, cnt, w);
-    else load8(t.param, t.flags & 1, i, cnt, w);
+    load8<GAP>(t.grad, t.flags & 2, i, two, g);
+    if (t.master) load8<GAP>(t.master, false, i, two, w);
+    else load8<GAP>(t.param, t.flags & 1, i, two, w);
     if constexpr (BITS == 32) {
-      load8(t.m, false, i, cnt, m);
-      load8(t.v, false, i, cnt, v);
+      load8<GAP>(t.m, false, i, two, m);
+      load8<GAP>(t.v, false, i, two, v);
     } else {
       const uint2 cm = load_codes(t.m, i, cnt), cv = load_codes(t.v, i, cnt);
       const float sm = cnt ? pow2(int(t.ms[i >> 7]) - 127) : 0.f, sv = cnt ? pow2(int(t.vs[i >> 7]) - 127) : 0.f;
@@ -305,11 +332,11 @@ __global__ __launch_bounds__(256) void adamw_kernel(aw::Args a) {
 #pragma unroll
     for (int c = 0; c < 8; ++c)
       w[c] = w[c] * sc.keep - sc.rate * (m[c] * __builtin_amdgcn_rcpf(fmaf(r[c], sc.root, h.eps)));
-    if (t.master) store8(t.master, false, i, cnt, w);
-    store8(t.param, t.flags & 1, i, cnt, w);
+    if (t.master) store8<GAP>(t.master, false, i, two, w);
+    store8<GAP>(t.param, t.flags & 1, i, two, w);
     if constexpr (BITS == 32) {
-      store8(t.m, false, i, cnt, m);
-      store8(t.v, false, i, cnt, v);
+      store8<GAP>(t.m, false, i, two, m);
+      store8<GAP>(t.v, false, i, two, v);
     } else {
       const uint32_t key = mix(key0 + 0x85A308D3u * uint32_t(uint64_t(i) >> 32));
       const int km = block_k(m), kv = block_k(r);
@@ -327,6 +354,11 @@ __global__ __launch_bounds__(256) void adamw_kernel(aw::Args a) {
         t.vs[i >> 7] = uint8_t(kv + 127);
       }
     }
+  };
+  for (int s = 0; s < h.strips; ++s) {
+    const int64_t at = (strip0 + s) * kStrip;
+    if (at + kStrip <= t.n) strip(at, std::true_type{});
+    else if (at < t.n) strip(at, std::false_type{});
   }
 }
 
@@ -345,11 +377,14 @@ hipError_t launch_adamw(const lc_moe_adamw_tensor* tensors, int count, const lc_
   a.h.grad_scale = h.grad_scale;
   a.h.p1 = power(double(h.beta1), h.step_dev ? 1 : h.step);
   a.h.p2 = power(double(h.beta2), h.step_dev ? 1 : h.step);
-  // strips of a workgroup: one where the step is small (its latency counts), else four, which
-  // share the workgroup's start
+  // Strips of a workgroup.  8 bits: eight share its start (the table of scales) where that
+  // leaves enough workgroups to fill the chip several times (403M weights: 842 us with four,
+  // 815 with eight, 818 with sixteen; a step of few elements is done sooner with one each).
+  // 32 bits: one, so that the workgroups in flight touch neighbouring memory (403M weights
+  // with masters: 2109 us with one, 2126 with two, 2171 with four).
   int64_t total = 0;
   for (int i = 0; i < count; ++i) total += (tensors[i].n + kStrip - 1) / kStrip;
-  a.h.strips = total >= 8192 ? 4 : 1;
+  a.h.strips = h.state_bits == 8 && total >= 16384 ? 8 : 1;
   // One launch covers up to kMaxTensors pieces and kMaxBlocks workgroups (the grid holds
   // 2^32 - 1 work-items); a tensor that needs more is cut at a multiple of its strips.
   constexpr int64_t kMaxBlocks = int64_t(1) << 23;
