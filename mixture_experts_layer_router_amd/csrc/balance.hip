@@ -1,9 +1,13 @@
 // Load-balance loss, per-expert counts, z loss and their gradient with respect to the router
-// logits (formulas in include/lc_moe_train.h).  Three passes: per-token softmax statistics
-// and per-block sums of the probabilities and counts; the sums over a sequence's blocks;
-// the gradient.  No atomics on floating-point values: every sum has a fixed order.
+// logits (formulas in include/lc_moe_train.h).  No atomics on floating-point values: every sum
+// has a fixed order.
+//
+// Three launches: softmax statistics of every token with each block's sums of probabilities
+// and counts (the logits are read once); the sums over a sequence's blocks; the losses and the
+// gradient (the logits are read again, from the memory-side cache where they fit).  A layer of
+// few logits does all of it in one workgroup and one launch.
 #include "train.h"
-#include "topk.h"
+#include "logit_row.h"
 
 namespace lcm {
 
@@ -13,231 +17,346 @@ __device__ __forceinline__ int seq_bound(const int32_t* __restrict__ off, int i,
   return v < 0 ? 0 : v > T ? T : v;
 }
 
-// One workgroup per kBalTok tokens, one wave per token at a time; expert e in lane e % 64.
-template <int EPL>
-__global__ __launch_bounds__(256) void balance_tokens_kernel(
-    const float* __restrict__ logits, const int32_t* __restrict__ idx, const int32_t* __restrict__ off, int S,
-    const uint8_t* __restrict__ mask, int T, int E, int K, TokStat* __restrict__ stat, float* __restrict__ part_p,
-    int32_t* __restrict__ part_c, int32_t* __restrict__ part_n, float* __restrict__ part_z) {
-  extern __shared__ int32_t lds[];
-  int32_t* cnt = lds;                                // [E]
-  float* ps = reinterpret_cast<float*>(lds + E);     // [E]
-  __shared__ int wn[4];
-  __shared__ float wz[4];
+struct BalArgs {
+  const float* logits;
+  const int32_t* idx;
+  const int32_t* off;
+  const uint8_t* mask;
+  int S, T, E, K, n_eb;
+  int tok, grad_tok;  // tokens of a workgroup: statistics, gradient
+  float balance, z;
+  TokStat* stat;
+  float* part_p;
+  int32_t* part_c;
+  int32_t* part_n;
+  float* part_z;
+  int32_t* seq_n;
+  float* seq_z;
+  float* seq_loss;
+  float* loss;
+  int32_t* load;
+  float* prob;
+  float* dlogits;
+};
+
+// f[s][i] for c picks among n tokens: E c / (K n), in fp64 (whole numbers up to 2^36).
+__device__ __forceinline__ float rel_load(int E, int K, int c, int n) {
+  return static_cast<float>(double(E) * c / (double(K) * n));
+}
+
+// The losses from the sequences' numbers (one workgroup of THREADS; fixed order).
+template <int THREADS>
+__device__ __forceinline__ void write_losses(const BalArgs& a) {
+  __shared__ double sl[THREADS], sz[THREADS];
+  __shared__ long long sn[THREADS];
+  __shared__ int sv[THREADS];
+  double l = 0., z = 0.;
+  long long n = 0;
+  int live = 0;
+  const int i = threadIdx.x;
+  for (int s = i; s < a.S; s += THREADS) {
+    n += a.seq_n[s];
+    live += a.seq_n[s] > 0;
+    z += a.seq_z[s];
+    for (int b = 0; b < a.n_eb; ++b) l += a.seq_loss[size_t(s) * a.n_eb + b];
+  }
+  sl[i] = l, sz[i] = z, sn[i] = n, sv[i] = live;
+  __syncthreads();
+  for (int h = THREADS / 2; h > 0; h >>= 1) {
+    if (i < h) sl[i] += sl[i + h], sz[i] += sz[i + h], sn[i] += sn[i + h], sv[i] += sv[i + h];
+    __syncthreads();
+  }
+  if (i == 0) {
+    a.loss[0] = sv[0] > 0 ? static_cast<float>(double(a.balance) / sv[0] * sl[0]) : 0.f;
+    a.loss[1] = sn[0] > 0 && a.z != 0.f ? static_cast<float>(double(a.z) / double(sn[0]) * sz[0]) : 0.f;
+  }
+}
+
+// Gradient of token t by one wave.  live, total: sequences with tokens that count, and those.
+template <int EPL, int V>
+__device__ __forceinline__ void token_grad(const BalArgs& a, int t, int lane, float (&p)[EPL], const TokStat& ts, int live,
+                                           long long total) {
+  float* out = a.dlogits + size_t(t) * a.E;
+  if (ts.seq < 0) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) p[i] = 0.f;
+    store_row<EPL, V>(out, a.E, lane, p);
+    return;
+  }
+  const int n = a.seq_n[ts.seq];
+  const long long kn = static_cast<long long>(a.K) * n;
+  const float scale = a.balance / (static_cast<float>(live) * static_cast<float>(kn) * static_cast<float>(n));
+  const float zl = a.z != 0.f ? 2.f * a.z / static_cast<float>(total) * ts.lse : 0.f;
+  float u[EPL], dot = 0.f;
+  const int32_t* cnt = a.load + size_t(ts.seq) * a.E;
+#pragma unroll
+  for (int j = 0; j < EPL / V; ++j) {
+    const int e = (j * 64 + lane) * V;
+    int c[V] = {};
+    if (e < a.E) {
+      if constexpr (V == 4) {
+        const int4 q = *reinterpret_cast<const int4*>(cnt + e);
+        c[0] = q.x, c[1] = q.y, c[2] = q.z, c[3] = q.w;
+      } else {
+        c[0] = cnt[e];
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < V; ++w)
+      u[j * V + w] = static_cast<float>(static_cast<long long>(a.E) * c[w] - kn) * scale;
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    p[i] = p[i] > -INFINITY ? exp_neg(p[i] - ts.m) * ts.rs : 0.f;
+    dot += p[i] * u[i];
+  }
+  dot = __ockl_wfred_add_f32(dot);
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) p[i] *= u[i] - dot + zl;
+  store_row<EPL, V>(out, a.E, lane, p);
+}
+
+// One workgroup of up to WAVES waves per a.tok tokens, a wave per token.  ONE: the only
+// workgroup; it finishes the sums, the losses and the gradient as well.
+template <int EPL, int V, int WAVES, bool ONE>
+__global__ __launch_bounds__(WAVES * 64) void balance_tokens_kernel(BalArgs a) {
+  __shared__ __attribute__((aligned(16))) float ps[WAVES][EPL * 64];  // a wave's sums of p
+  __shared__ int32_t cnt[EPL * 64];
+  __shared__ int wn[WAVES];
+  __shared__ float wz[WAVES], wl[WAVES];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int t0 = blockIdx.x * kBalTok, t1 = t0 + kBalTok < T ? t0 + kBalTok : T;
-  // the first sequence that ends behind t0
-  int s = 0, hi = S;
-  while (s < hi) {
-    const int mid = (s + hi) >> 1;
-    if (seq_bound(off, mid + 1, T) > t0) hi = mid;
-    else s = mid + 1;
+  const int T = a.T, E = a.E, K = a.K;
+  const int waves = blockDim.x >> 6, threads = blockDim.x;
+  const int t0 = blockIdx.x * a.tok, t1 = t0 + a.tok < T ? t0 + a.tok : T;
+  int s = 0;
+  if (!ONE) {  // the first sequence that ends behind t0
+    int hi = a.S;
+    while (s < hi) {
+      const int mid = (s + hi) >> 1;
+      if (seq_bound(a.off, mid + 1, T) > t0) hi = mid;
+      else s = mid + 1;
+    }
   }
   int done = t0;  // tokens before this one are dealt with
-  for (; s < S; ++s) {
-    const int lo = seq_bound(off, s, T), up = seq_bound(off, s + 1, T);
-    if (lo >= t1) break;
-    const int a = lo > done ? lo : done, b = up < t1 ? up : t1;
-    if (a >= b) continue;
-    for (int t = done + tid; t < a; t += 256) stat[t] = TokStat{0.f, 0.f, 0.f, -1};
-    done = b;
-    for (int e = tid; e < E; e += 256) cnt[e] = 0;
+  for (; s < a.S; ++s) {
+    const int lo = seq_bound(a.off, s, T), up = seq_bound(a.off, s + 1, T);
+    if (!ONE && lo >= t1) break;
+    const int first = lo > done ? lo : done, b = up < t1 ? up : t1;
+    const int tokens = b > first ? b - first : 0;
+    if (!ONE && tokens == 0) continue;
+    for (int t = done + tid; t < first && tokens; t += threads) a.stat[t] = TokStat{0.f, 0.f, 0.f, -1};
+    if (tokens) done = b;
+    for (int e = tid; e < E; e += threads) cnt[e] = 0;
     __syncthreads();
-    float acc[EPL];
+    float acc[EPL], v[EPL];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) acc[j] = 0.f;
+    for (int i = 0; i < EPL; ++i) acc[i] = 0.f;
     int n = 0;
     float z = 0.f;
-    for (int t = a + wave; t < b; t += 4) {
+    // the next token's row is on its way while this one's is worked on
+    float nxt[EPL];
+    bool take = false;
+    int t = first + wave;
+    if (t < b) {
+      take = !a.mask || a.mask[t];
+      if (take) load_row<EPL, V>(a.logits + size_t(t) * E, E, lane, -INFINITY, nxt);
+    }
+    for (; t < b; t += waves) {
+      const bool now = take;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[i] = nxt[i];
+      int pick = -1;
+      if (now && lane < K) pick = a.idx[size_t(t) * K + lane];
+      if (t + waves < b) {
+        take = !a.mask || a.mask[t + waves];
+        if (take) load_row<EPL, V>(a.logits + size_t(t + waves) * E, E, lane, -INFINITY, nxt);
+      }
       TokStat ts{0.f, 0.f, 0.f, -1};
-      if (!mask || mask[t]) {
-        float v[EPL], m = -INFINITY;
+      if (now) {
+        const RowSum r = softmax_row<EPL>(v);
+        if (r.m > -INFINITY) {
+          const float rs = 1.f / r.sum, lse = r.m + logf(r.sum);
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-          const int e = lane + 64 * j;
-          v[j] = e < E ? logits[size_t(t) * E + e] : -INFINITY;
-          m = fmaxf(m, v[j]);
-        }
-        m = __ockl_wfred_max_f32(m);
-        if (m > -INFINITY) {
-          float sum = 0.f;
-#pragma unroll
-          for (int j = 0; j < EPL; ++j) {
-            v[j] = expf(v[j] - m);
-            sum += v[j];
-          }
-          sum = __ockl_wfred_add_f32(sum);
-          const float rs = 1.f / sum, lse = m + logf(sum);
-#pragma unroll
-          for (int j = 0; j < EPL; ++j) acc[j] += v[j] * rs;
+          for (int i = 0; i < EPL; ++i) acc[i] = fmaf(v[i], rs, acc[i]);
           n += 1;
           z += lse * lse;
-          ts = TokStat{m, rs, lse, s};
-          for (int k = lane; k < K; k += 64) {
-            const int e = idx[size_t(t) * K + k];
+          ts = TokStat{r.m, rs, lse, s};
+          if (unsigned(pick) < unsigned(E)) atomicAdd(&cnt[pick], 1);
+          for (int k = lane + 64; k < K; k += 64) {
+            const int e = a.idx[size_t(t) * K + k];
             if (unsigned(e) < unsigned(E)) atomicAdd(&cnt[e], 1);
           }
         }
       }
-      if (lane == 0) stat[t] = ts;
+      if (lane == 0) a.stat[t] = ts;
     }
-    for (int w = 0; w < 4; ++w) {
-      if (wave == w) {
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-          const int e = lane + 64 * j;
-          if (e < E) ps[e] = w == 0 ? acc[j] : ps[e] + acc[j];
-        }
-      }
-      __syncthreads();
-    }
-    if (lane == 0) {
-      wn[wave] = n;
-      wz[wave] = z;
-    }
+    const int used = tokens < waves ? tokens : waves;  // waves that had a token
+    if (wave < used) store_row<EPL, V>(ps[wave], E, lane, acc);
+    if (lane == 0) wn[wave] = n, wz[wave] = z;
     __syncthreads();
-    const size_t row = size_t(blockIdx.x) + s;
-    for (int e = tid; e < E; e += 256) {
-      part_p[row * E + e] = ps[e];
-      part_c[row * E + e] = cnt[e];
-    }
-    if (tid == 0) {
-      part_n[row] = wn[0] + wn[1] + wn[2] + wn[3];
-      part_z[row] = (wz[0] + wz[1]) + (wz[2] + wz[3]);
+    int nsum = 0;
+    float zsum = 0.f;
+    for (int w = 0; w < used; ++w) nsum += wn[w], zsum += wz[w];
+    if constexpr (ONE) {
+      float term = 0.f;
+      for (int e = tid; e < E; e += threads) {
+        float p = 0.f;
+        for (int w = 0; w < used; ++w) p += ps[w][e];
+        const float mean = nsum > 0 ? p / static_cast<float>(nsum) : 0.f;
+        a.load[size_t(s) * E + e] = cnt[e];
+        a.prob[size_t(s) * E + e] = mean;
+        if (nsum > 0) term += rel_load(E, K, cnt[e], nsum) * mean;
+      }
+      term = __ockl_wfred_add_f32(term);
+      if (lane == 0) wl[wave] = term;
+      __syncthreads();
+      if (tid == 0) {
+        float l = 0.f;
+        for (int w = 0; w < waves; ++w) l += wl[w];
+        a.seq_loss[s] = l;
+        a.seq_n[s] = nsum;
+        a.seq_z[s] = zsum;
+      }
+    } else {
+      const size_t row = size_t(blockIdx.x) + s;
+      for (int e = tid; e < E; e += threads) {
+        float p = 0.f;
+        for (int w = 0; w < used; ++w) p += ps[w][e];
+        a.part_p[row * E + e] = p;
+        a.part_c[row * E + e] = cnt[e];
+      }
+      if (tid == 0) {
+        a.part_n[row] = nsum;
+        a.part_z[row] = zsum;
+      }
     }
     __syncthreads();
   }
-  for (int t = done + tid; t < t1; t += 256) stat[t] = TokStat{0.f, 0.f, 0.f, -1};
+  for (int t = done + tid; t < t1; t += threads) a.stat[t] = TokStat{0.f, 0.f, 0.f, -1};
+  if constexpr (ONE) {
+    __threadfence_block();
+    __syncthreads();
+    if (a.dlogits) {
+      long long total = 0;
+      int live = 0;
+      for (int q = 0; q < a.S; ++q) {
+        const int n = a.seq_n[q];
+        total += n;
+        live += n > 0;
+      }
+      for (int t = wave; t < T; t += waves) {
+        const TokStat ts = a.stat[t];
+        float v[EPL];
+        if (ts.seq >= 0) load_row<EPL, V>(a.logits + size_t(t) * E, E, lane, -INFINITY, v);
+        token_grad<EPL, V>(a, t, lane, v, ts, live, total);
+      }
+    }
+    write_losses<WAVES * 64>(a);
+  }
 }
 
-// Sums over a sequence's blocks: workgroup (block of 64 experts, sequence); wave w takes every
-// fourth block, the four are added in wave order.
-__global__ __launch_bounds__(256) void balance_sums_kernel(
-    const int32_t* __restrict__ off, int T, int E, int K, const float* __restrict__ part_p,
-    const int32_t* __restrict__ part_c, const int32_t* __restrict__ part_n, const float* __restrict__ part_z,
-    int32_t* __restrict__ load, float* __restrict__ prob, int32_t* __restrict__ seq_n, float* __restrict__ seq_z,
-    float* __restrict__ seq_loss) {
-  __shared__ float sp[4][64];
-  __shared__ int sc[4][64], sn[4];
-  __shared__ float sz[4];
+// Sums over a sequence's blocks: workgroup (64 experts, sequence); the 16 waves take every
+// sixteenth block each and are added in wave order.
+__global__ __launch_bounds__(1024) void balance_sums_kernel(BalArgs a) {
+  __shared__ float sp[16][64], sz[16];
+  __shared__ int sc[16][64], sn[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int s = blockIdx.y, e = blockIdx.x * 64 + lane;
-  const int lo = seq_bound(off, s, T), up = seq_bound(off, s + 1, T);
-  const int b0 = lo / kBalTok, b1 = up > lo ? (up - 1) / kBalTok + 1 : b0;
+  const int s = blockIdx.y, e = blockIdx.x * 64 + lane, E = a.E;
+  const int lo = seq_bound(a.off, s, a.T), up = seq_bound(a.off, s + 1, a.T);
+  const int b0 = lo / a.tok, b1 = up > lo ? (up - 1) / a.tok + 1 : b0;
+  const int ec = e < E ? e : E - 1;  // lanes past E repeat the last expert; never written
   float p = 0.f, z = 0.f;
   int c = 0, n = 0;
-  for (int b = b0 + wave; b < b1; b += 4) {
+#pragma unroll 4
+  for (int b = b0 + wave; b < b1; b += 16) {
     const size_t row = size_t(b) + s;
-    if (e < E) {
-      p += part_p[row * E + e];
-      c += part_c[row * E + e];
-    }
-    n += part_n[row];
-    z += part_z[row];
+    p += a.part_p[row * E + ec];
+    c += a.part_c[row * E + ec];
+    n += a.part_n[row];
+    z += a.part_z[row];
   }
   sp[wave][lane] = p;
   sc[wave][lane] = c;
-  if (lane == 0) {
-    sn[wave] = n;
-    sz[wave] = z;
-  }
+  if (lane == 0) sn[wave] = n, sz[wave] = z;
   __syncthreads();
   if (wave != 0) return;
-  n = sn[0] + sn[1] + sn[2] + sn[3];
-  p = (sp[0][lane] + sp[1][lane]) + (sp[2][lane] + sp[3][lane]);
-  c = sc[0][lane] + sc[1][lane] + sc[2][lane] + sc[3][lane];
+  p = z = 0.f;
+  c = n = 0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) p += sp[w][lane], c += sc[w][lane], n += sn[w], z += sz[w];
   float term = 0.f;
   if (e < E) {
     const float mean = n > 0 ? p / static_cast<float>(n) : 0.f;
-    load[size_t(s) * E + e] = c;
-    prob[size_t(s) * E + e] = mean;
-    if (n > 0) term = static_cast<float>(double(E) * c / (double(K) * n)) * mean;
+    a.load[size_t(s) * E + e] = c;
+    a.prob[size_t(s) * E + e] = mean;
+    if (n > 0) term = rel_load(E, a.K, c, n) * mean;
   }
   term = __ockl_wfred_add_f32(term);
   if (lane == 0) {
-    seq_loss[size_t(s) * gridDim.x + blockIdx.x] = term;
+    a.seq_loss[size_t(s) * a.n_eb + blockIdx.x] = term;
     if (blockIdx.x == 0) {
-      seq_n[s] = n;
-      seq_z[s] = (sz[0] + sz[1]) + (sz[2] + sz[3]);
+      a.seq_n[s] = n;
+      a.seq_z[s] = z;
     }
   }
 }
 
-// Totals over the sequences (one workgroup), the losses, and the gradient's two factors.
-__global__ __launch_bounds__(256) void balance_loss_kernel(int S, int n_eb, float balance, float zc,
-                                                           int32_t* __restrict__ seq_n,
-                                                           const float* __restrict__ seq_z,
-                                                           const float* __restrict__ seq_loss,
-                                                           float* __restrict__ loss, float* __restrict__ factors) {
-  __shared__ double sl[256], sz[256];
-  __shared__ long long sn[256];
-  __shared__ int sv[256];
-  double l = 0., z = 0.;
-  long long n = 0;
-  int live = 0;
-  for (int s = threadIdx.x; s < S; s += 256) {
-    n += seq_n[s];
-    live += seq_n[s] > 0;
-    z += seq_z[s];
-    for (int b = 0; b < n_eb; ++b) l += seq_loss[size_t(s) * n_eb + b];
-  }
-  const int i = threadIdx.x;
-  sl[i] = l;
-  sz[i] = z;
-  sn[i] = n;
-  sv[i] = live;
-  __syncthreads();
-  for (int h = 128; h > 0; h >>= 1) {
-    if (i < h) {
-      sl[i] += sl[i + h];
-      sz[i] += sz[i + h];
-      sn[i] += sn[i + h];
-      sv[i] += sv[i + h];
-    }
-    __syncthreads();
-  }
-  if (i == 0) {
-    loss[0] = sv[0] > 0 ? static_cast<float>(double(balance) / sv[0] * sl[0]) : 0.f;
-    loss[1] = sn[0] > 0 && zc != 0.f ? static_cast<float>(double(zc) / double(sn[0]) * sz[0]) : 0.f;
-    factors[0] = sv[0] > 0 ? static_cast<float>(double(balance) / sv[0]) : 0.f;
-    factors[1] = sn[0] > 0 ? static_cast<float>(2. * double(zc) / double(sn[0])) : 0.f;
-  }
-}
-
-// dlogits: one wave per token.
-template <int EPL>
-__global__ __launch_bounds__(256) void balance_grad_kernel(const float* __restrict__ logits, int T, int E, int K,
-                                                           const TokStat* __restrict__ stat,
-                                                           const int32_t* __restrict__ load,
-                                                           const int32_t* __restrict__ seq_n,
-                                                           const float* __restrict__ factors,
-                                                           float* __restrict__ dlogits) {
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (t >= T) return;
-  const TokStat ts = stat[t];
-  float* out = dlogits + size_t(t) * E;
-  if (ts.seq < 0) {
-    for (int e = lane; e < E; e += 64) out[e] = 0.f;
+// Workgroup 0: the losses.  The others: the gradient.
+template <int EPL, int V>
+__global__ __launch_bounds__(256) void balance_grad_kernel(BalArgs a) {
+  if (blockIdx.x == 0) {
+    write_losses<256>(a);
     return;
   }
-  const int n = seq_n[ts.seq];
-  const long long kn = static_cast<long long>(K) * n;
-  const float scale = factors[0] / (static_cast<float>(kn) * static_cast<float>(n));
-  const float zl = factors[1] != 0.f ? factors[1] * ts.lse : 0.f;
-  float p[EPL], u[EPL], dot = 0.f;
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const int e = lane + 64 * j;
-    p[j] = e < E ? expf(logits[size_t(t) * E + e] - ts.m) * ts.rs : 0.f;
-    u[j] = e < E ? static_cast<float>(static_cast<long long>(E) * load[size_t(ts.seq) * E + e] - kn) * scale : 0.f;
-    dot += p[j] * u[j];
+  __shared__ int wt[4], wl[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int t = (int(blockIdx.x) - 1) * a.grad_tok + wave;
+  const int t1 = int(blockIdx.x) * a.grad_tok < a.T ? int(blockIdx.x) * a.grad_tok : a.T;
+  float nxt[EPL], v[EPL];
+  TokStat nts{0.f, 0.f, 0.f, -1};
+  if (t < t1) {
+    nts = a.stat[t];
+    if (nts.seq >= 0) load_row<EPL, V>(a.logits + size_t(t) * a.E, a.E, lane, -INFINITY, nxt);
   }
-  dot = __ockl_wfred_add_f32(dot);
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const int e = lane + 64 * j;
-    if (e < E) out[e] = p[j] * (u[j] - dot + zl);
+  int total = 0, live = 0;  // tokens that count: at most T
+  for (int s = tid; s < a.S; s += 256) {
+    const int n = a.seq_n[s];
+    total += n;
+    live += n > 0;
   }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o), live += __shfl_xor(live, o);
+  if (lane == 0) wt[wave] = total, wl[wave] = live;
+  __syncthreads();
+  total = wt[0] + wt[1] + wt[2] + wt[3];
+  live = wl[0] + wl[1] + wl[2] + wl[3];
+  for (; t < t1; t += 4) {
+    const TokStat ts = nts;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) v[i] = nxt[i];
+    if (t + 4 < t1) {
+      nts = a.stat[t + 4];
+      if (nts.seq >= 0) load_row<EPL, V>(a.logits + size_t(t + 4) * a.E, a.E, lane, -INFINITY, nxt);
+    }
+    token_grad<EPL, V>(a, t, lane, v, ts, live, total);
+  }
+}
+
+template <int EPL, int V>
+static void launch_passes(const BalArgs& a, const BalPlan& p, hipStream_t st) {
+  // most waves of a workgroup: LDS holds one row of sums for each, at most 64 KB in all
+  // (T = 16384, E = 768: 38.7 us with 8 waves and 32 tokens, 39.8 with 16 and 64, 41 with 8 and
+  // 64 or 4 and 16)
+  constexpr int WAVES = EPL <= 32 ? 8 : 4;
+  if (p.one) {
+    hipLaunchKernelGGL((balance_tokens_kernel<EPL, V, WAVES, true>), dim3(1), dim3(WAVES * 64), 0, st, a);
+    return;
+  }
+  const int waves = p.tok < WAVES ? p.tok : WAVES;
+  hipLaunchKernelGGL((balance_tokens_kernel<EPL, V, WAVES, false>), dim3(p.nblocks), dim3(waves * 64), 0, st, a);
+  hipLaunchKernelGGL(balance_sums_kernel, dim3(p.n_eb, a.S), dim3(1024), 0, st, a);
+  const int grads = a.dlogits ? (a.T + a.grad_tok - 1) / a.grad_tok : 0;
+  hipLaunchKernelGGL((balance_grad_kernel<EPL, V>), dim3(1 + grads), dim3(256), 0, st, a);
 }
 
 hipError_t launch_balance_loss(const lc_moe_shape& s, const BalPlan& p, void* ws, float balance, float z,
@@ -246,35 +365,46 @@ hipError_t launch_balance_loss(const lc_moe_shape& s, const BalPlan& p, void* ws
                                hipStream_t st) {
   const int E = s.N + s.Z, epl = (E + 63) / 64;
   char* w = static_cast<char*>(ws);
-  TokStat* stat = reinterpret_cast<TokStat*>(w + p.stat);
-  float* part_p = reinterpret_cast<float*>(w + p.part_p);
-  int32_t* part_c = reinterpret_cast<int32_t*>(w + p.part_c);
-  int32_t* part_n = reinterpret_cast<int32_t*>(w + p.part_n);
-  float* part_z = reinterpret_cast<float*>(w + p.part_z);
-  int32_t* seq_n = reinterpret_cast<int32_t*>(w + p.seq_n);
-  float* seq_z = reinterpret_cast<float*>(w + p.seq_z);
-  float* seq_loss = reinterpret_cast<float*>(w + p.seq_loss);
-  float* factors = reinterpret_cast<float*>(w + p.factors);
-#define LCM_EPL(launch)            \
-  if (epl <= 2) launch(2);         \
-  else if (epl <= 4) launch(4);    \
-  else if (epl <= 8) launch(8);    \
-  else if (epl <= 16) launch(16);  \
-  else if (epl <= 32) launch(32);  \
-  else launch(64);
-#define LCM_TOKENS(n)                                                                                       \
-  hipLaunchKernelGGL(balance_tokens_kernel<n>, dim3(p.nblocks), dim3(256), size_t(E) * 8, st, logits, idx, \
-                     offsets, S, mask, s.T, E, s.K, stat, part_p, part_c, part_n, part_z)
-  LCM_EPL(LCM_TOKENS)
-  hipLaunchKernelGGL(balance_sums_kernel, dim3(p.n_eb, S), dim3(256), 0, st, offsets, s.T, E, s.K, part_p, part_c,
-                     part_n, part_z, load, prob, seq_n, seq_z, seq_loss);
-  hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(256), 0, st, S, p.n_eb, balance, z, seq_n, seq_z, seq_loss,
-                     loss, factors);
-  if (dlogits) {
-#define LCM_GRAD(n)                                                                                              \
-  hipLaunchKernelGGL(balance_grad_kernel<n>, dim3((s.T + 3) / 4), dim3(256), 0, st, logits, s.T, E, s.K, stat, \
-                     load, seq_n, factors, dlogits)
-    LCM_EPL(LCM_GRAD)
+  BalArgs a{};
+  a.logits = logits;
+  a.idx = idx;
+  a.off = offsets;
+  a.mask = mask;
+  a.S = S;
+  a.T = s.T;
+  a.E = E;
+  a.K = s.K;
+  a.n_eb = p.one ? 1 : p.n_eb;
+  a.tok = p.tok;
+  // enough workgroups to fill the chip, then four tokens a wave
+  a.grad_tok = s.T < 8192 ? 4 : 16;
+  a.balance = balance;
+  a.z = z;
+  a.stat = reinterpret_cast<TokStat*>(w + p.stat);
+  a.part_p = reinterpret_cast<float*>(w + p.part_p);
+  a.part_c = reinterpret_cast<int32_t*>(w + p.part_c);
+  a.part_n = reinterpret_cast<int32_t*>(w + p.part_n);
+  a.part_z = reinterpret_cast<float*>(w + p.part_z);
+  a.seq_n = reinterpret_cast<int32_t*>(w + p.seq_n);
+  a.seq_z = reinterpret_cast<float*>(w + p.seq_z);
+  a.seq_loss = reinterpret_cast<float*>(w + p.seq_loss);
+  a.loss = loss;
+  a.load = load;
+  a.prob = prob;
+  a.dlogits = dlogits;
+  if (E % 4 == 0) {
+    if (epl <= 4) launch_passes<4, 4>(a, p, st);
+    else if (epl <= 8) launch_passes<8, 4>(a, p, st);
+    else if (epl <= 12) launch_passes<12, 4>(a, p, st);
+    else if (epl <= 16) launch_passes<16, 4>(a, p, st);
+    else if (epl <= 32) launch_passes<32, 4>(a, p, st);
+    else launch_passes<64, 4>(a, p, st);
+  } else {
+    if (epl <= 2) launch_passes<2, 1>(a, p, st);
+    else if (epl <= 8) launch_passes<8, 1>(a, p, st);
+    else if (epl <= 16) launch_passes<16, 1>(a, p, st);
+    else if (epl <= 32) launch_passes<32, 1>(a, p, st);
+    else launch_passes<64, 1>(a, p, st);
   }
   return hipGetLastError();
 }

@@ -11,7 +11,7 @@
 #include "train.h"
 #include "lanes.h"
 #include "lds_dma.h"
-#include "topk.h"
+#include "logit_row.h"
 
 namespace lcm {
 
@@ -25,48 +25,23 @@ __device__ __forceinline__ void cut3(float v, bf16_t (&o)[3]) {
 }
 
 // ---------------------------------------------------------------------------------------
-// dlogits of one token per wave.  A lane holds EPL experts: V consecutive ones (V = 4 where
-// E is a multiple of 4: 16-byte loads; else 1) of every block of 64 V.  The picks' gradients
-// are added in pick order by the lane that holds the expert.
+// dlogits of one token per wave, the row in its registers as in logit_row.h.  The picks'
+// gradients are added in pick order by the lane that holds the expert.
 // ---------------------------------------------------------------------------------------
 template <int EPL, int V>
 __global__ __launch_bounds__(256) void dlogits_kernel(const float* __restrict__ logits,
                                                       const int32_t* __restrict__ idx,
                                                       const float* __restrict__ dgate, const float* aux, int T, int E,
                                                       int K, int Ep, float* out, bf16_t* __restrict__ parts) {
-  constexpr int J = EPL / V;  // blocks of 64 V experts
+  constexpr int J = EPL / V;  // runs of 64 V experts
   const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   if (t >= T) return;
-  auto load = [&](const float* p, float (&v)[EPL], float other) {
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int e = (j * 64 + lane) * V;
-      if constexpr (V == 4) {
-        const float4 q = e < E ? *reinterpret_cast<const float4*>(p + size_t(t) * E + e)
-                               : make_float4(other, other, other, other);
-        v[4 * j] = q.x, v[4 * j + 1] = q.y, v[4 * j + 2] = q.z, v[4 * j + 3] = q.w;
-      } else {
-        v[j] = e < E ? p[size_t(t) * E + e] : other;
-      }
-    }
-  };
   float v[EPL], ax[EPL];
-  if (dgate) load(logits, v, -INFINITY);
-  if (aux) load(aux, ax, 0.f);
+  if (dgate) load_row<EPL, V>(logits + size_t(t) * E, E, lane, -INFINITY, v);
+  if (aux) load_row<EPL, V>(aux + size_t(t) * E, E, lane, 0.f, ax);
   if (dgate) {
-    float m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) m = fmaxf(m, v[i]);
-    m = __ockl_wfred_max_f32(m);
-    const bool any = m > -INFINITY;  // else no expert has a probability
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      v[i] = any ? expf(v[i] - m) : 0.f;
-      sum += v[i];
-    }
-    sum = __ockl_wfred_add_f32(sum);
-    const float rs = any ? 1.f / sum : 0.f;
+    const RowSum r = softmax_row<EPL>(v);
+    const float rs = r.m > -INFINITY ? 1.f / r.sum : 0.f;
     float dp[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) dp[i] = 0.f;
@@ -481,6 +456,7 @@ hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, 
   if (E % 4 == 0) {
     if (epl <= 4) LCM_DL(4, 4);
     else if (epl <= 8) LCM_DL(8, 4);
+    else if (epl <= 12) LCM_DL(12, 4);
     else if (epl <= 16) LCM_DL(16, 4);
     else if (epl <= 32) LCM_DL(32, 4);
     else LCM_DL(64, 4);

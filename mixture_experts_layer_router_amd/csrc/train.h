@@ -7,25 +7,29 @@
 namespace lcm {
 
 // ---- balance loss --------------------------------------------------------------------
-// Tokens per block of the statistics pass.  A block's tokens may belong to several
+// The statistics pass cuts the tokens into blocks.  A block's tokens may belong to several
 // sequences; its share of sequence s is partial row (block + s): along the tokens either
 // the block or the sequence (or both) goes up from one share to the next, so these numbers
 // are all different and below blocks + sequences.
-constexpr int kBalTok = 64;
-
 struct TokStat {  // what the gradient needs of a token's softmax
   float m, rs, lse;  // largest logit, 1 / sum of exponentials, m + log of that sum
   int32_t seq;       // the token's sequence; -1: the token does not count
 };
 
 struct BalPlan {
-  size_t stat, part_p, part_c, part_n, part_z, seq_n, seq_z, seq_loss, factors, total;
-  int nblocks, nparts, n_eb;  // token blocks, partial rows, blocks of 64 experts
+  size_t stat, part_p, part_c, part_n, part_z, seq_n, seq_z, seq_loss, total;
+  int tok, nblocks, nparts, n_eb;  // tokens of a block, blocks, partial rows, runs of 64 experts
+  bool one;                        // all in one workgroup
 };
 inline BalPlan plan_balance(const lc_moe_shape& s, int S) {
   BalPlan p{};
   const size_t T = s.T, E = size_t(s.N) + s.Z;
-  p.nblocks = int((T + kBalTok - 1) / kBalTok);
+  // one block per CU until a block has 32 tokens (at least 4, a power of two)
+  p.tok = 4;
+  while (p.tok < 32 && size_t(p.tok) * 256 < T) p.tok *= 2;
+  p.one = T <= 64 && T * E <= 16384;
+  if (p.one) p.tok = 64;
+  p.nblocks = int((T + p.tok - 1) / p.tok);
   p.nparts = p.nblocks + S;
   p.n_eb = int((E + 63) / 64);
   size_t o = 0;
@@ -38,7 +42,6 @@ inline BalPlan plan_balance(const lc_moe_shape& s, int S) {
   p.seq_n = take(size_t(S) * 4);
   p.seq_z = take(size_t(S) * 4);
   p.seq_loss = take(size_t(S) * p.n_eb * 4);
-  p.factors = take(8);
   p.total = o;
   return p;
 }

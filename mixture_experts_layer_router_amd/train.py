@@ -13,8 +13,7 @@ import ctypes
 
 import torch
 
-from . import (BF16, F32, LcMoeError, Shape, _check, _nbytes, _ptr, _stream, ffn_backward, lc_moe_workspace_size, lib,
-               make_shape)
+from . import BF16, F32, LcMoeError, Shape, _check, ffn_backward, lib
 
 
 class Saved(ctypes.Structure):
@@ -67,41 +66,55 @@ def _lib():
 
 
 # ---- low-level: same names and argument order as the C-ABI ------------------------------
+# Addresses go as plain integers (the argument types are declared above): a call costs a few
+# microseconds, which counts for layers of few tokens.
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _nbytes(t):
+    return 0 if t is None else t.nbytes
+
+
+def _stream(stream):
+    """The stream's handle; None: the current stream of the current device."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
+
 
 def lc_moe_forward_saved(shape, workspace) -> Saved:
     out = Saved()
-    _check(_lib().lc_moe_forward_saved(ctypes.byref(shape), _ptr(workspace), _nbytes(workspace), ctypes.byref(out)),
+    _check(_lib().lc_moe_forward_saved(ctypes.byref(shape), _p(workspace), _nbytes(workspace), ctypes.byref(out)),
            "lc_moe_forward_saved")
     return out
 
 
 def lc_moe_balance_workspace_size(shape, num_seqs) -> int:
-    return int(_lib().lc_moe_balance_workspace_size(ctypes.byref(shape), num_seqs))
+    return _lib().lc_moe_balance_workspace_size(ctypes.byref(shape), num_seqs)
 
 
 def lc_moe_balance_loss(shape, coef, logits, topk_idx, seq_offsets, num_seqs, token_mask, loss, load, prob, dlogits,
                         workspace, stream=None):
-    _check(_lib().lc_moe_balance_loss(ctypes.byref(shape), ctypes.byref(coef), _ptr(logits), _ptr(topk_idx),
-                                     _ptr(seq_offsets), num_seqs, _ptr(token_mask), _ptr(loss), _ptr(load),
-                                     _ptr(prob), _ptr(dlogits), _ptr(workspace), _nbytes(workspace),
-                                     _stream(stream)), "lc_moe_balance_loss")
+    _check(_lib().lc_moe_balance_loss(ctypes.byref(shape), ctypes.byref(coef), _p(logits), _p(topk_idx),
+                                     _p(seq_offsets), num_seqs, _p(token_mask), _p(loss), _p(load), _p(prob),
+                                     _p(dlogits), _p(workspace), _nbytes(workspace), _stream(stream)),
+           "lc_moe_balance_loss")
 
 
 def lc_moe_gate_backward(shape, x, ffn_rows, num_rows, slot_row, dy, dgate, stream=None):
-    _check(_lib().lc_moe_gate_backward(ctypes.byref(shape), _ptr(x), _ptr(ffn_rows), num_rows, _ptr(slot_row),
-                                      _ptr(dy), _ptr(dgate), _stream(stream)), "lc_moe_gate_backward")
+    _check(_lib().lc_moe_gate_backward(ctypes.byref(shape), _p(x), _p(ffn_rows), num_rows, _p(slot_row), _p(dy),
+                                      _p(dgate), _stream(stream)), "lc_moe_gate_backward")
 
 
 def lc_moe_router_backward_workspace_size(shape) -> int:
-    return int(_lib().lc_moe_router_backward_workspace_size(ctypes.byref(shape)))
+    return _lib().lc_moe_router_backward_workspace_size(ctypes.byref(shape))
 
 
 def lc_moe_router_backward(shape, x, w_router, logits, topk_idx, dgate, dlogits_aux, dx_add, dx, dw_router, dlogits,
                            workspace, stream=None):
-    _check(_lib().lc_moe_router_backward(ctypes.byref(shape), _ptr(x), _ptr(w_router), _ptr(logits), _ptr(topk_idx),
-                                        _ptr(dgate), _ptr(dlogits_aux), _ptr(dx_add), _ptr(dx), _ptr(dw_router),
-                                        _ptr(dlogits), _ptr(workspace), _nbytes(workspace), _stream(stream)),
-           "lc_moe_router_backward")
+    _check(_lib().lc_moe_router_backward(ctypes.byref(shape), _p(x), _p(w_router), _p(logits), _p(topk_idx), _p(dgate),
+                                        _p(dlogits_aux), _p(dx_add), _p(dx), _p(dw_router), _p(dlogits),
+                                        _p(workspace), _nbytes(workspace), _stream(stream)), "lc_moe_router_backward")
 
 
 def lc_moe_adamw(tensors, count, hyper, stream=None):
@@ -110,43 +123,38 @@ def lc_moe_adamw(tensors, count, hyper, stream=None):
 
 # ---- checked wrappers -------------------------------------------------------------------
 
-def _need(t, name, shape, dtype, device, optional=False):
-    if t is None:
-        if optional:
-            return
-        raise TypeError(f"{name} is required")
-    if t.dtype != dtype:
+def _need(t, name, shape, dtype, device):
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _given(t, name):
+    if t is None:
+        raise TypeError(f"{name} is required")
 
 
 def _dtype_code(t, name):
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return F32
     raise TypeError(f"{name}: {t.dtype}, expected torch.bfloat16 or torch.float32")
 
 
-class _On:
-    """Makes a tensor's device current: a launch goes to the device its stream belongs to."""
-
-    def __init__(self, device):
-        self.guard = torch.cuda.device(device) if device.type == "cuda" and \
-            device.index != torch.cuda.current_device() else None
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _on(device, call, *args):
+    """call(*args) with the tensors' device current: a launch goes to the device its stream
+    belongs to."""
+    if device.type != "cuda" or device.index == torch._C._cuda_getDevice():
+        return call(*args)
+    with torch.cuda.device(device):
+        return call(*args)
 
 
 def _space(size, given, device, where):
@@ -164,7 +172,7 @@ def forward_saved(x, N, Z, K, I, workspace):
     it: dict(logits fp32 [T,E], ffn_rows [T*K,d], slot_row int32 [T,K], ffn_offsets int32
     [N+1], perm_token int32 [T*K]).  x and the sizes are those of the forward."""
     T, d = x.shape
-    shape = make_shape(T, d, N, Z, K, I, _dtype_code(x, "x"))
+    shape = Shape(T, d, N, Z, K, I, _dtype_code(x, "x"))
     s = lc_moe_forward_saved(shape, workspace)
     base, flat = workspace.data_ptr(), workspace.view(torch.uint8).reshape(-1)
 
@@ -189,17 +197,18 @@ def balance_loss(logits, topk_idx, N, balance_coef, z_coef=0.0, seq_offsets=None
     S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
     _need(logits, "logits", (T, E), torch.float32, dev)
     _need(topk_idx, "topk_idx", (T, K), torch.int32, dev)
-    _need(seq_offsets, "seq_offsets", (S + 1,), torch.int32, dev, optional=True)
-    _need(token_mask, "token_mask", (T,), torch.uint8, dev, optional=True)
-    shape = make_shape(T, 8, N, E - N, K, 8, BF16)
+    if seq_offsets is not None:
+        _need(seq_offsets, "seq_offsets", (S + 1,), torch.int32, dev)
+    if token_mask is not None:
+        _need(token_mask, "token_mask", (T,), torch.uint8, dev)
+    shape = Shape(T, 8, N, E - N, K, 8, BF16)
     ws = _space(lc_moe_balance_workspace_size(shape, S), workspace, dev, "lc_moe_balance_workspace_size")
     out = dict(loss=torch.empty(2, dtype=torch.float32, device=dev),
                load=torch.empty((S, E), dtype=torch.int32, device=dev),
                prob=torch.empty((S, E), dtype=torch.float32, device=dev),
                dlogits=torch.empty_like(logits) if need_grad else None)
-    with _On(dev):
-        lc_moe_balance_loss(shape, BalanceCoef(balance_coef, z_coef), logits, topk_idx, seq_offsets, S, token_mask,
-                            out["loss"], out["load"], out["prob"], out["dlogits"], ws)
+    _on(dev, lc_moe_balance_loss, shape, BalanceCoef(balance_coef, z_coef), logits, topk_idx, seq_offsets, S,
+        token_mask, out["loss"], out["load"], out["prob"], out["dlogits"], ws)
     return out
 
 
@@ -214,10 +223,9 @@ def gate_backward(x, ffn_rows, slot_row, dy):
     _need(slot_row, "slot_row", (T, K), torch.int32, dev)
     _need(ffn_rows, "ffn_rows", (ffn_rows.shape[0], d), x.dtype, dev)
     N = min(K, 2048)
-    shape = make_shape(T, d, N, K - N, K, 8, code)
     dgate = torch.empty((T, K), dtype=torch.float32, device=dev)
-    with _On(dev):
-        lc_moe_gate_backward(shape, x, ffn_rows, min(ffn_rows.shape[0], T * K), slot_row, dy, dgate)
+    _on(dev, lc_moe_gate_backward, Shape(T, d, N, K - N, K, 8, code), x, ffn_rows, min(ffn_rows.shape[0], T * K),
+        slot_row, dy, dgate)
     return dgate
 
 
@@ -232,13 +240,19 @@ def router_backward(x, w_router, logits, topk_idx, dgate, N, dlogits_aux=None, d
     K = topk_idx.shape[1] if topk_idx is not None else 1
     _need(x, "x", (T, d), x.dtype, dev)
     _need(w_router, "w_router", (E, d), torch.float32, dev)
-    _need(dgate, "dgate", (T, K), torch.float32, dev, optional=True)
-    _need(logits, "logits", (T, E), torch.float32, dev, optional=dgate is None)
-    _need(topk_idx, "topk_idx", (T, K), torch.int32, dev, optional=dgate is None)
-    _need(dlogits_aux, "dlogits_aux", (T, E), torch.float32, dev, optional=True)
-    _need(dx_add, "dx_add", (T, d), x.dtype, dev, optional=True)
-    _need(dx, "dx", (T, d), x.dtype, dev, optional=True)
-    shape = make_shape(T, d, N, E - N, K, 8, code)
+    if dgate is not None:
+        _given(logits, "logits")
+        _given(topk_idx, "topk_idx")
+        _need(dgate, "dgate", (T, K), torch.float32, dev)
+        _need(logits, "logits", (T, E), torch.float32, dev)
+        _need(topk_idx, "topk_idx", (T, K), torch.int32, dev)
+    if dlogits_aux is not None:
+        _need(dlogits_aux, "dlogits_aux", (T, E), torch.float32, dev)
+    if dx_add is not None:
+        _need(dx_add, "dx_add", (T, d), x.dtype, dev)
+    if dx is not None:
+        _need(dx, "dx", (T, d), x.dtype, dev)
+    shape = Shape(T, d, N, E - N, K, 8, code)
     ws = _space(lc_moe_router_backward_workspace_size(shape), workspace, dev, "lc_moe_router_backward_workspace_size")
     out = {}
     if need_dx:
@@ -247,9 +261,8 @@ def router_backward(x, w_router, logits, topk_idx, dgate, N, dlogits_aux=None, d
         out["dw_router"] = torch.empty_like(w_router)
     if need_dlogits:
         out["dlogits"] = torch.empty((T, E), dtype=torch.float32, device=dev)
-    with _On(dev):
-        lc_moe_router_backward(shape, x, w_router, logits, topk_idx, dgate, dlogits_aux, dx_add, out.get("dx"),
-                               out.get("dw_router"), out.get("dlogits"), ws)
+    _on(dev, lc_moe_router_backward, shape, x, w_router, logits, topk_idx, dgate, dlogits_aux, dx_add, out.get("dx"),
+        out.get("dw_router"), out.get("dlogits"), ws)
     return out
 
 
@@ -267,8 +280,7 @@ def layer_backward(x, w_router, w_gate, w_up, w_down, out, dy, workspace, balanc
     if balance_coef or z_coef:
         bal = balance_loss(saved["logits"], out["topk_idx"], N, balance_coef, z_coef, seq_offsets, token_mask)
     dgate = gate_backward(x, saved["ffn_rows"], saved["slot_row"], dy)
-    with _On(x.device):
-        grads = ffn_backward(x, w_gate, w_up, w_down, out["topk_idx"], out["topk_gate"], dy, E - N)
+    grads = _on(x.device, ffn_backward, x, w_gate, w_up, w_down, out["topk_idx"], out["topk_gate"], dy, E - N)
     r = router_backward(x, w_router, saved["logits"], out["topk_idx"], dgate, N, dlogits_aux=bal["dlogits"],
                         dx_add=grads["dx"], dx=grads["dx"])
     return dict(grads, dw_router=r["dw_router"], dgate=dgate, loss=bal["loss"], load=bal["load"], prob=bal["prob"])
@@ -346,5 +358,4 @@ class AdamW:
         hyper = AdamwHyper(lr, beta1, beta2, eps, self.state_bits, step,
                            None if step_dev is None else step_dev.data_ptr(),
                            None if grad_scale is None else grad_scale.data_ptr(), seed & 0xFFFFFFFF)
-        with _On(self.device):
-            lc_moe_adamw(self._tensors, len(self._tensors), hyper)
+        _on(self.device, lc_moe_adamw, self._tensors, len(self._tensors), hyper)
