@@ -112,10 +112,11 @@ lc_moe_status lc_moe_gate_backward(const lc_moe_shape* shape, const void* x, con
  *   dlogits_t,i = p_t,i (dp_t,i - sum_j p_t,j dp_t,j) + dlogits_aux_t,i,  p_t = softmax(logits_t)
  *   dx          = dlogits W_r + dx_add
  *   dw_router   = dlogits^T x
- * in fp32 precision: for the matrix cores dlogits, W_r and fp32 tokens are split into
- * bf16 parts whose products are exact and summed in fp32 (dx of a bf16 layer, which is
- * rounded to bf16, from parts that keep 16 bits of dlogits and W_r; everything else from
- * parts that keep 24).  dx is rounded once.
+ * with fp32 sums.  For the matrix cores dlogits, W_r and fp32 tokens are cut into parts of 8
+ * bits whose products are exact; dw_router, and dx of an fp32 layer, keep 24 bits of every
+ * operand.  dx of a bf16 layer, which is rounded to bf16, keeps 16 bits of dlogits and W_r, or
+ * 11 (fp16 with a power of two taken out of every row) in layers of many tokens.  dx is
+ * rounded once.
  * A pick outside 0..N+Z-1 has no gradient.  A token whose logits are all -infinity has
  * dlogits = dlogits_aux.
  *   x            [T][d] dtype

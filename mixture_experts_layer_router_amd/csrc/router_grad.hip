@@ -2,10 +2,20 @@
 // products with the router weight and with the tokens (formulas in
 // include/lc_moe_train.h).
 //
-//   dlogits_kernel   one wave per token: dlogits in fp32, cut into three bf16 parts
-//   parts_kernel     W_r (and fp32 tokens) cut into parts
-//   product_kernel   dx = dlogits W_r (+ dx_add) and dW = dlogits^T x on the matrix cores
-//   sum_parts_kernel the pieces of dW's reduction over the tokens, added in order
+//   weight_f16_kernel  big layers of bf16 tokens: W_r as fp16, scaled row by row
+//   operands_kernel    dlogits, one wave per token, cut into the products' operands; W_r and
+//                      fp32 tokens cut into parts
+//   products_kernel    dx = dlogits W_r (+ dx_add) and dW = dlogits^T x on the matrix cores, side
+//                      by side in one grid
+//   sum_parts_kernel   the pieces of dW's reduction over the tokens, added in order
+//
+// Precision.  dW is an fp32 output: dlogits is cut into three bf16 parts (24 bits), the tokens
+// are bf16 already (or cut the same way), every product of parts is exact and the matrix cores
+// add them in fp32.  dx of an fp32 layer is made the same way.  dx of a bf16 layer is rounded
+// to bf16, so its operands keep 16 bits (two bf16 parts each, three products), or 11 in the
+// form for many tokens: fp16 with a power of two taken out of every row, one product.  An
+// operand rounded to fp16 is off by at most 2^-11 of its value (2^-25 of its row's largest
+// below 2^-29 of that); the result's own rounding is 2^-8.
 #include <type_traits>
 
 #include "train.h"
@@ -14,6 +24,8 @@
 #include "logit_row.h"
 
 namespace lcm {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 // v = h + m + l exactly but for the last of its 24 significant bits (each part keeps 8, the
 // remainders are exact in fp32).
@@ -24,22 +36,100 @@ __device__ __forceinline__ void cut3(float v, bf16_t (&o)[3]) {
   o[2] = f2bf(r1 - bf2f(o[1]));
 }
 
-// ---------------------------------------------------------------------------------------
-// dlogits of one token per wave, the row in its registers as in logit_row.h.  The picks'
-// gradients are added in pick order by the lane that holds the expert.
-// ---------------------------------------------------------------------------------------
+__device__ __forceinline__ bf16_t f16_bits(float v) { return __builtin_bit_cast(bf16_t, static_cast<_Float16>(v)); }
+
+// Exponent of the largest magnitude, so that 2^(14 - it) brings it into [2^14, 2^15), well inside
+// fp16; 0 for a row of zeros.
+__device__ __forceinline__ int top_exp(float amax) { return amax > 0.f ? ilogbf(amax) : 0; }
+
+// W_r row by row as fp16: w16[e] = 2^(14 - x) w[e], wexp[e] = x.  One workgroup per row; rows
+// from E on are zeros.
+__global__ __launch_bounds__(256) void weight_f16_kernel(const float* __restrict__ w, bf16_t* __restrict__ w16,
+                                                         int32_t* __restrict__ wexp, int E, int d, int dp) {
+  __shared__ float wm[4];
+  const int e = blockIdx.x, tid = threadIdx.x;
+  const float* row = w + size_t(e) * d;
+  float amax = 0.f;
+  if (e < E) {
+    for (int c = tid * 4; c < d; c += 1024) {
+      const float4 q = *reinterpret_cast<const float4*>(row + c);
+      amax = fmaxf(fmaxf(amax, fmaxf(fabsf(q.x), fabsf(q.y))), fmaxf(fabsf(q.z), fabsf(q.w)));
+    }
+  }
+  amax = __ockl_wfred_max_f32(amax);
+  if ((tid & 63) == 0) wm[tid >> 6] = amax;
+  __syncthreads();
+  const int x = top_exp(fmaxf(fmaxf(wm[0], wm[1]), fmaxf(wm[2], wm[3])));
+  if (tid == 0) wexp[e] = x;
+  for (int c = tid * 4; c < dp; c += 1024) {
+    float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (e < E && c < d) q = *reinterpret_cast<const float4*>(row + c);
+    *reinterpret_cast<uint2*>(w16 + size_t(e) * dp + c) =
+        make_uint2(f16_bits(ldexpf(q.x, 14 - x)) | (uint32_t(f16_bits(ldexpf(q.y, 14 - x))) << 16),
+                   f16_bits(ldexpf(q.z, 14 - x)) | (uint32_t(f16_bits(ldexpf(q.w, 14 - x))) << 16));
+  }
+}
+
+struct OperandArgs {
+  const float* logits;
+  const int32_t* idx;
+  const float* dgate;
+  const float* aux;
+  float* out;        // dlogits in fp32, or NULL
+  bf16_t* parts;     // [3][T][Ep]
+  bf16_t* dl16;      // [T][Ep] fp16: 2^(wexp[e] + 14 - x) dlogits, x the row's exponent; or NULL
+  float* rscale;     // [T] 2^(x - 28)
+  const int32_t* wexp;
+  int T, E, K, Ep;
+  // matrices [R][C] fp32 to cut into np bf16 planes [Rp][Cp], zeros past R and C
+  struct Matrix {
+    const float* src;
+    bf16_t* dst;
+    int R, C, Cp, np;
+    size_t n4;       // Rp Cp / 4
+    unsigned blocks;
+  } mat[2];
+  unsigned dl_blocks;
+  uint4* zero;       // 16 zero bytes: the source of operand chunks past the data
+};
+
+__device__ __forceinline__ void cut_matrix(const OperandArgs::Matrix& m, unsigned block) {
+  const size_t i = size_t(block) * 256 + threadIdx.x;
+  if (i >= m.n4) return;
+  const size_t r = i / (m.Cp / 4);
+  const int c = int(i - r * (m.Cp / 4)) * 4;
+  const float4 v = r < size_t(m.R) && c < m.C ? *reinterpret_cast<const float4*>(m.src + r * m.C + c)
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+  bf16_t h[4][3];
+  cut3(v.x, h[0]);
+  cut3(v.y, h[1]);
+  cut3(v.z, h[2]);
+  cut3(v.w, h[3]);
+  for (int q = 0; q < m.np; ++q)
+    *reinterpret_cast<uint2*>(m.dst + q * m.n4 * 4 + i * 4) =
+        make_uint2(h[0][q] | (uint32_t(h[1][q]) << 16), h[2][q] | (uint32_t(h[3][q]) << 16));
+}
+
+// Workgroups 0 .. dl_blocks-1: dlogits of four tokens, one per wave, the row in its registers as
+// in logit_row.h; the picks' gradients are added in pick order by the lane that holds the
+// expert.  The others cut matrices, 4 columns a thread.
 template <int EPL, int V>
-__global__ __launch_bounds__(256) void dlogits_kernel(const float* __restrict__ logits,
-                                                      const int32_t* __restrict__ idx,
-                                                      const float* __restrict__ dgate, const float* aux, int T, int E,
-                                                      int K, int Ep, float* out, bf16_t* __restrict__ parts) {
+__global__ __launch_bounds__(256) void operands_kernel(OperandArgs a) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.zero = make_uint4(0, 0, 0, 0);
+  if (blockIdx.x >= a.dl_blocks) {
+    const unsigned b = blockIdx.x - a.dl_blocks;
+    if (b < a.mat[0].blocks) cut_matrix(a.mat[0], b);
+    else cut_matrix(a.mat[1], b - a.mat[0].blocks);
+    return;
+  }
   constexpr int J = EPL / V;  // runs of 64 V experts
   const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (t >= T) return;
+  const int E = a.E, K = a.K;
+  if (t >= a.T) return;
   float v[EPL], ax[EPL];
-  if (dgate) load_row<EPL, V>(logits + size_t(t) * E, E, lane, -INFINITY, v);
-  if (aux) load_row<EPL, V>(aux + size_t(t) * E, E, lane, 0.f, ax);
-  if (dgate) {
+  if (a.dgate) load_row<EPL, V>(a.logits + size_t(t) * E, E, lane, -INFINITY, v);
+  if (a.aux) load_row<EPL, V>(a.aux + size_t(t) * E, E, lane, 0.f, ax);
+  if (a.dgate) {
     const RowSum r = softmax_row<EPL>(v);
     const float rs = r.m > -INFINITY ? 1.f / r.sum : 0.f;
     float dp[EPL];
@@ -50,8 +140,8 @@ __global__ __launch_bounds__(256) void dlogits_kernel(const float* __restrict__ 
       int pe = -1;
       float pg = 0.f;
       if (lane < n) {
-        pe = idx[size_t(t) * K + k0 + lane];
-        pg = dgate[size_t(t) * K + k0 + lane];
+        pe = a.idx[size_t(t) * K + k0 + lane];
+        pg = a.dgate[size_t(t) * K + k0 + lane];
       }
       for (int k = 0; k < n; ++k) {
         const int e = __builtin_amdgcn_readlane(pe, k);
@@ -80,100 +170,102 @@ __global__ __launch_bounds__(256) void dlogits_kernel(const float* __restrict__ 
 #pragma unroll
     for (int i = 0; i < EPL; ++i) v[i] = 0.f;
   }
-  if (aux) {
+  if (a.aux) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) v[i] += ax[i];
   }
-  const size_t plane = size_t(T) * Ep;
+  if (a.out) store_row<EPL, V>(a.out + size_t(t) * E, E, lane, v);
+  auto put = [&](bf16_t* dst, int j, const bf16_t (&h)[V]) {
+    const int e = (j * 64 + lane) * V;
+    if (e >= a.Ep) return;
+    if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(dst + e) = make_uint2(h[0] | (uint32_t(h[1]) << 16), h[2] | (uint32_t(h[3]) << 16));
+    else
+      dst[e] = h[0];
+  };
+  const size_t plane = size_t(a.T) * a.Ep;
+  bf16_t* row = a.parts + size_t(t) * a.Ep;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int e = (j * 64 + lane) * V;
-    if (e >= Ep) continue;
-    bf16_t* dst = parts + size_t(t) * Ep + e;
-    if constexpr (V == 4) {
-      bf16_t h[4][3];
+    bf16_t h[3][V];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) cut3(e < E ? v[4 * j + w] : 0.f, h[w]);
-#pragma unroll
-      for (int q = 0; q < 3; ++q)
-        *reinterpret_cast<uint2*>(dst + q * plane) =
-            make_uint2(h[0][q] | (uint32_t(h[1][q]) << 16), h[2][q] | (uint32_t(h[3][q]) << 16));
-      if (out && e < E)
-        *reinterpret_cast<float4*>(out + size_t(t) * E + e) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    } else {
-      bf16_t h[3];
-      cut3(e < E ? v[j] : 0.f, h);
-#pragma unroll
-      for (int q = 0; q < 3; ++q) dst[q * plane] = h[q];
-      if (out && e < E) out[size_t(t) * E + e] = v[j];
+    for (int w = 0; w < V; ++w) {
+      bf16_t c[3];
+      cut3((j * 64 + lane) * V < E ? v[j * V + w] : 0.f, c);
+      h[0][w] = c[0], h[1][w] = c[1], h[2][w] = c[2];
     }
+#pragma unroll
+    for (int q = 0; q < 3; ++q) put(row + q * plane, j, h[q]);
+  }
+  if (a.dl16) {
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int w = 0; w < V; ++w) {
+        const int e = (j * 64 + lane) * V + w;
+        v[j * V + w] = e < E ? ldexpf(v[j * V + w], a.wexp[e]) : 0.f;
+        amax = fmaxf(amax, fabsf(v[j * V + w]));
+      }
+    int x = top_exp(__ockl_wfred_max_f32(amax));
+    x = x < -98 ? -98 : x;  // keeps 2^(28 - x), which dx_add is taken in units of, inside fp32
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      bf16_t h[V];
+#pragma unroll
+      for (int w = 0; w < V; ++w) h[w] = f16_bits(ldexpf(v[j * V + w], 14 - x));
+      put(a.dl16 + size_t(t) * a.Ep, j, h);
+    }
+    if (lane == 0) a.rscale[t] = ldexpf(1.f, x - 28);
   }
 }
 
-// Parts of a matrix [R][C] fp32 (C a multiple of 4): NP planes [Rp][Cp], zeros past R and C.
-// Thread: 4 columns.  Also the 16 zero bytes that operand chunks past the data are read from.
-template <int NP>
-__global__ __launch_bounds__(256) void parts_kernel(const float* __restrict__ src, bf16_t* __restrict__ dst, int R,
-                                                    int C, size_t n4, int Cp, uint4* __restrict__ zero) {
-  const size_t i = size_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i == 0) *zero = make_uint4(0, 0, 0, 0);
-  if (i >= n4) return;
-  const size_t r = i / (Cp / 4);
-  const int c = int(i - r * (Cp / 4)) * 4;
-  const float4 v = r < size_t(R) && c < C ? *reinterpret_cast<const float4*>(src + r * C + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-  bf16_t h[4][3];
-  cut3(v.x, h[0]);
-  cut3(v.y, h[1]);
-  cut3(v.z, h[2]);
-  cut3(v.w, h[3]);
-#pragma unroll
-  for (int q = 0; q < NP; ++q)
-    *reinterpret_cast<uint2*>(dst + q * n4 * 4 + i * 4) =
-        make_uint2(h[0][q] | (uint32_t(h[1][q]) << 16), h[2][q] | (uint32_t(h[3][q]) << 16));
-}
-
 // ---------------------------------------------------------------------------------------
-// C[M][N] = sum over pairs of parts (a, b) of A_a B_b, fp32 accumulation on
-// v_mfma_f32_32x32x16_bf16.  One stage holds 32 reduction steps of NA parts of A and NB
-// parts of B, so a loaded part serves every product it takes part in: with pairs
-// a + b < max(NA, NB) (h h, h m, m h of two parts each; h x, m x, l x of three and one; the
-// six largest of three and three) a stage's (NA + NB) operand tiles carry 3 or 6 products.
-//   DX: A(m, k) = dlogits parts, row m, K-contiguous; B(k, n) = W_r parts, row k.
-//   DW: A(m, k) = dlogits parts, row k (tokens), M-contiguous; B(k, n) = tokens, row k.
-// Tile BM x BN, 64 x (BN / 2) outputs per wave, BM / 32 waves, a two-stage ring in LDS
+// One tile of C[M][N] = sum over pairs of parts (a, b) of A_a B_b, fp32 accumulation on
+// v_mfma_f32_32x32x16.  A stage holds BK reduction steps of NA parts of A and NB parts of B, so
+// a loaded part serves every product it takes part in: with the pairs a + b < max(NA, NB)
+// (h h, h m, m h of two parts each; h x, m x, l x of three and one; the six largest of three
+// and three) the NA + NB operand tiles of a stage carry 1, 3 or 6 products.
+//   DX: A(m, k) = dlogits, row m, K-contiguous; B(k, n) = W_r, row k.
+//   DW: A(m, k) = dlogits, row k (a token), M-contiguous; B(k, n) = tokens, row k.
+// Tile BM x BN, 64 x (BN / 2) outputs per wave, BM / 32 waves, a ring of NST stages in LDS
 // filled by direct global->LDS loads.  Operands whose output index is contiguous lie in LDS
-// as in memory ([32 steps][columns]) and are read by the transposing LDS read; 16-byte chunk
-// c of row r sits in the 32-byte granule (c / 2) ^ 2 (r % 4), which spreads the four rows of
-// a read over the banks.  K-contiguous rows are 64 bytes, chunk c in slot c ^ swz4(r).
+// as in memory ([BK][columns]) and are read by the transposing LDS read; 16-byte chunk c of
+// row r sits in the 32-byte granule (c / 2) ^ 2 (r % 4), which spreads the four rows of a
+// read over the banks.  K-contiguous rows are 64 bytes, chunk c in slot c ^ swz4(r).
 // ---------------------------------------------------------------------------------------
 struct ProdArgs {
-  const bf16_t* a;  // [NA][T][Ep]
+  const bf16_t* a;  // [NA][T][Ep] (or its fp16 form)
   const bf16_t* b;  // DX: [NB][Ep][ldb]; DW: [NB][T][ldb]
   size_t plane_a, plane_b;
   const bf16_t* zero;
   const void* add;
   void* c;
+  const float* rscale;  // fp16: units of the rows' sums
   int M, N, Kdim, lda, ldb;
-  int chunk;        // reduction steps of a piece (a multiple of 32)
+  int chunk;            // reduction steps of a piece (a multiple of 32)
   int n_mt, n_nt, splits;
 };
 
-template <bool DX, int BM, int BN, int NA, int NB, typename Tc>
-__global__ __launch_bounds__(BM * 2, 1) void product_kernel(ProdArgs p) {
-  constexpr int BK = 32, WAVES = BM / 32, WN = 2, WC = BN / WN;  // wave tile: 64 x WC
-  constexpr int NBL = WC / 32;                                  // 32-wide column blocks of a wave
-  constexpr int A_OP = BM * BK * 2, B_OP = BN * BK * 2;          // bytes of one part in a stage
+template <bool DX, bool F16, int BM, int BN, int NA, int NB, int BK, int NST, typename Tc>
+__device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, unsigned char* smem) {
+  constexpr int WAVES = BM / 32, WN = 2, WC = BN / WN;  // wave tile: 64 x WC
+  constexpr int NBL = WC / 32;                          // 32-wide column blocks of a wave
+  constexpr int A_OP = BM * BK * 2, B_OP = BN * BK * 2;  // bytes of one part in a stage
   constexpr int STAGE = NA * A_OP + NB * B_OP;
   constexpr int NP = NA > NB ? NA : NB;
   constexpr int LA = A_OP / 1024 / WAVES, LB = B_OP / 1024 / WAVES;  // direct loads of a wave per part
+  constexpr int LOADS = NA * LA + NB * LB;                           // and per stage
   static_assert(A_OP % (1024 * WAVES) == 0 && B_OP % (1024 * WAVES) == 0, "whole loads");
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * STAGE];
+  static_assert(!DX || BK == 32, "K-contiguous rows are staged 64 bytes at a time");
+  static_assert(NBL == 2 || NBL == 4, "wave tiles of 64 or 128 columns");
 
-  // unit: groups of 4 M-tiles, in a group column tiles, in them its M-tiles; each XCD takes a
-  // contiguous eighth, so workgroups side by side share operand rows in its L2
-  const int U = p.n_mt * p.n_nt * p.splits, per = (U + 7) >> 3, slot_w = blockIdx.x >> 3;
+  // unit: pieces of the reduction, in them groups of 4 M-tiles, in a group column tiles, in them
+  // its M-tiles; each XCD takes a contiguous eighth, so workgroups side by side share operand
+  // rows in its L2
+  const int U = p.n_mt * p.n_nt * p.splits, per = (U + 7) >> 3, slot_w = block >> 3;
   if (slot_w >= per) return;
-  const int u = (blockIdx.x & 7) * per + slot_w;
+  const int u = (block & 7) * per + slot_w;
   if (u >= U) return;
   const int tiles = p.n_mt * p.n_nt, sp = u / tiles;
   int r0 = u - sp * tiles;
@@ -188,22 +280,22 @@ __global__ __launch_bounds__(BM * 2, 1) void product_kernel(ProdArgs p) {
   const int wm = wave >> 1, wn = wave & 1;
 
   // a wave's load i of an operand with contiguous columns (BC of them) fills bytes
-  // 1024 (wave + WAVES i) of its part: RPL rows of 2 BC bytes
+  // 1024 (wave + WAVES i) of its part: 512 / BC rows of 2 BC bytes
   auto col_load = [&](const bf16_t* src, size_t plane, int np, int op_bytes, int BC, int n_loads, int k0, int c0, int ld,
-                      int cols, unsigned char* dst) {
+                      unsigned char* dst) {
     const int rpl = 512 / BC, cpr = BC / 8;  // rows of a load, 16-byte chunks of a row
     for (int i = 0; i < n_loads; ++i) {
       const int kr = rpl * (wave + WAVES * i) + lane / cpr, sl = lane % cpr;
       const int ch = 2 * ((sl >> 1) ^ (2 * (kr & 3))) + (sl & 1);
       const int k = k0 + kr, c = c0 + ch * 8;
-      const bool in = k < kend && c < cols;
+      const bool in = k < kend && c < ld;
       const bf16_t* g = src + size_t(k) * ld + c;
       for (int q = 0; q < np; ++q)
         dma16(in ? g + q * plane : p.zero, dst + q * op_bytes + (wave + WAVES * i) * 1024);
     }
   };
   auto issue = [&](int kt) {
-    unsigned char* st = smem + (kt & 1) * STAGE;
+    unsigned char* st = smem + (kt % NST) * STAGE;
     const int k0 = kbeg + kt * BK;
     if constexpr (DX) {
 #pragma unroll
@@ -215,9 +307,9 @@ __global__ __launch_bounds__(BM * 2, 1) void product_kernel(ProdArgs p) {
         for (int q = 0; q < NA; ++q) dma16(g + q * p.plane_a, st + q * A_OP + (wave + WAVES * i) * 1024);
       }
     } else {
-      col_load(p.a, p.plane_a, NA, A_OP, BM, LA, k0, m0, p.lda, p.lda, st);
+      col_load(p.a, p.plane_a, NA, A_OP, BM, LA, k0, m0, p.lda, st);
     }
-    col_load(p.b, p.plane_b, NB, B_OP, BN, LB, k0, n0, p.ldb, p.ldb, st + NA * A_OP);
+    col_load(p.b, p.plane_b, NB, B_OP, BN, LB, k0, n0, p.ldb, st + NA * A_OP);
   };
 
   const int l32 = lane & 31, khalf = lane >> 5;
@@ -232,21 +324,70 @@ __global__ __launch_bounds__(BM * 2, 1) void product_kernel(ProdArgs p) {
   };
   typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
 
-  f32x16 acc[2][NBL];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < NBL; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  // Output row and column of accumulator quad (i, j, rq) after a transpose among four lanes (the
+  // 32x32 D layout: column lane % 32, rows 8 (r / 4) + 4 (lane / 32) + r % 4): one row, 4 columns.
+  const int q4 = lane & 3;
+  auto row_of = [&](int i, int rq) { return m0 + wm * 64 + i * 32 + 8 * rq + 4 * khalf + q4; };
+  auto col_of = [&](int j) { return n0 + wn * WC + j * 32 + (lane & 28); };
+  const Tc* add = static_cast<const Tc*>(p.add);
+  // A bf16 dx starts from dx_add (in the units of its row's sum), whose loads run beside the
+  // first stages'; an fp32 one adds it last, with one rounding.
+  constexpr bool START = DX && sizeof(Tc) == 2;
 
-  if (nk > 0) issue(0);
+  f32x16 acc[2][NBL];
+  const int npro = nk < NST ? nk : NST;
+  if (START && add) {
+    uint2 q[2][NBL][4];
+    float un[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int rq = 0; rq < 4; ++rq) {
+        const int m = row_of(i, rq);
+        un[i][rq] = F16 && m < p.M ? p.rscale[m] : 1.f;
+#pragma unroll
+        for (int j = 0; j < NBL; ++j) {
+          const int n = col_of(j);
+          q[i][j][rq] = m < p.M && n < p.N ? *reinterpret_cast<const uint2*>(add + size_t(m) * p.N + n) : make_uint2(0, 0);
+        }
+      }
+    for (int s = 0; s < npro; ++s) issue(s);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int rq = 0; rq < 4; ++rq) {
+        // 1 / 2^k by its exponent
+        const float inv = F16 ? __uint_as_float((254u << 23) - __float_as_uint(un[i][rq])) : 1.f;
+#pragma unroll
+        for (int j = 0; j < NBL; ++j) {
+          const uint2 b = q[i][j][rq];
+          const float v[4] = {__uint_as_float(b.x << 16) * inv, __uint_as_float(b.x & 0xFFFF0000u) * inv,
+                              __uint_as_float(b.y << 16) * inv, __uint_as_float(b.y & 0xFFFF0000u) * inv};
+          float w[4];
+          quad_transpose(v, q4, w);
+#pragma unroll
+          for (int t4 = 0; t4 < 4; ++t4) acc[i][j][rq * 4 + t4] = w[t4];
+        }
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < NBL; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    for (int s = 0; s < npro; ++s) issue(s);
+  }
+
   for (int kt = 0; kt < nk; ++kt) {
-    LCM_WAIT_VMCNT(0);  // stage kt landed (stage kt + 1 is not issued yet)
+    // stage kt landed: later stages up to kt + NST - 2 (at the start kt + NST - 1) are on their way
+    int last = kt == 0 ? NST - 1 : kt + NST - 2;
+    if (last > nk - 1) last = nk - 1;
+    wait_vmcnt((last - kt) * LOADS);
     wait_lds_reads();
-    block_barrier();    // every wave's loads of stage kt visible; stage kt - 1 read by all
-    if (kt + 1 < nk) issue(kt + 1);
-    const unsigned char* st = smem + (kt & 1) * STAGE;
+    block_barrier();  // every wave's loads of stage kt visible; stage kt - 1 read by all
+    if (kt > 0 && kt + NST - 1 < nk) issue(kt + NST - 1);  // into stage kt - 1's slot
+    const unsigned char* st = smem + (kt % NST) * STAGE;
     const unsigned char* sb = st + NA * A_OP;
 #pragma unroll
     for (int ks = 0; ks < BK; ks += 16) {
@@ -308,7 +449,6 @@ __global__ __launch_bounds__(BM * 2, 1) void product_kernel(ProdArgs p) {
           for (int j = 0; j < 4; ++j) ad[j] = tr_addr(sb + q * B_OP, BN * 2, wn * WC + 32 * j, ks);
           tr8(std::integral_constant<int, BN * 2>{}, ad, fb[q]);
         } else {
-          static_assert(NBL == 2, "wave tiles of 64 or 128 columns");
           tr4(std::integral_constant<int, BN * 2>{}, tr_addr(sb + q * B_OP, BN * 2, wn * WC, ks),
               tr_addr(sb + q * B_OP, BN * 2, wn * WC + 32, ks), fb[q][0], fb[q][1]);
         }
@@ -321,17 +461,23 @@ __global__ __launch_bounds__(BM * 2, 1) void product_kernel(ProdArgs p) {
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < NBL; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[qa][i], fb[qb][j], acc[i][j], 0, 0, 0);
+            for (int j = 0; j < NBL; ++j) {
+              if constexpr (F16)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, fa[qa][i]),
+                                                                  __builtin_bit_cast(f16x8, fb[qb][j]), acc[i][j], 0, 0, 0);
+              else
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[qa][i], fb[qb][j], acc[i][j], 0, 0, 0);
+            }
         }
     }
   }
 
-  // 32x32 D layout: column lane % 32, rows 8 (r / 4) + 4 (lane / 32) + r % 4; a transpose among
-  // four lanes gives each lane one row of 4 columns
-  const int q4 = lane & 3;
   Tc* out = static_cast<Tc*>(p.c) + (DX ? 0 : size_t(sp) * p.M * p.N);
-  const Tc* add = static_cast<const Tc*>(p.add);
+  float un[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int rq = 0; rq < 4; ++rq) un[i][rq] = F16 && row_of(i, rq) < p.M ? p.rscale[row_of(i, rq)] : 1.f;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -342,17 +488,13 @@ __global__ __launch_bounds__(BM * 2, 1) void product_kernel(ProdArgs p) {
 #pragma unroll
         for (int t4 = 0; t4 < 4; ++t4) v[t4] = acc[i][j][rq * 4 + t4];
         quad_transpose(v, q4, w);
-        const int m = m0 + wm * 64 + i * 32 + 8 * rq + 4 * khalf + q4;
-        const int n = n0 + wn * WC + j * 32 + (lane & 28);
+        const int m = row_of(i, rq), n = col_of(j);
         if (m >= p.M || n >= p.N) continue;
         const size_t o = size_t(m) * p.N + n;
         if constexpr (sizeof(Tc) == 2) {
-          if (add) {
-            const uint2 q = *reinterpret_cast<const uint2*>(add + o);
-            w[0] += __uint_as_float(q.x << 16);
-            w[1] += __uint_as_float(q.x & 0xFFFF0000u);
-            w[2] += __uint_as_float(q.y << 16);
-            w[3] += __uint_as_float(q.y & 0xFFFF0000u);
+          if constexpr (F16) {
+#pragma unroll
+            for (int t4 = 0; t4 < 4; ++t4) w[t4] *= un[i][rq];
           }
           *reinterpret_cast<uint2*>(out + o) =
               make_uint2(f2bf(w[0]) | (uint32_t(f2bf(w[1])) << 16), f2bf(w[2]) | (uint32_t(f2bf(w[3])) << 16));
@@ -364,6 +506,115 @@ __global__ __launch_bounds__(BM * 2, 1) void product_kernel(ProdArgs p) {
           *reinterpret_cast<float4*>(out + o) = make_float4(w[0], w[1], w[2], w[3]);
         }
       }
+}
+
+// dx of at most 64 tokens: 32 columns a workgroup, every fourth 16-step of the reduction a
+// wave, the four sums added through LDS in wave order.  W_r is read as it lies, once, and cut
+// into NP parts in registers: lane (l32, half) holds column n0 + l32 of rows 8 half + 0..7.
+template <int NP, typename Tx>
+__device__ __forceinline__ void dx_few(const ProdArgs& p, const float* __restrict__ w, int E, unsigned block, float* sums) {
+  const int n0 = block * 32;
+  if (n0 >= p.N) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l32 = lane & 31, half = lane >> 5;
+  const int n = n0 + l32 < p.N ? n0 + l32 : n0;
+  const bf16_t* arow[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int m = i * 32 + l32 < p.M ? i * 32 + l32 : 0;
+    arow[i] = p.a + size_t(m) * p.lda + 8 * half;
+  }
+  f32x16 acc[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
+  constexpr int B = 3;  // steps whose loads are in flight together
+  for (int k0 = wave * 16; k0 < p.Kdim; k0 += 64 * B) {
+    float wv[B][8];
+    bf16x8 fa[B][NP][2];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int k = k0 + 64 * b < p.Kdim ? k0 + 64 * b : k0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int e = k + 8 * half + q;
+        wv[b][q] = w[size_t(e < E ? e : E - 1) * p.N + n];  // dlogits' columns past E are zero
+      }
+#pragma unroll
+      for (int q = 0; q < NP; ++q)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) fa[b][q][i] = *reinterpret_cast<const bf16x8*>(arow[i] + q * p.plane_a + k);
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      if (k0 + 64 * b >= p.Kdim) break;
+      typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+      u16x8 h[NP];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        bf16_t c[3];
+        cut3(wv[b][q], c);
+#pragma unroll
+        for (int z = 0; z < NP; ++z) h[z][q] = c[z];
+      }
+#pragma unroll
+      for (int qa = 0; qa < NP; ++qa)
+#pragma unroll
+        for (int qb = 0; qb + qa < NP; ++qb)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[b][qa][i], __builtin_bit_cast(bf16x8, h[qb]), acc[i], 0, 0, 0);
+    }
+  }
+  float(*s)[64][33] = reinterpret_cast<float(*)[64][33]>(sums);  // [4][64 rows][32 columns + 1]
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[wave][i * 32 + 8 * (r >> 2) + 4 * half + (r & 3)][l32] = acc[i][r];
+  __syncthreads();
+  const Tx* add = static_cast<const Tx*>(p.add);
+  Tx* out = static_cast<Tx*>(p.c);
+  for (int i = tid; i < 64 * 32; i += 256) {
+    const int m = i >> 5, c = i & 31;
+    if (m >= p.M || n0 + c >= p.N) continue;
+    float v = (s[0][m][c] + s[1][m][c]) + (s[2][m][c] + s[3][m][c]);
+    const size_t o = size_t(m) * p.N + n0 + c;
+    if constexpr (sizeof(Tx) == 2) {
+      if (add) v += bf2f(add[o]);
+      out[o] = f2bf(v);
+    } else {
+      if (add) v += add[o];
+      out[o] = v;
+    }
+  }
+}
+
+// Both products in one grid: dW's workgroups first (their tiles are the longest), then dx's.
+struct ProductsArgs {
+  ProdArgs dw, dx;
+  unsigned dw_blocks;  // a multiple of 8
+  const float* w;      // the fp32 weight (few tokens)
+  int E;
+};
+
+template <int FORM, bool BF>
+__global__ __launch_bounds__(FORM == kRbBig ? 512 : 256, 1) void products_kernel(ProductsArgs a) {
+  typedef typename std::conditional<BF, bf16_t, float>::type Tx;
+  constexpr int X = BF ? 1 : 3, W = BF ? 2 : 3;  // parts of the tokens; of W_r (and dlogits for dx)
+  // ring: big 4 x 32 KB (fp32 layers 2 x 72 KB), else 2 x 32 KB (2 x 48 KB)
+  constexpr int LDS = FORM == kRbBig ? (BF ? 131072 : 147456) : BF ? 65536 : 98304;
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[LDS];
+  if (blockIdx.x < a.dw_blocks) {
+    if constexpr (FORM == kRbBig && BF) product_tile<false, false, 256, 256, 3, 1, 16, 4, float>(a.dw, blockIdx.x, smem);
+    else if constexpr (FORM == kRbBig) product_tile<false, false, 256, 128, 3, 3, 32, 2, float>(a.dw, blockIdx.x, smem);
+    else product_tile<false, false, 128, 128, 3, X, 32, 2, float>(a.dw, blockIdx.x, smem);
+  } else {
+    const unsigned b = blockIdx.x - a.dw_blocks;
+    if constexpr (FORM == kRbFew) dx_few<W, Tx>(a.dx, a.w, a.E, b, reinterpret_cast<float*>(smem));
+    else if constexpr (FORM == kRbSmall) product_tile<true, false, 128, 128, W, W, 32, 2, Tx>(a.dx, b, smem);
+    else if constexpr (BF) product_tile<true, true, 256, 256, 1, 1, 32, 4, Tx>(a.dx, b, smem);
+    else product_tile<true, false, 256, 128, 3, 3, 32, 2, Tx>(a.dx, b, smem);
+  }
 }
 
 // dW = its pieces, added in order (n values, a multiple of 4; 4 per thread).
@@ -384,63 +635,21 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict_
   *reinterpret_cast<float4*>(out + i) = a;
 }
 
-template <bool DX, int BM, int BN, int NA, int NB, typename Tc>
-static void product(ProdArgs p, hipStream_t st) {
-  p.n_mt = (p.M + BM - 1) / BM;
-  p.n_nt = (p.N + BN - 1) / BN;
-  const size_t units = size_t(p.n_mt) * p.n_nt * p.splits;
-  hipLaunchKernelGGL((product_kernel<DX, BM, BN, NA, NB, Tc>), dim3(unsigned((units + 7) / 8 * 8)), dim3(BM * 2), 0, st, p);
-}
-
-template <bool BF>
-static void products(const lc_moe_shape& s, const RouterBwPlan& pl, char* w, const void* x, const float* w_router,
-                     const void* add, void* dx, float* dw, hipStream_t st) {
-  typedef typename std::conditional<BF, bf16_t, float>::type Tx;
-  constexpr int BN = BF ? kRbBig : kRbSmall, W = BF ? 2 : 3, X = BF ? 1 : 3;
-  const int E = s.N + s.Z;
-  bf16_t* wp = reinterpret_cast<bf16_t*>(w + pl.wp);
-  bf16_t* xp = reinterpret_cast<bf16_t*>(w + pl.xp);
-  uint4* zero = reinterpret_cast<uint4*>(w + pl.zero);
-  const size_t nw = dx ? size_t(pl.Ep) * pl.dp / 4 : 0, nx = size_t(s.T) * pl.dp / 4;
-  hipLaunchKernelGGL((parts_kernel<W>), dim3(unsigned(nw / 256 + 1)), dim3(256), 0, st, w_router, wp, E, s.d, nw, pl.dp, zero);
-  ProdArgs p{};
-  p.a = reinterpret_cast<const bf16_t*>(w + pl.dl);
-  p.plane_a = size_t(s.T) * pl.Ep;
-  p.lda = pl.Ep;
-  p.ldb = pl.dp;
-  p.zero = reinterpret_cast<const bf16_t*>(zero);
-  p.N = s.d;
-  if (dx) {
-    p.b = wp;
-    p.plane_b = size_t(pl.Ep) * pl.dp;
-    p.M = s.T;
-    p.Kdim = p.chunk = pl.Ep;
-    p.splits = 1;
-    p.add = add;
-    p.c = dx;
-    if (pl.dx_big) product<true, kRbBig, BN, W, W, Tx>(p, st);
-    else product<true, kRbSmall, kRbSmall, W, W, Tx>(p, st);
+template <int FORM, bool BF>
+static void launch_products(ProductsArgs a, hipStream_t st) {
+  constexpr int BM = FORM == kRbBig ? 256 : 128, BN = FORM == kRbBig && BF ? 256 : 128;
+  size_t dx_blocks = 0;
+  if (a.dw.c) {
+    a.dw.n_mt = (a.dw.M + BM - 1) / BM;
+    a.dw.n_nt = (a.dw.N + BN - 1) / BN;
+    a.dw_blocks = unsigned((size_t(a.dw.n_mt) * a.dw.n_nt * a.dw.splits + 7) / 8 * 8);
   }
-  if (dw) {
-    if (!BF)
-      hipLaunchKernelGGL((parts_kernel<3>), dim3(unsigned((nx + 255) / 256)), dim3(256), 0, st,
-                         static_cast<const float*>(x), xp, s.T, s.d, nx, pl.dp, zero);
-    p.b = BF ? static_cast<const bf16_t*>(x) : xp;
-    p.plane_b = size_t(s.T) * pl.dp;
-    p.M = E;
-    p.Kdim = s.T;
-    p.chunk = pl.chunk;
-    p.splits = pl.splits;
-    p.add = nullptr;
-    p.c = pl.splits > 1 ? reinterpret_cast<float*>(w + pl.part) : dw;
-    if (pl.dw_big) product<false, kRbBig, BN, 3, X, float>(p, st);
-    else product<false, kRbSmall, kRbSmall, 3, X, float>(p, st);
-    if (pl.splits > 1) {
-      const size_t n = size_t(E) * s.d;
-      hipLaunchKernelGGL(sum_parts_kernel, dim3(unsigned((n / 4 + 255) / 256)), dim3(256), 0, st,
-                         reinterpret_cast<const float*>(w + pl.part), dw, pl.splits, n);
-    }
+  if (a.dx.c) {
+    a.dx.n_mt = (a.dx.M + BM - 1) / BM;
+    a.dx.n_nt = (a.dx.N + BN - 1) / BN;
+    dx_blocks = FORM == kRbFew ? size_t(a.dx.N + 31) / 32 : (size_t(a.dx.n_mt) * a.dx.n_nt + 7) / 8 * 8;
   }
+  hipLaunchKernelGGL((products_kernel<FORM, BF>), dim3(unsigned(a.dw_blocks + dx_blocks)), dim3(BM * 2), 0, st, a);
 }
 
 hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, void* ws, const void* x,
@@ -448,11 +657,44 @@ hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, 
                                   const float* dgate, const float* aux, const void* dx_add, void* dx, float* dw,
                                   float* dlogits, hipStream_t st) {
   const int E = s.N + s.Z, epl = (E + 63) / 64;
+  const bool bf = s.dtype == LC_MOE_BF16;
   char* w = static_cast<char*>(ws);
-  bf16_t* parts = reinterpret_cast<bf16_t*>(w + p.dl);
-#define LCM_DL(n, v)                                                                                                  \
-  hipLaunchKernelGGL((dlogits_kernel<n, v>), dim3((s.T + 3) / 4), dim3(256), 0, st, logits, idx, dgate, aux, s.T, E, \
-                     s.K, p.Ep, dlogits, parts)
+  bf16_t* wp = reinterpret_cast<bf16_t*>(w + p.wp);
+  bf16_t* xp = reinterpret_cast<bf16_t*>(w + p.xp);
+  OperandArgs o{};
+  o.logits = logits;
+  o.idx = idx;
+  o.dgate = dgate;
+  o.aux = aux;
+  o.out = dlogits;
+  o.parts = reinterpret_cast<bf16_t*>(w + p.dl);
+  o.zero = reinterpret_cast<uint4*>(w + p.zero);
+  o.T = s.T;
+  o.E = E;
+  o.K = s.K;
+  o.Ep = p.Ep;
+  o.dl_blocks = unsigned((s.T + 3) / 4);
+  if (dx && p.f16) {
+    o.dl16 = reinterpret_cast<bf16_t*>(w + p.dl16);
+    o.rscale = reinterpret_cast<float*>(w + p.rscale);
+    int32_t* wexp = reinterpret_cast<int32_t*>(w + p.wexp);
+    o.wexp = wexp;
+    hipLaunchKernelGGL(weight_f16_kernel, dim3(p.Ep), dim3(256), 0, st, w_router, wp, wexp, E, s.d, p.dp);
+  }
+  auto matrix = [&](int i, const float* src, bf16_t* dst, int R, int Rp, int np) {
+    o.mat[i].src = src;
+    o.mat[i].dst = dst;
+    o.mat[i].R = R;
+    o.mat[i].C = s.d;
+    o.mat[i].Cp = p.dp;
+    o.mat[i].np = np;
+    o.mat[i].n4 = size_t(Rp) * p.dp / 4;
+    o.mat[i].blocks = unsigned((o.mat[i].n4 + 255) / 256);
+  };
+  if (dx && !p.f16 && p.form != kRbFew) matrix(0, w_router, wp, E, p.Ep, bf ? 2 : 3);
+  if (dw && !bf) matrix(1, static_cast<const float*>(x), xp, s.T, s.T, 3);
+  const dim3 grid(o.dl_blocks + o.mat[0].blocks + o.mat[1].blocks);
+#define LCM_DL(n, v) hipLaunchKernelGGL((operands_kernel<n, v>), grid, dim3(256), 0, st, o)
   if (E % 4 == 0) {
     if (epl <= 4) LCM_DL(4, 4);
     else if (epl <= 8) LCM_DL(8, 4);
@@ -462,15 +704,49 @@ hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, 
     else LCM_DL(64, 4);
   } else {
     if (epl <= 2) LCM_DL(2, 1);
-    else if (epl <= 4) LCM_DL(4, 1);
     else if (epl <= 8) LCM_DL(8, 1);
     else if (epl <= 16) LCM_DL(16, 1);
     else if (epl <= 32) LCM_DL(32, 1);
     else LCM_DL(64, 1);
   }
 #undef LCM_DL
-  if (s.dtype == LC_MOE_BF16) products<true>(s, p, w, x, w_router, dx_add, dx, dw, st);
-  else products<false>(s, p, w, x, w_router, dx_add, dx, dw, st);
+  if (!dx && !dw) return hipGetLastError();
+  ProductsArgs a{};
+  a.w = w_router;
+  a.E = E;
+  ProdArgs q{};
+  q.lda = p.Ep;
+  q.ldb = p.dp;
+  q.zero = reinterpret_cast<const bf16_t*>(o.zero);
+  q.N = s.d;
+  a.dx = a.dw = q;
+  a.dx.a = p.f16 ? o.dl16 : o.parts;
+  a.dx.plane_a = size_t(s.T) * p.Ep;
+  a.dx.b = wp;
+  a.dx.plane_b = size_t(p.Ep) * p.dp;
+  a.dx.rscale = o.rscale;
+  a.dx.M = s.T;
+  a.dx.Kdim = a.dx.chunk = p.Ep;
+  a.dx.splits = 1;
+  a.dx.add = dx_add;
+  a.dx.c = dx;
+  a.dw.a = o.parts;
+  a.dw.plane_a = size_t(s.T) * p.Ep;
+  a.dw.b = bf ? static_cast<const bf16_t*>(x) : xp;
+  a.dw.plane_b = size_t(s.T) * p.dp;
+  a.dw.M = E;
+  a.dw.Kdim = s.T;
+  a.dw.chunk = p.chunk;
+  a.dw.splits = p.splits;
+  float* part = reinterpret_cast<float*>(w + p.part);
+  a.dw.c = !dw ? nullptr : p.splits > 1 ? part : dw;
+  if (p.form == kRbBig) bf ? launch_products<kRbBig, true>(a, st) : launch_products<kRbBig, false>(a, st);
+  else if (p.form == kRbSmall) bf ? launch_products<kRbSmall, true>(a, st) : launch_products<kRbSmall, false>(a, st);
+  else bf ? launch_products<kRbFew, true>(a, st) : launch_products<kRbFew, false>(a, st);
+  if (dw && p.splits > 1) {
+    const size_t n = size_t(E) * s.d;
+    hipLaunchKernelGGL(sum_parts_kernel, dim3(unsigned((n / 4 + 255) / 256)), dim3(256), 0, st, part, dw, p.splits, n);
+  }
   return hipGetLastError();
 }
 

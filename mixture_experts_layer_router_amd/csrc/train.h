@@ -55,35 +55,34 @@ hipError_t launch_gate_backward(const lc_moe_shape& s, const void* x, const void
                                 const int32_t* slot_row, const void* dy, float* dgate, hipStream_t st);
 
 // ---- router backward -----------------------------------------------------------------
-// The two products run on the bf16 matrix cores, their fp32 operands cut into bf16 parts
-// (each 8 of the value's 24 significant bits).  dlogits parts: [3][T][Ep]; W_r parts:
-// [Ep][dp]; fp32 tokens: parts [3][T][dp].  Ep and dp: E and d rounded up to whole operand
-// rows (32 experts; 16 bytes).
+// The two products run on the matrix cores, their fp32 operands cut into parts (router_grad.hip).
+//   few    at most 64 tokens: dx straight from the fp32 weight
+//   small  128 x 128 tiles, operands as bf16 parts
+//   big    256 x 256 tiles (fp32 layers 256 x 128); dx of a bf16 layer from scaled fp16
+// Ep and dp: E and d rounded up to whole operand rows (32 experts; 16 bytes).
+enum RbForm { kRbFew, kRbSmall, kRbBig };
 struct RouterBwPlan {
-  size_t dl, wp, xp, part, zero, total;
+  size_t dl, dl16, rscale, wp, wexp, xp, part, zero, total;
   int Ep, dp;
-  int w_parts;      // parts of W_r: 2 where dx is rounded to bf16, else 3
-  bool dx_big;      // dx on 256-row tiles (else 128 x 128)
-  bool dw_big;      // the same of dW
+  RbForm form;
+  bool f16;           // dx from fp16 operands
   int splits, chunk;  // dW: pieces of the reduction over the tokens, tokens of each (x 32)
 };
-// Rows x columns of a tile of the products.
-constexpr int kRbBig = 256, kRbSmall = 128;
 inline RouterBwPlan plan_router_backward(const lc_moe_shape& s) {
   RouterBwPlan p{};
   const size_t T = s.T, E = size_t(s.N) + s.Z;
   const bool bf = s.dtype == LC_MOE_BF16;
   p.Ep = int((E + 31) / 32 * 32);
   p.dp = (s.d + 7) / 8 * 8;
-  p.w_parts = bf ? 2 : 3;
   auto tiles = [](size_t m, size_t n, size_t bm, size_t bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
-  const size_t bn = bf ? kRbBig : kRbSmall;  // columns of a big tile
-  p.dx_big = tiles(T, s.d, kRbBig, bn) >= 256;
-  p.dw_big = E > kRbSmall;
-  // dW: enough pieces to fill 256 workgroups (512 of the small form), of at least 4 stages
-  const size_t t = p.dw_big ? tiles(E, s.d, kRbBig, bn) : tiles(E, s.d, kRbSmall, kRbSmall);
-  const size_t slots = p.dw_big ? 512 : 512;
-  size_t want = slots / t;
+  // big tiles where they fill the chip and dW's are not mostly empty
+  const size_t bn = bf ? 256 : 128;
+  const bool big = E > 128 && tiles(T, s.d, 256, bn) >= 256;
+  p.form = T <= 64 ? kRbFew : big ? kRbBig : kRbSmall;
+  p.f16 = bf && p.form == kRbBig;
+  // dW: pieces for two workgroups a CU (one after another with big tiles), of 128 tokens at least
+  const size_t t = p.form == kRbBig ? tiles(E, s.d, 256, bn) : tiles(E, s.d, 128, 128);
+  size_t want = 512 / t;
   const size_t most = (T + 127) / 128;
   want = want > most ? most : want < 1 ? 1 : want;
   p.chunk = int((T + want - 1) / want + 31) / 32 * 32;
@@ -91,7 +90,10 @@ inline RouterBwPlan plan_router_backward(const lc_moe_shape& s) {
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align256(o + bytes); return at; };
   p.dl = take(3 * T * p.Ep * 2);
-  p.wp = take(size_t(p.w_parts) * p.Ep * p.dp * 2);
+  p.dl16 = take(p.f16 ? T * p.Ep * 2 : 0);
+  p.rscale = take(p.f16 ? T * 4 : 0);
+  p.wp = take(p.form == kRbFew ? 0 : size_t(p.f16 ? 1 : bf ? 2 : 3) * p.Ep * p.dp * 2);
+  p.wexp = take(p.f16 ? size_t(p.Ep) * 4 : 0);
   p.xp = take(bf ? 0 : 3 * T * p.dp * 2);
   p.part = take(p.splits > 1 ? size_t(p.splits) * E * s.d * 4 : 0);
   p.zero = take(16);
