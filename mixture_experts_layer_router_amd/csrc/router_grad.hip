@@ -96,8 +96,9 @@ struct OperandArgs {
 __device__ __forceinline__ void cut_matrix(const OperandArgs::Matrix& m, unsigned block) {
   const size_t i = size_t(block) * 256 + threadIdx.x;
   if (i >= m.n4) return;
-  const size_t r = i / (m.Cp / 4);
-  const int c = int(i - r * (m.Cp / 4)) * 4;
+  const unsigned c4 = m.Cp / 4;
+  const size_t r = m.n4 >> 32 ? i / c4 : unsigned(i) / c4;
+  const int c = int(i - r * c4) * 4;
   const float4 v = r < size_t(m.R) && c < m.C ? *reinterpret_cast<const float4*>(m.src + r * m.C + c)
                                               : make_float4(0.f, 0.f, 0.f, 0.f);
   bf16_t h[4][3];
@@ -105,9 +106,12 @@ __device__ __forceinline__ void cut_matrix(const OperandArgs::Matrix& m, unsigne
   cut3(v.y, h[1]);
   cut3(v.z, h[2]);
   cut3(v.w, h[3]);
-  for (int q = 0; q < m.np; ++q)
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    if (q >= m.np) break;
     *reinterpret_cast<uint2*>(m.dst + q * m.n4 * 4 + i * 4) =
         make_uint2(h[0][q] | (uint32_t(h[1][q]) << 16), h[2][q] | (uint32_t(h[3][q]) << 16));
+  }
 }
 
 // Workgroups 0 .. dl_blocks-1: dlogits of four tokens, one per wave, the row in its registers as
@@ -208,7 +212,7 @@ __global__ __launch_bounds__(256) void operands_kernel(OperandArgs a) {
         amax = fmaxf(amax, fabsf(v[j * V + w]));
       }
     int x = top_exp(__ockl_wfred_max_f32(amax));
-    x = x < -98 ? -98 : x;  // keeps 2^(28 - x), which dx_add is taken in units of, inside fp32
+    x = x < -98 ? -98 : x;  // 2^(x - 28) is a normal fp32 number
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       bf16_t h[V];
@@ -324,60 +328,15 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
   };
   typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
 
-  // Output row and column of accumulator quad (i, j, rq) after a transpose among four lanes (the
-  // 32x32 D layout: column lane % 32, rows 8 (r / 4) + 4 (lane / 32) + r % 4): one row, 4 columns.
-  const int q4 = lane & 3;
-  auto row_of = [&](int i, int rq) { return m0 + wm * 64 + i * 32 + 8 * rq + 4 * khalf + q4; };
-  auto col_of = [&](int j) { return n0 + wn * WC + j * 32 + (lane & 28); };
-  const Tc* add = static_cast<const Tc*>(p.add);
-  // A bf16 dx starts from dx_add (in the units of its row's sum), whose loads run beside the
-  // first stages'; an fp32 one adds it last, with one rounding.
-  constexpr bool START = DX && sizeof(Tc) == 2;
-
   f32x16 acc[2][NBL];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < NBL; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   const int npro = nk < NST ? nk : NST;
-  if (START && add) {
-    uint2 q[2][NBL][4];
-    float un[2][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int rq = 0; rq < 4; ++rq) {
-        const int m = row_of(i, rq);
-        un[i][rq] = F16 && m < p.M ? p.rscale[m] : 1.f;
-#pragma unroll
-        for (int j = 0; j < NBL; ++j) {
-          const int n = col_of(j);
-          q[i][j][rq] = m < p.M && n < p.N ? *reinterpret_cast<const uint2*>(add + size_t(m) * p.N + n) : make_uint2(0, 0);
-        }
-      }
-    for (int s = 0; s < npro; ++s) issue(s);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int rq = 0; rq < 4; ++rq) {
-        // 1 / 2^k by its exponent
-        const float inv = F16 ? __uint_as_float((254u << 23) - __float_as_uint(un[i][rq])) : 1.f;
-#pragma unroll
-        for (int j = 0; j < NBL; ++j) {
-          const uint2 b = q[i][j][rq];
-          const float v[4] = {__uint_as_float(b.x << 16) * inv, __uint_as_float(b.x & 0xFFFF0000u) * inv,
-                              __uint_as_float(b.y << 16) * inv, __uint_as_float(b.y & 0xFFFF0000u) * inv};
-          float w[4];
-          quad_transpose(v, q4, w);
-#pragma unroll
-          for (int t4 = 0; t4 < 4; ++t4) acc[i][j][rq * 4 + t4] = w[t4];
-        }
-      }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < NBL; ++j)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-    for (int s = 0; s < npro; ++s) issue(s);
-  }
+  for (int s = 0; s < npro; ++s) issue(s);
 
   for (int kt = 0; kt < nk; ++kt) {
     // stage kt landed: later stages up to kt + NST - 2 (at the start kt + NST - 1) are on their way
@@ -472,40 +431,75 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
     }
   }
 
-  Tc* out = static_cast<Tc*>(p.c) + (DX ? 0 : size_t(sp) * p.M * p.N);
-  float un[2][4];
+  // 32x32 D layout: column lane % 32, rows 8 (r / 4) + 4 (lane / 32) + r % 4
+  const Tc* add = static_cast<const Tc*>(p.add);
+  if constexpr (sizeof(Tc) == 2) {
+    // bf16: 32 rows at a time through the wave's own piece of the ring, so that dx_add is read and
+    // dx written 16 bytes a lane in whole lines (8 bytes a lane from the accumulators as they
+    // lie took 120 us for dx_add and 60 us for dx at T = 16384, d = 6144)
+    constexpr int PITCH = WC + 4, LPR = WC / 8, RPI = 64 / LPR;  // lanes of a row, rows at a time
+    static_assert(WAVES * 32 * PITCH * 4 <= NST * STAGE, "fits the ring");
+    Tc* out = static_cast<Tc*>(p.c);
+    float* buf = reinterpret_cast<float*>(smem) + wave * 32 * PITCH;
+    const int rl = lane / LPR, cl = (lane % LPR) * 8, n = n0 + wn * WC + cl;
+    wait_lds_reads();
+    block_barrier();  // the ring is read by all
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i) {
+      uint4 q[32 / RPI];
+      float un[32 / RPI];
 #pragma unroll
-    for (int rq = 0; rq < 4; ++rq) un[i][rq] = F16 && row_of(i, rq) < p.M ? p.rscale[row_of(i, rq)] : 1.f;
+      for (int g = 0; g < 32 / RPI; ++g) {
+        const int m = m0 + wm * 64 + i * 32 + g * RPI + rl;
+        const bool in = m < p.M && n < p.N;
+        q[g] = add && in ? *reinterpret_cast<const uint4*>(add + size_t(m) * p.N + n) : make_uint4(0, 0, 0, 0);
+        un[g] = F16 && in ? p.rscale[m] : 1.f;
+      }
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < NBL; ++j)
 #pragma unroll
-    for (int j = 0; j < NBL; ++j)
+        for (int r = 0; r < 16; ++r) buf[(8 * (r >> 2) + 4 * khalf + (r & 3)) * PITCH + j * 32 + l32] = acc[i][j][r];
+      wait_lds_reads();  // (its writes: the same counter)
 #pragma unroll
-      for (int rq = 0; rq < 4; ++rq) {
-        float v[4], w[4];
+      for (int g = 0; g < 32 / RPI; ++g) {
+        const int m = m0 + wm * 64 + i * 32 + g * RPI + rl;
+        const float* v = buf + (g * RPI + rl) * PITCH + cl;
+        const float4 lo = *reinterpret_cast<const float4*>(v), hi = *reinterpret_cast<const float4*>(v + 4);
+        const float w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        const uint32_t u[4] = {q[g].x, q[g].y, q[g].z, q[g].w};
+        uint32_t o[4];
 #pragma unroll
-        for (int t4 = 0; t4 < 4; ++t4) v[t4] = acc[i][j][rq * 4 + t4];
-        quad_transpose(v, q4, w);
-        const int m = row_of(i, rq), n = col_of(j);
-        if (m >= p.M || n >= p.N) continue;
-        const size_t o = size_t(m) * p.N + n;
-        if constexpr (sizeof(Tc) == 2) {
-          if constexpr (F16) {
+        for (int c = 0; c < 4; ++c)
+          o[c] = f2bf(fmaf(w[2 * c], un[g], __uint_as_float(u[c] << 16))) |
+                 (uint32_t(f2bf(fmaf(w[2 * c + 1], un[g], __uint_as_float(u[c] & 0xFFFF0000u)))) << 16);
+        if (m < p.M && n < p.N) *reinterpret_cast<uint4*>(out + size_t(m) * p.N + n) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      wait_lds_reads();  // read before the next 32 rows are written
+    }
+  } else {
+    // fp32: a transpose among four lanes gives each lane one row of 4 columns, 16 bytes
+    const int q4 = lane & 3;
+    float* out = static_cast<float*>(p.c) + (DX ? 0 : size_t(sp) * p.M * p.N);
 #pragma unroll
-            for (int t4 = 0; t4 < 4; ++t4) w[t4] *= un[i][rq];
-          }
-          *reinterpret_cast<uint2*>(out + o) =
-              make_uint2(f2bf(w[0]) | (uint32_t(f2bf(w[1])) << 16), f2bf(w[2]) | (uint32_t(f2bf(w[3])) << 16));
-        } else {
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < NBL; ++j)
+#pragma unroll
+        for (int rq = 0; rq < 4; ++rq) {
+          float v[4], w[4];
+#pragma unroll
+          for (int t4 = 0; t4 < 4; ++t4) v[t4] = acc[i][j][rq * 4 + t4];
+          quad_transpose(v, q4, w);
+          const int m = m0 + wm * 64 + i * 32 + 8 * rq + 4 * khalf + q4, n = n0 + wn * WC + j * 32 + (lane & 28);
+          if (m >= p.M || n >= p.N) continue;
+          const size_t o = size_t(m) * p.N + n;
           if (add) {
             const float4 q = *reinterpret_cast<const float4*>(add + o);
             w[0] += q.x, w[1] += q.y, w[2] += q.z, w[3] += q.w;
           }
           *reinterpret_cast<float4*>(out + o) = make_float4(w[0], w[1], w[2], w[3]);
         }
-      }
+  }
 }
 
 // dx of at most 64 tokens: 32 columns a workgroup, every fourth 16-step of the reduction a
@@ -528,7 +522,7 @@ __device__ __forceinline__ void dx_few(const ProdArgs& p, const float* __restric
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
-  constexpr int B = 3;  // steps whose loads are in flight together
+  constexpr int B = NP == 2 ? 6 : 3;  // steps whose loads are in flight together
   for (int k0 = wave * 16; k0 < p.Kdim; k0 += 64 * B) {
     float wv[B][8];
     bf16x8 fa[B][NP][2];
@@ -598,22 +592,20 @@ struct ProductsArgs {
 };
 
 template <int FORM, bool BF>
-__global__ __launch_bounds__(FORM == kRbBig ? 512 : 256, 1) void products_kernel(ProductsArgs a) {
+__global__ __launch_bounds__(256, 2) void products_kernel(ProductsArgs a) {
   typedef typename std::conditional<BF, bf16_t, float>::type Tx;
   constexpr int X = BF ? 1 : 3, W = BF ? 2 : 3;  // parts of the tokens; of W_r (and dlogits for dx)
-  // ring: big 4 x 32 KB (fp32 layers 2 x 72 KB), else 2 x 32 KB (2 x 48 KB)
-  constexpr int LDS = FORM == kRbBig ? (BF ? 131072 : 147456) : BF ? 65536 : 98304;
+  // ring: big 2 x 40 KB for dW, 3 x 24 KB for dx; else 2 x 32 KB (fp32 layers 2 x 48 KB)
+  constexpr int LDS = FORM == kRbBig ? 81920 : BF ? 65536 : 98304;
   __shared__ __attribute__((aligned(1024))) unsigned char smem[LDS];
   if (blockIdx.x < a.dw_blocks) {
-    if constexpr (FORM == kRbBig && BF) product_tile<false, false, 256, 256, 3, 1, 16, 4, float>(a.dw, blockIdx.x, smem);
-    else if constexpr (FORM == kRbBig) product_tile<false, false, 256, 128, 3, 3, 32, 2, float>(a.dw, blockIdx.x, smem);
+    if constexpr (FORM == kRbBig) product_tile<false, false, 128, 256, 3, 1, 32, 2, float>(a.dw, blockIdx.x, smem);
     else product_tile<false, false, 128, 128, 3, X, 32, 2, float>(a.dw, blockIdx.x, smem);
   } else {
     const unsigned b = blockIdx.x - a.dw_blocks;
     if constexpr (FORM == kRbFew) dx_few<W, Tx>(a.dx, a.w, a.E, b, reinterpret_cast<float*>(smem));
     else if constexpr (FORM == kRbSmall) product_tile<true, false, 128, 128, W, W, 32, 2, Tx>(a.dx, b, smem);
-    else if constexpr (BF) product_tile<true, true, 256, 256, 1, 1, 32, 4, Tx>(a.dx, b, smem);
-    else product_tile<true, false, 256, 128, 3, 3, 32, 2, Tx>(a.dx, b, smem);
+    else product_tile<true, true, 128, 256, 1, 1, 32, 3, Tx>(a.dx, b, smem);
   }
 }
 
@@ -637,7 +629,7 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict_
 
 template <int FORM, bool BF>
 static void launch_products(ProductsArgs a, hipStream_t st) {
-  constexpr int BM = FORM == kRbBig ? 256 : 128, BN = FORM == kRbBig && BF ? 256 : 128;
+  constexpr int BM = 128, BN = FORM == kRbBig ? 256 : 128;
   size_t dx_blocks = 0;
   if (a.dw.c) {
     a.dw.n_mt = (a.dw.M + BM - 1) / BM;
@@ -657,7 +649,7 @@ hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, 
                                   const float* dgate, const float* aux, const void* dx_add, void* dx, float* dw,
                                   float* dlogits, hipStream_t st) {
   const int E = s.N + s.Z, epl = (E + 63) / 64;
-  const bool bf = s.dtype == LC_MOE_BF16;
+  const bool bf = s.dtype == LC_MOE_BF16, f16 = p.form == kRbBig;
   char* w = static_cast<char*>(ws);
   bf16_t* wp = reinterpret_cast<bf16_t*>(w + p.wp);
   bf16_t* xp = reinterpret_cast<bf16_t*>(w + p.xp);
@@ -674,7 +666,7 @@ hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, 
   o.K = s.K;
   o.Ep = p.Ep;
   o.dl_blocks = unsigned((s.T + 3) / 4);
-  if (dx && p.f16) {
+  if (dx && f16) {
     o.dl16 = reinterpret_cast<bf16_t*>(w + p.dl16);
     o.rscale = reinterpret_cast<float*>(w + p.rscale);
     int32_t* wexp = reinterpret_cast<int32_t*>(w + p.wexp);
@@ -691,7 +683,7 @@ hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, 
     o.mat[i].n4 = size_t(Rp) * p.dp / 4;
     o.mat[i].blocks = unsigned((o.mat[i].n4 + 255) / 256);
   };
-  if (dx && !p.f16 && p.form != kRbFew) matrix(0, w_router, wp, E, p.Ep, bf ? 2 : 3);
+  if (dx && !f16 && p.form != kRbFew) matrix(0, w_router, wp, E, p.Ep, bf ? 2 : 3);
   if (dw && !bf) matrix(1, static_cast<const float*>(x), xp, s.T, s.T, 3);
   const dim3 grid(o.dl_blocks + o.mat[0].blocks + o.mat[1].blocks);
 #define LCM_DL(n, v) hipLaunchKernelGGL((operands_kernel<n, v>), grid, dim3(256), 0, st, o)
@@ -720,7 +712,7 @@ hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, 
   q.zero = reinterpret_cast<const bf16_t*>(o.zero);
   q.N = s.d;
   a.dx = a.dw = q;
-  a.dx.a = p.f16 ? o.dl16 : o.parts;
+  a.dx.a = f16 ? o.dl16 : o.parts;
   a.dx.plane_a = size_t(s.T) * p.Ep;
   a.dx.b = wp;
   a.dx.plane_b = size_t(p.Ep) * p.dp;
@@ -740,7 +732,7 @@ hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, 
   a.dw.splits = p.splits;
   float* part = reinterpret_cast<float*>(w + p.part);
   a.dw.c = !dw ? nullptr : p.splits > 1 ? part : dw;
-  if (p.form == kRbBig) bf ? launch_products<kRbBig, true>(a, st) : launch_products<kRbBig, false>(a, st);
+  if (p.form == kRbBig) launch_products<kRbBig, true>(a, st);
   else if (p.form == kRbSmall) bf ? launch_products<kRbSmall, true>(a, st) : launch_products<kRbSmall, false>(a, st);
   else bf ? launch_products<kRbFew, true>(a, st) : launch_products<kRbFew, false>(a, st);
   if (dw && p.splits > 1) {

@@ -58,14 +58,13 @@ hipError_t launch_gate_backward(const lc_moe_shape& s, const void* x, const void
 // The two products run on the matrix cores, their fp32 operands cut into parts (router_grad.hip).
 //   few    at most 64 tokens: dx straight from the fp32 weight
 //   small  128 x 128 tiles, operands as bf16 parts
-//   big    256 x 256 tiles (fp32 layers 256 x 128); dx of a bf16 layer from scaled fp16
+//   big    bf16 layers: 128 x 256 tiles, dx from scaled fp16
 // Ep and dp: E and d rounded up to whole operand rows (32 experts; 16 bytes).
 enum RbForm { kRbFew, kRbSmall, kRbBig };
 struct RouterBwPlan {
   size_t dl, dl16, rscale, wp, wexp, xp, part, zero, total;
   int Ep, dp;
   RbForm form;
-  bool f16;           // dx from fp16 operands
   int splits, chunk;  // dW: pieces of the reduction over the tokens, tokens of each (x 32)
 };
 inline RouterBwPlan plan_router_backward(const lc_moe_shape& s) {
@@ -75,14 +74,13 @@ inline RouterBwPlan plan_router_backward(const lc_moe_shape& s) {
   p.Ep = int((E + 31) / 32 * 32);
   p.dp = (s.d + 7) / 8 * 8;
   auto tiles = [](size_t m, size_t n, size_t bm, size_t bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
-  // big tiles where they fill the chip and dW's are not mostly empty
-  const size_t bn = bf ? 256 : 128;
-  const bool big = E > 128 && tiles(T, s.d, 256, bn) >= 256;
+  // wide tiles where they fill the chip twice
+  const bool big = bf && E > 128 && tiles(T, s.d, 128, 256) >= 512;
   p.form = T <= 64 ? kRbFew : big ? kRbBig : kRbSmall;
-  p.f16 = bf && p.form == kRbBig;
-  // dW: pieces for two workgroups a CU (one after another with big tiles), of 128 tokens at least
-  const size_t t = p.form == kRbBig ? tiles(E, s.d, 256, bn) : tiles(E, s.d, 128, 128);
-  size_t want = 512 / t;
+  // dW: pieces of 128 tokens at least, for two workgroups a CU with wide tiles, for one else,
+  // where dx's tiles run beside them (T = 4096, d = 2048, E = 96: 35 us with two, 32 with one)
+  const size_t t = tiles(E, s.d, 128, p.form == kRbBig ? 256 : 128);
+  size_t want = (big ? 512 : 256) / t;
   const size_t most = (T + 127) / 128;
   want = want > most ? most : want < 1 ? 1 : want;
   p.chunk = int((T + want - 1) / want + 31) / 32 * 32;
@@ -90,10 +88,10 @@ inline RouterBwPlan plan_router_backward(const lc_moe_shape& s) {
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align256(o + bytes); return at; };
   p.dl = take(3 * T * p.Ep * 2);
-  p.dl16 = take(p.f16 ? T * p.Ep * 2 : 0);
-  p.rscale = take(p.f16 ? T * 4 : 0);
-  p.wp = take(p.form == kRbFew ? 0 : size_t(p.f16 ? 1 : bf ? 2 : 3) * p.Ep * p.dp * 2);
-  p.wexp = take(p.f16 ? size_t(p.Ep) * 4 : 0);
+  p.dl16 = take(big ? T * p.Ep * 2 : 0);
+  p.rscale = take(big ? T * 4 : 0);
+  p.wp = take(p.form == kRbFew ? 0 : size_t(big ? 1 : bf ? 2 : 3) * p.Ep * p.dp * 2);
+  p.wexp = take(big ? size_t(p.Ep) * 4 : 0);
   p.xp = take(bf ? 0 : 3 * T * p.dp * 2);
   p.part = take(p.splits > 1 ? size_t(p.splits) * E * s.d * 4 : 0);
   p.zero = take(16);
