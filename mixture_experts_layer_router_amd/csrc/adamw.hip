@@ -265,10 +265,7 @@ __global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args 
   for (int i = 1; i < a.count; ++i) ti = a.first[i] <= blockIdx.x ? i : ti;
   const Desc& t = a.t[ti];
   float gs = 1.f;
-  if (h.grad_scale) {
-    gs = *h.grad_scale;
-    if (!(fabsf(gs) < INFINITY)) return;
-  }
+  if (h.grad_scale) gs = *h.grad_scale;
   int step = h.step;
   double p1 = h.p1, p2 = h.p2;
   if (h.step_dev) {
@@ -313,6 +310,8 @@ __global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args 
         v[2 * c + 1] = mul(r1, r1);
       }
     }
+    // a step that is left out: the scale is asked for behind the loads, which it would hold up
+    if (!(fabsf(gs) < INFINITY)) return;
     float least = INFINITY;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {

@@ -4,8 +4,9 @@
 //
 // Three launches: softmax statistics of every token with each block's sums of probabilities
 // and counts (the logits are read once); the sums over a sequence's blocks; the losses and the
-// gradient (the logits are read again, from the memory-side cache where they fit).  A layer of
-// few logits does all of it in one workgroup and one launch.
+// gradient (the logits are read again, from the memory-side cache where they fit).  With few
+// blocks the last launch adds them itself, and few logits take one workgroup and one launch:
+// there a launch's 5 us count.
 #include "train.h"
 #include "logit_row.h"
 
@@ -72,10 +73,18 @@ __device__ __forceinline__ void write_losses(const BalArgs& a) {
   }
 }
 
-// Gradient of token t by one wave.  live, total: sequences with tokens that count, and those.
-template <int EPL, int V>
-__device__ __forceinline__ void token_grad(const BalArgs& a, int t, int lane, float (&p)[EPL], const TokStat& ts, int live,
-                                           long long total) {
+// The blocks of sequence s: b0 .. b1-1.
+__device__ __forceinline__ void seq_blocks(const BalArgs& a, int s, int& b0, int& b1) {
+  const int lo = seq_bound(a.off, s, a.T), up = seq_bound(a.off, s + 1, a.T);
+  b0 = lo / a.tok;
+  b1 = up > lo ? (up - 1) / a.tok + 1 : b0;
+}
+
+// Gradient of token t by one wave.  n: the tokens of its sequence that count; live, total:
+// sequences with such tokens, and all of those.  ADD: the counts are added from the blocks'.
+template <int EPL, int V, bool ADD>
+__device__ __forceinline__ void token_grad(const BalArgs& a, int t, int lane, float (&p)[EPL], const TokStat& ts, int n,
+                                           int live, long long total) {
   float* out = a.dlogits + size_t(t) * a.E;
   if (ts.seq < 0) {
 #pragma unroll
@@ -83,22 +92,26 @@ __device__ __forceinline__ void token_grad(const BalArgs& a, int t, int lane, fl
     store_row<EPL, V>(out, a.E, lane, p);
     return;
   }
-  const int n = a.seq_n[ts.seq];
   const long long kn = static_cast<long long>(a.K) * n;
   const float scale = a.balance / (static_cast<float>(live) * static_cast<float>(kn) * static_cast<float>(n));
   const float zl = a.z != 0.f ? 2.f * a.z / static_cast<float>(total) * ts.lse : 0.f;
   float u[EPL], dot = 0.f;
-  const int32_t* cnt = a.load + size_t(ts.seq) * a.E;
+  int b0 = 0, b1 = 1;
+  if (ADD) seq_blocks(a, ts.seq, b0, b1);
+  const int32_t* cnt = ADD ? a.part_c + (size_t(b0) + ts.seq) * a.E : a.load + size_t(ts.seq) * a.E;
 #pragma unroll
   for (int j = 0; j < EPL / V; ++j) {
     const int e = (j * 64 + lane) * V;
     int c[V] = {};
     if (e < a.E) {
-      if constexpr (V == 4) {
-        const int4 q = *reinterpret_cast<const int4*>(cnt + e);
-        c[0] = q.x, c[1] = q.y, c[2] = q.z, c[3] = q.w;
-      } else {
-        c[0] = cnt[e];
+#pragma unroll 8
+      for (int b = 0; b < b1 - b0; ++b) {
+        if constexpr (V == 4) {
+          const int4 q = *reinterpret_cast<const int4*>(cnt + size_t(b) * a.E + e);
+          c[0] += q.x, c[1] += q.y, c[2] += q.z, c[3] += q.w;
+        } else {
+          c[0] += cnt[size_t(b) * a.E + e];
+        }
       }
     }
 #pragma unroll
@@ -248,7 +261,7 @@ __global__ __launch_bounds__(WAVES * 64) void balance_tokens_kernel(BalArgs a) {
         const TokStat ts = a.stat[t];
         float v[EPL];
         if (ts.seq >= 0) load_row<EPL, V>(a.logits + size_t(t) * E, E, lane, -INFINITY, v);
-        token_grad<EPL, V>(a, t, lane, v, ts, live, total);
+        token_grad<EPL, V, false>(a, t, lane, v, ts, ts.seq >= 0 ? a.seq_n[ts.seq] : 0, live, total);
       }
     }
     write_losses<WAVES * 64>(a);
@@ -262,8 +275,8 @@ __global__ __launch_bounds__(1024) void balance_sums_kernel(BalArgs a) {
   __shared__ int sc[16][64], sn[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int s = blockIdx.y, e = blockIdx.x * 64 + lane, E = a.E;
-  const int lo = seq_bound(a.off, s, a.T), up = seq_bound(a.off, s + 1, a.T);
-  const int b0 = lo / a.tok, b1 = up > lo ? (up - 1) / a.tok + 1 : b0;
+  int b0, b1;
+  seq_blocks(a, s, b0, b1);
   const int ec = e < E ? e : E - 1;  // lanes past E repeat the last expert; never written
   float p = 0.f, z = 0.f;
   int c = 0, n = 0;
@@ -301,14 +314,62 @@ __global__ __launch_bounds__(1024) void balance_sums_kernel(BalArgs a) {
   }
 }
 
-// Workgroup 0: the losses.  The others: the gradient.
-template <int EPL, int V>
+// Few blocks and sequences: the sums over them in the last launch.
+constexpr int kFewBlocks = 32, kFewSeqs = 64;
+
+// Workgroup 0 of the last launch with few blocks: load, prob and the losses.
+__device__ __forceinline__ void few_sums(const BalArgs& a) {
+  __shared__ double sl[256], sz[256];
+  __shared__ int sn[256], sv[256];
+  const int i = threadIdx.x, E = a.E;
+  double l = 0., z = 0.;
+  int total = 0, live = 0;
+  for (int s = 0; s < a.S; ++s) {
+    int b0, b1, n = 0;
+    seq_blocks(a, s, b0, b1);
+    float zs = 0.f;
+#pragma unroll 8
+    for (int b = b0; b < b1; ++b) n += a.part_n[b + s], zs += a.part_z[b + s];
+    if (i == 0) {
+      z += zs;
+      total += n;
+      live += n > 0;
+    }
+    for (int e = i; e < E; e += 256) {
+      float p = 0.f;
+      int c = 0;
+#pragma unroll 8
+      for (int b = b0; b < b1; ++b) {
+        p += a.part_p[(size_t(b) + s) * E + e];
+        c += a.part_c[(size_t(b) + s) * E + e];
+      }
+      const float mean = n > 0 ? p / static_cast<float>(n) : 0.f;
+      a.load[size_t(s) * E + e] = c;
+      a.prob[size_t(s) * E + e] = mean;
+      if (n > 0) l += rel_load(E, a.K, c, n) * mean;
+    }
+  }
+  sl[i] = l, sz[i] = z, sn[i] = total, sv[i] = live;
+  __syncthreads();
+  for (int h = 128; h > 0; h >>= 1) {
+    if (i < h) sl[i] += sl[i + h], sz[i] += sz[i + h], sn[i] += sn[i + h], sv[i] += sv[i + h];
+    __syncthreads();
+  }
+  if (i == 0) {
+    a.loss[0] = sv[0] > 0 ? static_cast<float>(double(a.balance) / sv[0] * sl[0]) : 0.f;
+    a.loss[1] = sn[0] > 0 && a.z != 0.f ? static_cast<float>(double(a.z) / double(sn[0]) * sz[0]) : 0.f;
+  }
+}
+
+// Workgroup 0: the losses.  The others: the gradient.  FEW: see above.
+template <int EPL, int V, bool FEW>
 __global__ __launch_bounds__(256) void balance_grad_kernel(BalArgs a) {
   if (blockIdx.x == 0) {
-    write_losses<256>(a);
+    if constexpr (FEW) few_sums(a);
+    else write_losses<256>(a);
     return;
   }
-  __shared__ int wt[4], wl[4];
+  __shared__ int wt[4], wl[4], ns[FEW ? kFewSeqs : 1];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int t = (int(blockIdx.x) - 1) * a.grad_tok + wave;
   const int t1 = int(blockIdx.x) * a.grad_tok < a.T ? int(blockIdx.x) * a.grad_tok : a.T;
@@ -320,7 +381,16 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalArgs a) {
   }
   int total = 0, live = 0;  // tokens that count: at most T
   for (int s = tid; s < a.S; s += 256) {
-    const int n = a.seq_n[s];
+    int n = 0;
+    if constexpr (FEW) {
+      int b0, b1;
+      seq_blocks(a, s, b0, b1);
+#pragma unroll 8
+      for (int b = b0; b < b1; ++b) n += a.part_n[b + s];
+      ns[s] = n;
+    } else {
+      n = a.seq_n[s];
+    }
     total += n;
     live += n > 0;
   }
@@ -338,7 +408,8 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalArgs a) {
       nts = a.stat[t + 4];
       if (nts.seq >= 0) load_row<EPL, V>(a.logits + size_t(t + 4) * a.E, a.E, lane, -INFINITY, nxt);
     }
-    token_grad<EPL, V>(a, t, lane, v, ts, live, total);
+    const int n = ts.seq < 0 ? 0 : FEW ? ns[ts.seq] : a.seq_n[ts.seq];
+    token_grad<EPL, V, FEW>(a, t, lane, v, ts, n, live, total);
   }
 }
 
@@ -354,9 +425,13 @@ static void launch_passes(const BalArgs& a, const BalPlan& p, hipStream_t st) {
   }
   const int waves = p.tok < WAVES ? p.tok : WAVES;
   hipLaunchKernelGGL((balance_tokens_kernel<EPL, V, WAVES, false>), dim3(p.nblocks), dim3(waves * 64), 0, st, a);
+  const dim3 grid(1 + (a.dlogits ? (a.T + a.grad_tok - 1) / a.grad_tok : 0));
+  if (p.nblocks <= kFewBlocks && a.S <= kFewSeqs) {
+    hipLaunchKernelGGL((balance_grad_kernel<EPL, V, true>), grid, dim3(256), 0, st, a);
+    return;
+  }
   hipLaunchKernelGGL(balance_sums_kernel, dim3(p.n_eb, a.S), dim3(1024), 0, st, a);
-  const int grads = a.dlogits ? (a.T + a.grad_tok - 1) / a.grad_tok : 0;
-  hipLaunchKernelGGL((balance_grad_kernel<EPL, V>), dim3(1 + grads), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((balance_grad_kernel<EPL, V, false>), grid, dim3(256), 0, st, a);
 }
 
 hipError_t launch_balance_loss(const lc_moe_shape& s, const BalPlan& p, void* ws, float balance, float z,
