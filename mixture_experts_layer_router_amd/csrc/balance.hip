@@ -314,8 +314,8 @@ __global__ __launch_bounds__(1024) void balance_sums_kernel(BalArgs a) {
   }
 }
 
-// Few blocks and sequences: the sums over them in the last launch.
-constexpr int kFewBlocks = 32, kFewSeqs = 64;
+// Few blocks and sequences (they are taken one after another): the sums in the last launch.
+constexpr int kFewBlocks = 32, kFewSeqs = 2;
 
 // Workgroup 0 of the last launch with few blocks: load, prob and the losses.
 __device__ __forceinline__ void few_sums(const BalArgs& a) {

@@ -584,6 +584,8 @@ __device__ __forceinline__ void dx_few(const ProdArgs& p, const float* __restric
 }
 
 // Both products in one grid: dW's workgroups first (their tiles are the longest), then dx's.
+// (Mixed one to three, so that both kinds share a CU, they take 1.6 ms instead of 0.64 at
+// T = 16384, d = 6144, E = 768: their operands push each other out of the L2.)
 struct ProductsArgs {
   ProdArgs dw, dx;
   unsigned dw_blocks;  // a multiple of 8

@@ -27,7 +27,7 @@ inline BalPlan plan_balance(const lc_moe_shape& s, int S) {
   // one block per CU until a block has 32 tokens (at least 4, a power of two)
   p.tok = 4;
   while (p.tok < 32 && size_t(p.tok) * 256 < T) p.tok *= 2;
-  p.one = T <= 64 && T * E <= 16384;
+  p.one = T <= 64 && T * E <= 16384 && S <= 2;
   if (p.one) p.tok = 64;
   p.nblocks = int((T + p.tok - 1) / p.tok);
   p.nparts = p.nblocks + S;

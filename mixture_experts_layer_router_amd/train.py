@@ -203,9 +203,7 @@ def balance_loss(logits, topk_idx, N, balance_coef, z_coef=0.0, seq_offsets=None
         _need(token_mask, "token_mask", (T,), torch.uint8, dev)
     shape = Shape(T, 8, N, E - N, K, 8, BF16)
     ws = _space(lc_moe_balance_workspace_size(shape, S), workspace, dev, "lc_moe_balance_workspace_size")
-    out = dict(loss=torch.empty(2, dtype=torch.float32, device=dev),
-               load=torch.empty((S, E), dtype=torch.int32, device=dev),
-               prob=torch.empty((S, E), dtype=torch.float32, device=dev),
+    out = dict(loss=logits.new_empty(2), load=topk_idx.new_empty((S, E)), prob=logits.new_empty((S, E)),
                dlogits=torch.empty_like(logits) if need_grad else None)
     _on(dev, lc_moe_balance_loss, shape, BalanceCoef(balance_coef, z_coef), logits, topk_idx, seq_offsets, S,
         token_mask, out["loss"], out["load"], out["prob"], out["dlogits"], ws)
