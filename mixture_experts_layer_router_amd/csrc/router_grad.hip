@@ -264,7 +264,7 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
   static_assert(!DX || BK == 32, "K-contiguous rows are staged 64 bytes at a time");
   static_assert(NBL == 2 || NBL == 4, "wave tiles of 64 or 128 columns");
 
-  // unit: pieces of the reduction, in them groups of 4 M-tiles, in a group column tiles, in them
+  // unit: pieces of the reduction, in them groups of 8 M-tiles, in a group column tiles, in them
   // its M-tiles; each XCD takes a contiguous eighth, so workgroups side by side share operand
   // rows in its L2
   const int U = p.n_mt * p.n_nt * p.splits, per = (U + 7) >> 3, slot_w = block >> 3;
@@ -273,10 +273,10 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
   if (u >= U) return;
   const int tiles = p.n_mt * p.n_nt, sp = u / tiles;
   int r0 = u - sp * tiles;
-  const int grp = r0 / (4 * p.n_nt);
-  r0 -= grp * 4 * p.n_nt;
-  const int gm = p.n_mt - grp * 4 < 4 ? p.n_mt - grp * 4 : 4;
-  const int m0 = (grp * 4 + r0 % gm) * BM, n0 = (r0 / gm) * BN;
+  const int grp = r0 / (8 * p.n_nt);
+  r0 -= grp * 8 * p.n_nt;
+  const int gm = p.n_mt - grp * 8 < 8 ? p.n_mt - grp * 8 : 8;
+  const int m0 = (grp * 8 + r0 % gm) * BM, n0 = (r0 / gm) * BN;
   const int kbeg = sp * p.chunk, kend = kbeg + p.chunk < p.Kdim ? kbeg + p.chunk : p.Kdim;
   const int nk = (kend - kbeg + BK - 1) / BK;
   const int tid = threadIdx.x, lane = tid & 63;

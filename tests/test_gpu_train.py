@@ -260,7 +260,7 @@ def check_router(r, x, w, lg, idx, dg, aux, add):
     half = x.dtype == torch.bfloat16
     mag = np.abs(ref["dlogits"]) @ np.abs(ws)
     # at most three partial products an expert, added in one chain
-    f16 = half and E > 128 and -(-T // 128) * -(-d // 256) >= 512
+    f16 = half and T > 64 and -(-T // 128) * -(-d // 256) >= 384
     part = 2.0 ** -10 * (1 + 2.0 ** -11) if f16 else 2.0 ** -16 if half else 4 * U
     tol = err @ np.abs(ws) + ((3 * E + 8) * U + part) * mag
     if f16:  # what falls below fp16's normal numbers in a row of W_r or of 2^wexp dlogits
