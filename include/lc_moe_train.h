@@ -42,7 +42,8 @@ typedef struct {
  * The arrays hold the values of the last lc_moe_forward / lc_moe_forward_staged on this
  * workspace with this shape, until another call uses the workspace: a program that trains
  * gives each layer a workspace of its own from forward to backward.  After a call of
- * lc_moe_route only `logits` is valid. */
+ * lc_moe_route only `logits` is valid.  (lc_moe_forward_noalloc keeps its intermediates in
+ * the library's own array, which has no such view.) */
 lc_moe_status lc_moe_forward_saved(const lc_moe_shape* shape, const void* workspace,
                                    size_t workspace_bytes, lc_moe_saved* saved);
 
@@ -75,7 +76,8 @@ typedef struct {
  *   topk_idx     [T][K] int32
  *   seq_offsets  [num_seqs+1] int32, ascending, 0 <= seq_offsets[0], last <= T; or NULL with
  *                num_seqs = 1: one sequence of all T tokens.  Sequences may be empty.
- *                Offsets outside 0..T are taken as the nearest of the two.
+ *                Offsets outside 0..T are taken as the nearest of the two; offsets that
+ *                descend give unspecified numbers, but nothing out of range is touched.
  *   token_mask   [T] uint8, or NULL: every token
  *   loss         [2] fp32 (out)
  *   load         [num_seqs][N+Z] int32 (out); prob [num_seqs][N+Z] fp32 (out)
@@ -128,7 +130,8 @@ lc_moe_status lc_moe_gate_backward(const lc_moe_shape* shape, const void* x, con
  *   dx           [T][d] dtype (out), or NULL: not computed
  *   dw_router    [N+Z][d] fp32 (out), or NULL: not computed
  *   dlogits      [T][N+Z] fp32 (out), or NULL; may be dlogits_aux itself
- * Reads T, d, N, Z, K and dtype of shape.  Outputs and inputs may overlap only as said. */
+ * Reads T, d, N, Z, K and dtype of shape (LC_MOE_E_SHAPE also for fp32 layers of about 1.7e10
+ * token elements and more).  Outputs and inputs may overlap only as said. */
 size_t lc_moe_router_backward_workspace_size(const lc_moe_shape* shape);
 lc_moe_status lc_moe_router_backward(const lc_moe_shape* shape, const void* x,
                                      const float* w_router, const float* logits,

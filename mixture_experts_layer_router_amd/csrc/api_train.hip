@@ -77,7 +77,8 @@ lc_moe_status lc_moe_gate_backward(const lc_moe_shape* shape, const void* x, con
 
 size_t lc_moe_router_backward_workspace_size(const lc_moe_shape* shape) {
   if (check_shape(shape) != LC_MOE_OK) return 0;
-  return plan_router_backward(*shape).total;
+  const RouterBwPlan p = plan_router_backward(*shape);
+  return router_grid_fits(*shape, p) ? p.total : 0;
 }
 
 lc_moe_status lc_moe_router_backward(const lc_moe_shape* shape, const void* x, const float* w_router,
@@ -85,6 +86,8 @@ lc_moe_status lc_moe_router_backward(const lc_moe_shape* shape, const void* x, c
                                      const float* dlogits_aux, const void* dx_add, void* dx, float* dw_router,
                                      float* dlogits, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   LCM_CHECK(check_shape(shape));
+  const RouterBwPlan p = plan_router_backward(*shape);
+  if (!router_grid_fits(*shape, p)) return LC_MOE_E_SHAPE;
   LCM_CHECK(check_ptr(x, !dw_router));
   LCM_CHECK(check_ptr(w_router, !dx));
   LCM_CHECK(check_ptr(dgate, true));
@@ -95,7 +98,6 @@ lc_moe_status lc_moe_router_backward(const lc_moe_shape* shape, const void* x, c
   LCM_CHECK(check_ptr(dx, true));
   LCM_CHECK(check_ptr(dw_router, true));
   LCM_CHECK(check_ptr(dlogits, true));
-  const RouterBwPlan p = plan_router_backward(*shape);
   LCM_CHECK(check_space(workspace, workspace_bytes, p.total));
   LCM_LAUNCH(launch_router_backward(*shape, p, workspace, x, w_router, logits, topk_idx, dgate, dlogits_aux, dx_add,
                                     dx, dw_router, dlogits, stream));

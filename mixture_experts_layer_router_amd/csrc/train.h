@@ -100,6 +100,13 @@ inline RouterBwPlan plan_router_backward(const lc_moe_shape& s) {
   p.total = o;
   return p;
 }
+// operands_kernel's grid (four tokens a workgroup, then 1024 elements of W_r and of fp32
+// tokens a workgroup) within 2^32 - 1 work-items.
+inline bool router_grid_fits(const lc_moe_shape& s, const RouterBwPlan& p) {
+  const unsigned long long T = s.T, w = (size_t(p.Ep) * p.dp / 4 + 255) / 256,
+                           x = s.dtype == LC_MOE_BF16 ? 0 : (T * p.dp / 4 + 255) / 256;
+  return ((T + 3) / 4 + w + x) * 256 <= 0xFFFFFFFFull;
+}
 hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, void* ws, const void* x,
                                   const float* w_router, const float* logits, const int32_t* idx,
                                   const float* dgate, const float* aux, const void* dx_add, void* dx, float* dw,

@@ -157,7 +157,13 @@ def _on(device, call, *args):
         return call(*args)
 
 
+def _on_gpu(device):
+    if device.type != "cuda":
+        raise ValueError(f"the tensors are on {device}; the operators run on the GPU")
+
+
 def _space(size, given, device, where):
+    _on_gpu(device)
     if size == 0:
         raise LcMoeError(2, where)
     if given is None:
@@ -220,6 +226,7 @@ def gate_backward(x, ffn_rows, slot_row, dy):
     _need(dy, "dy", (T, d), x.dtype, dev)
     _need(slot_row, "slot_row", (T, K), torch.int32, dev)
     _need(ffn_rows, "ffn_rows", (ffn_rows.shape[0], d), x.dtype, dev)
+    _on_gpu(dev)
     N = min(K, 2048)
     dgate = torch.empty((T, K), dtype=torch.float32, device=dev)
     _on(dev, lc_moe_gate_backward, Shape(T, d, N, K - N, K, 8, code), x, ffn_rows, min(ffn_rows.shape[0], T * K),
@@ -323,6 +330,10 @@ class AdamW:
         lists = (grads, m, v, m_scales, v_scales, masters, wd, ls)
         if any(a is None or len(a) != n for a in lists):
             raise ValueError(f"AdamW: every list needs {n} entries")
+        for name, ts in (("params", params), ("m", m), ("v", v)):
+            at = [t.data_ptr() for t in ts if t.numel()]
+            if len(set(at)) < len(at):
+                raise ValueError(f"AdamW: a tensor is twice in {name}")
         self.params, self.grads, self.m, self.v = list(params), list(grads), list(m), list(v)
         self.m_scales, self.v_scales, self.masters = list(m_scales), list(v_scales), list(masters)
         self.state_bits, self.device = state_bits, params[0].device
@@ -346,6 +357,7 @@ class AdamW:
                                            p(self.m_scales[i]), p(self.v_scales[i]), size,
                                            _dtype_code(t, f"params[{i}]"),
                                            _dtype_code(self.grads[i], f"grads[{i}]"), wd[i], ls[i])
+        _on_gpu(self.device)
 
     def step(self, lr, beta1=0.9, beta2=0.95, eps=1e-8, step=1, seed=0, grad_scale=None, step_dev=None):
         """One step on the current stream.  step: its number, from 1 on, or step_dev: an int32

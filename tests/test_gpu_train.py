@@ -161,6 +161,32 @@ def test_balance_offsets_out_of_range_are_clamped():
                   0.1, 0.01, 50)
 
 
+@pytest.mark.parametrize("T,E", [(50, 20), (300, 70), (90, 600)])
+def test_balance_descending_offsets_stay_in_range(T, E):
+    """Unspecified numbers, but every output is written in place: the rows around them keep
+    their values, and the next call is right."""
+    import torch
+    from mixture_experts_layer_router_amd import train as lt
+    import mixture_experts_layer_router_amd as lm
+    lg, idx, _, _ = balance_inputs(dict(T=T, E=E, K=3))
+    dev, S = device(), 4
+    shape = lm.make_shape(T, 8, E, 0, 3, 8, lm.BF16)
+    ws = torch.zeros(lt.lc_moe_balance_workspace_size(shape, S), dtype=torch.uint8, device=dev)
+    for off in ([T // 2, 0, T, 3, T // 3], [T, T // 2, 5, 1, 0], [0, T, 0, T, 0]):
+        dl = torch.full((T + 8, E), 7.0, device=dev)
+        load = torch.full((S + 8, E), 7, dtype=torch.int32, device=dev)
+        prob = torch.full((S + 8, E), 7.0, device=dev)
+        loss = torch.full((4,), 7.0, device=dev)
+        lt.lc_moe_balance_loss(shape, lt.BalanceCoef(0.1, 0.1), put(lg), put(idx), put(np.array(off, np.int32)), S, None, loss,
+                               load, prob, dl, ws)
+        torch.cuda.synchronize()
+        assert bool((dl[T:] == 7).all()) and bool((load[S:] == 7).all()) and bool((prob[S:] == 7).all())
+        assert bool((loss[2:] == 7).all()) and not bool((dl[:T] == 7).any())
+    good = np.array([0, 5, T // 2, T // 2, T], np.int32)
+    r = run_balance(lg, idx, good, None, 0.1, 0.1)
+    check_balance(r, reference(lg, idx, good, None, float(np.float32(0.1)), float(np.float32(0.1))), 0.1, 0.1, T)
+
+
 def test_balance_without_gradient():
     import torch
     lg, idx, off, mask = balance_inputs(BAL[4])
