@@ -335,14 +335,32 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
     for (int j = 0; j < NBL; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  // bf16: dx_add of the wave's first 32 rows, loaded beside the stages (see the end)
+  constexpr bool HALF = sizeof(Tc) == 2;
+  constexpr int LPR = WC / 8, RPI = 64 / LPR, NG = HALF ? 32 / RPI : 1;  // lanes of a row, rows at a time
+  const Tc* add = static_cast<const Tc*>(p.add);
+  const int rl = lane / LPR, cl = (lane % LPR) * 8;
+  uint4 q0[NG];
+  auto load_add = [&](int i, uint4 (&q)[NG]) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int m = m0 + wm * 64 + i * 32 + g * RPI + rl, n = n0 + wn * WC + cl;
+      q[g] = add && m < p.M && n < p.N ? *reinterpret_cast<const uint4*>(add + size_t(m) * p.N + n) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if constexpr (HALF) load_add(0, q0);
   const int npro = nk < NST ? nk : NST;
   for (int s = 0; s < npro; ++s) issue(s);
 
   for (int kt = 0; kt < nk; ++kt) {
     // stage kt landed: later stages up to kt + NST - 2 (at the start kt + NST - 1) are on their way
-    int last = kt == 0 ? NST - 1 : kt + NST - 2;
-    if (last > nk - 1) last = nk - 1;
-    wait_vmcnt((last - kt) * LOADS);
+    // (a constant count but at both ends: the run-time count is a jump through a table)
+    if (kt > 0 && kt + NST - 2 < nk) {
+      LCM_WAIT_VMCNT((NST - 2) * LOADS);
+    } else {
+      const int last = kt + NST - 1 < nk ? kt + NST - 1 : nk - 1;
+      wait_vmcnt((last - kt) * LOADS);
+    }
     wait_lds_reads();
     block_barrier();  // every wave's loads of stage kt visible; stage kt - 1 read by all
     if (kt > 0 && kt + NST - 1 < nk) issue(kt + NST - 1);  // into stage kt - 1's slot
@@ -432,28 +450,27 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
   }
 
   // 32x32 D layout: column lane % 32, rows 8 (r / 4) + 4 (lane / 32) + r % 4
-  const Tc* add = static_cast<const Tc*>(p.add);
-  if constexpr (sizeof(Tc) == 2) {
+  if constexpr (HALF) {
     // bf16: 32 rows at a time through the wave's own piece of the ring, so that dx_add is read and
     // dx written 16 bytes a lane in whole lines (8 bytes a lane from the accumulators as they
     // lie took 120 us for dx_add and 60 us for dx at T = 16384, d = 6144)
-    constexpr int PITCH = WC + 4, LPR = WC / 8, RPI = 64 / LPR;  // lanes of a row, rows at a time
+    constexpr int PITCH = WC + 4;
     static_assert(WAVES * 32 * PITCH * 4 <= NST * STAGE, "fits the ring");
     Tc* out = static_cast<Tc*>(p.c);
     float* buf = reinterpret_cast<float*>(smem) + wave * 32 * PITCH;
-    const int rl = lane / LPR, cl = (lane % LPR) * 8, n = n0 + wn * WC + cl;
+    const int n = n0 + wn * WC + cl;
+    uint4 q1[NG];
+    load_add(1, q1);
     wait_lds_reads();
     block_barrier();  // the ring is read by all
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      uint4 q[32 / RPI];
-      float un[32 / RPI];
+      const uint4(&q)[NG] = i == 0 ? q0 : q1;
+      float un[NG];
 #pragma unroll
-      for (int g = 0; g < 32 / RPI; ++g) {
+      for (int g = 0; g < NG; ++g) {
         const int m = m0 + wm * 64 + i * 32 + g * RPI + rl;
-        const bool in = m < p.M && n < p.N;
-        q[g] = add && in ? *reinterpret_cast<const uint4*>(add + size_t(m) * p.N + n) : make_uint4(0, 0, 0, 0);
-        un[g] = F16 && in ? p.rscale[m] : 1.f;
+        un[g] = F16 && m < p.M ? p.rscale[m] : 1.f;
       }
 #pragma unroll
       for (int j = 0; j < NBL; ++j)
@@ -461,7 +478,7 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
         for (int r = 0; r < 16; ++r) buf[(8 * (r >> 2) + 4 * khalf + (r & 3)) * PITCH + j * 32 + l32] = acc[i][j][r];
       wait_lds_reads();  // (its writes: the same counter)
 #pragma unroll
-      for (int g = 0; g < 32 / RPI; ++g) {
+      for (int g = 0; g < NG; ++g) {
         const int m = m0 + wm * 64 + i * 32 + g * RPI + rl;
         const float* v = buf + (g * RPI + rl) * PITCH + cl;
         const float4 lo = *reinterpret_cast<const float4*>(v), hi = *reinterpret_cast<const float4*>(v + 4);
