@@ -283,37 +283,78 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
 
-  // a wave's load i of an operand with contiguous columns (BC of them) fills bytes
-  // 1024 (wave + WAVES i) of its part: 512 / BC rows of 2 BC bytes
-  auto col_load = [&](const bf16_t* src, size_t plane, int np, int op_bytes, int BC, int n_loads, int k0, int c0, int ld,
-                      unsigned char* dst) {
-    const int rpl = 512 / BC, cpr = BC / 8;  // rows of a load, 16-byte chunks of a row
-    for (int i = 0; i < n_loads; ++i) {
-      const int kr = rpl * (wave + WAVES * i) + lane / cpr, sl = lane % cpr;
-      const int ch = 2 * ((sl >> 1) ^ (2 * (kr & 3))) + (sl & 1);
-      const int k = k0 + kr, c = c0 + ch * 8;
-      const bool in = k < kend && c < ld;
-      const bf16_t* g = src + size_t(k) * ld + c;
-      for (int q = 0; q < np; ++q)
-        dma16(in ? g + q * plane : p.zero, dst + q * op_bytes + (wave + WAVES * i) * 1024);
-    }
+  // A wave's load i of an operand with contiguous columns (BC of them) fills bytes
+  // 1024 (wave + WAVES i) of its part: 512 / BC rows of 2 BC bytes.
+  auto col_place = [&](int BC, int i, int& kr, int& ch) {  // the lane's row and 16-byte chunk
+    const int rpl = 512 / BC, cpr = BC / 8;  // rows of a load, chunks of a row
+    const int sl = lane % cpr;
+    kr = rpl * (wave + WAVES * i) + lane / cpr;
+    ch = 2 * ((sl >> 1) ^ (2 * (kr & 3))) + (sl & 1);
   };
+  // Whole stages: the lane's byte offset from the stage's first element does not change, so a
+  // load is a scalar base and that offset.  Columns past the operand repeat a valid column and
+  // rows past M a valid row; neither is stored.
+  uint32_t off_a[LA], off_b[LB];
+#pragma unroll
+  for (int i = 0; i < LA; ++i) {
+    if constexpr (DX) {
+      const int r = 16 * (wave + WAVES * i) + (lane >> 2);
+      off_a[i] = uint32_t(m0 + r < p.M ? r : 0) * p.lda * 2 + ((lane & 3) ^ swz4(r)) * 16;
+    } else {
+      int kr, ch;
+      col_place(BM, i, kr, ch);
+      off_a[i] = uint32_t(kr) * p.lda * 2 + (m0 + ch * 8 < p.lda ? ch * 16 : 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < LB; ++i) {
+    int kr, ch;
+    col_place(BN, i, kr, ch);
+    off_b[i] = uint32_t(kr) * p.ldb * 2 + (n0 + ch * 8 < p.ldb ? ch * 16 : 0);
+  }
+  const bool near = p.ldb < (1 << 25);  // 32 rows within 2^32 bytes
   auto issue = [&](int kt) {
     unsigned char* st = smem + (kt % NST) * STAGE;
+    unsigned char* sb = st + NA * A_OP;
     const int k0 = kbeg + kt * BK;
-    if constexpr (DX) {
+    const bf16_t* a0 = DX ? p.a + size_t(m0) * p.lda + k0 : p.a + size_t(k0) * p.lda + m0;
+    const bf16_t* b0 = p.b + size_t(k0) * p.ldb + n0;
+    if (near && k0 + BK <= kend) {
 #pragma unroll
-      for (int i = 0; i < LA; ++i) {
-        const int r = 16 * (wave + WAVES * i) + (lane >> 2);
-        const int m = m0 + r < p.M ? m0 + r : m0;  // rows past M repeat a valid row; never stored
-        const bf16_t* g = p.a + size_t(m) * p.lda + k0 + ((lane & 3) ^ swz4(r)) * 8;
+      for (int q = 0; q < NA; ++q) {
+        const char* g = reinterpret_cast<const char*>(a0 + q * p.plane_a);
 #pragma unroll
-        for (int q = 0; q < NA; ++q) dma16(g + q * p.plane_a, st + q * A_OP + (wave + WAVES * i) * 1024);
+        for (int i = 0; i < LA; ++i) dma16(g + off_a[i], st + q * A_OP + (wave + WAVES * i) * 1024);
       }
-    } else {
-      col_load(p.a, p.plane_a, NA, A_OP, BM, LA, k0, m0, p.lda, st);
+#pragma unroll
+      for (int q = 0; q < NB; ++q) {
+        const char* g = reinterpret_cast<const char*>(b0 + q * p.plane_b);
+#pragma unroll
+        for (int i = 0; i < LB; ++i) dma16(g + off_b[i], sb + q * B_OP + (wave + WAVES * i) * 1024);
+      }
+      return;
     }
-    col_load(p.b, p.plane_b, NB, B_OP, BN, LB, k0, n0, p.ldb, st + NA * A_OP);
+    // a piece's last, partial stage (the tokens of dW): rows past its end are zeros
+    for (int q = 0; q < NA; ++q)
+      for (int i = 0; i < LA; ++i) {
+        const bf16_t* g;
+        if constexpr (DX) {
+          g = reinterpret_cast<const bf16_t*>(reinterpret_cast<const char*>(a0 + q * p.plane_a) + off_a[i]);
+        } else {
+          int kr, ch;
+          col_place(BM, i, kr, ch);
+          const bool in = k0 + kr < kend && m0 + ch * 8 < p.lda;
+          g = in ? a0 + q * p.plane_a + size_t(kr) * p.lda + ch * 8 : p.zero;
+        }
+        dma16(g, st + q * A_OP + (wave + WAVES * i) * 1024);
+      }
+    for (int q = 0; q < NB; ++q)
+      for (int i = 0; i < LB; ++i) {
+        int kr, ch;
+        col_place(BN, i, kr, ch);
+        const bool in = k0 + kr < kend && n0 + ch * 8 < p.ldb;
+        dma16(in ? b0 + q * p.plane_b + size_t(kr) * p.ldb + ch * 8 : p.zero, sb + q * B_OP + (wave + WAVES * i) * 1024);
+      }
   };
 
   const int l32 = lane & 31, khalf = lane >> 5;
