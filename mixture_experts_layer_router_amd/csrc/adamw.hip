@@ -266,6 +266,11 @@ __global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args 
   const Desc& t = a.t[ti];
   float gs = 1.f;
   if (h.grad_scale) gs = *h.grad_scale;
+  // A scale that is not finite leaves the step out.  32 bits: asked for behind the strip's loads,
+  // which it would hold up (40 small tensors: 9.7 us before, 7.2 behind); 8 bits: once for all
+  // strips (403M weights: 880 us behind every strip's loads, 815 before).
+  const bool finite = fabsf(gs) < INFINITY;
+  if (BITS == 8 && !finite) return;
   int step = h.step;
   double p1 = h.p1, p2 = h.p2;
   if (h.step_dev) {
@@ -310,8 +315,7 @@ __global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args 
         v[2 * c + 1] = mul(r1, r1);
       }
     }
-    // a step that is left out: the scale is asked for behind the loads, which it would hold up
-    if (!(fabsf(gs) < INFINITY)) return;
+    if (BITS == 32 && !finite) return;
     float least = INFINITY;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
