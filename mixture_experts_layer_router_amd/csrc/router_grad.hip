@@ -9,6 +9,17 @@
 //                      by side in one grid
 //   sum_parts_kernel   the pieces of dW's reduction over the tokens, added in order
 //
+// What bounds it.  T = 16384, d = 6144, E = 768, bf16: 0.66 ms.  dW's three products of
+// 155 GFLOP take 0.37-0.40 ms, 1.15-1.25 PFLOP/s, the rate of a large library product (1.2
+// measured on this card); dx's one takes 0.20-0.22 for 0.4 GB of dx_add and dx and 155 GFLOP;
+// the operands 0.045, W_r 0.01, the sum of dW's three pieces 0.014.  One 155 GFLOP product
+// each in fp32 (150 TFLOP/s) would take 1.0 ms.  Steps that got it there: 8.0 ms on plain fp32
+// tiles, 0.95 on bf16 parts, 0.77 with dx from fp16 rows, 0.71 with two workgroups a CU and dx
+// through LDS, 0.66 with constant waits, dx_add loaded early and lane offsets kept.
+// Few tokens and narrow pools are bound by their launches and by a few memory latencies
+// each: T = 64, d = 6144, E = 768 takes 23 us (operands 6.5, products 18), T = 4096, d = 2048,
+// E = 96 takes 31 (6.6, 21.5, sum 4), fp32 T = 1777, d = 1028, E = 77 takes 25 (9, 14, 3).
+//
 // Precision.  dW is an fp32 output: dlogits is cut into three bf16 parts (24 bits), the tokens
 // are bf16 already (or cut the same way), every product of parts is exact and the matrix cores
 // add them in fp32.  dx of an fp32 layer is made the same way.  dx of a bf16 layer is rounded
