@@ -218,7 +218,8 @@ __device__ __forceinline__ void store_codes(void* p, int64_t i, int cnt, uint2 v
     if (c < cnt) q[c] = uint8_t((c < 4 ? v.x : v.y) >> (8 * (c & 3)));
 }
 
-// Block exponent (at least -127) of the 8 values of each of a row of 16 lanes.
+// Block exponent of the 8 values of each of a row of 16 lanes, within -127..127 (the exponent of an
+// infinity, as g^2 overflows to one, is far outside).
 template <int CTRL>
 __device__ __forceinline__ float row_max(float v) {
   return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 15, 15, true)));
@@ -230,7 +231,7 @@ __device__ __forceinline__ int block_k(const float (&val)[8]) {
   // rotations of the row by 8, 4, 2, 1 lanes
   amax = row_max<0x121>(row_max<0x122>(row_max<0x124>(row_max<0x128>(amax))));
   const int k = block_exp(amax);
-  return k < -127 ? -127 : k;
+  return k < -127 ? -127 : k > 127 ? 127 : k;
 }
 
 template <bool SMALL>
@@ -320,15 +321,16 @@ __global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args 
       }
     }
     if (BITS == 32 && !finite) return;
-    float least = INFINITY;
+    float least = INFINITY, most = 0.f;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       const float gr = mul(g[c], gs);
       m[c] = add(mul(h.beta1, m[c]), mul(h.omb1, gr));
       v[c] = add(mul(h.beta2, v[c]), mul(mul(h.omb2, gr), gr));
       least = fminf(least, v[c]);
+      most = fmaxf(most, v[c]);
     }
-    if (__any(least < 7.888609052210118e-31f)) {  // 2^-100
+    if (__any(least < 7.888609052210118e-31f || most == INFINITY)) {  // 2^-100; g^2 may overflow
 #pragma unroll
       for (int c = 0; c < 8; ++c) r[c] = sqrtf(v[c]);
     } else {

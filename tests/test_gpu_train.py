@@ -486,6 +486,53 @@ def test_adamw_skips_a_step_that_is_not_finite(bits, value):
         assert all(torch.equal(s, t) for s, t in zip(x, y))
 
 
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_overflowing_square_moves_no_weight(bits):
+    """A finite gradient whose square is infinite: v and its root are infinite, so by the formula
+    that weight's update is 0 (m / infinity), in this step and in the next."""
+    import torch
+    import mixture_experts_layer_router_amd as lm
+    n, at = 3000, 2222
+    say(f"adamw {bits} bits, gradient 1e20")
+    g = torch.full((n,), 0.5, device=device())
+    g[at] = 1e20
+    p = torch.ones(n, device=device())
+    opt = lm.AdamW([p], [g], state_bits=bits)
+    for step in (1, 2):
+        opt.step(1e-2, step=step)
+        w = to_np(p)
+        assert w[at] == 1.0 and np.isfinite(w).all()
+        assert (np.delete(w, np.s_[2176:2304]) < 1.0).all()
+    if bits == 32:
+        assert np.isinf(to_np(opt.v[0])[at]) and np.isfinite(np.delete(to_np(opt.v[0]), at)).all()
+
+
+@pytest.mark.parametrize("big", [1e20, np.inf])
+def test_adamw_8bit_overflow_stays_in_its_block(big):
+    """v overflows in one block of 128: that block gets the largest exponent, the others are
+    the bits of a step without it."""
+    import torch
+    import mixture_experts_layer_router_amd as lm
+    say(f"adamw 8 bits, gradient {big}")
+    rng = np.random.default_rng(21)
+    n, at = 1000, 300  # block 2: 256..383
+    g = rng.standard_normal(n).astype(np.float32)
+    runs = []
+    for value in (g[at], np.float32(big)):
+        g[at] = value
+        p = torch.ones(n, device=device())
+        opt = lm.AdamW([p], [torch.tensor(g, device=device())], state_bits=8)
+        for step in (1, 2):
+            opt.step(1e-2, step=step, seed=3)
+        runs.append([to_np(t) for t in (p, opt.m[0], opt.v[0], opt.m_scales[0], opt.v_scales[0])])
+    out, blk = np.r_[0:256, 384:n], np.r_[0:2, 3:8]
+    for a, b in zip(runs[0][:3], runs[1][:3]):
+        np.testing.assert_array_equal(a[out], b[out])
+    for a, b in zip(runs[0][3:], runs[1][3:]):
+        np.testing.assert_array_equal(a[blk], b[blk])
+    assert runs[1][4][2] == 254 and runs[1][2][at] == 126
+
+
 def test_adamw_zero_gradients_and_betas():
     """Zero gradients on a new state: the weight only decays, the states stay zero (exponent
     byte 127); beta1 = beta2 = 0: m = g, v = g^2."""
