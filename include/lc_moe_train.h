@@ -196,8 +196,8 @@ typedef struct {
  * A state starts as zeros: codes 0 and exponent bytes 127.
  *
  * state_bits = 32: m and v are fp32, m_scale and v_scale are not read (may be NULL).
- * Tensors with n = 0 are skipped and their pointers not read.  The tensors of one call may
- * not overlap.  count = 0 does nothing; count < 0, n out of range, state_bits other than 8
+ * Tensors with n = 0 are skipped and their pointers not read.  What a call
+ * writes may overlap nothing else of it; gradients may be shared.  count = 0 does nothing; count < 0, n out of range, state_bits other than 8
  * and 32, step < 1 without step_dev, a beta outside [0, 1) or eps < 0: LC_MOE_E_SHAPE; an
  * unknown dtype: LC_MOE_E_DTYPE. */
 lc_moe_status lc_moe_adamw(const lc_moe_adamw_tensor* tensors, int32_t count,

@@ -162,15 +162,23 @@ def _on_gpu(device):
         raise ValueError(f"the tensors are on {device}; the operators run on the GPU")
 
 
-def _space(size, given, device, where):
+def _apart(name, t, others):
+    """t, which a call writes, shares no memory with the others (contiguous tensors or None)."""
+    lo, hi = t.data_ptr(), t.data_ptr() + t.nbytes
+    for q in others:
+        if q is not None and q.nbytes and lo < q.data_ptr() + q.nbytes and q.data_ptr() < hi:
+            raise ValueError(f"{name} overlaps another tensor of the call")
+
+
+def _space(size, given, device, where, used=()):
+    if given is not None:
+        if given.device != device or not given.is_contiguous():
+            raise ValueError(f"workspace: a contiguous tensor on {device} is needed")
+        _apart("workspace", given, used)
     _on_gpu(device)
     if size == 0:
         raise LcMoeError(2, where)
-    if given is None:
-        return torch.empty(size, dtype=torch.uint8, device=device)
-    if given.device != device or not given.is_contiguous():
-        raise ValueError(f"workspace: a contiguous tensor on {device} is needed")
-    return given
+    return torch.empty(size, dtype=torch.uint8, device=device) if given is None else given
 
 
 def forward_saved(x, N, Z, K, I, workspace):
@@ -208,7 +216,8 @@ def balance_loss(logits, topk_idx, N, balance_coef, z_coef=0.0, seq_offsets=None
     if token_mask is not None:
         _need(token_mask, "token_mask", (T,), torch.uint8, dev)
     shape = Shape(T, 8, N, E - N, K, 8, BF16)
-    ws = _space(lc_moe_balance_workspace_size(shape, S), workspace, dev, "lc_moe_balance_workspace_size")
+    ws = _space(lc_moe_balance_workspace_size(shape, S), workspace, dev, "lc_moe_balance_workspace_size",
+                (logits, topk_idx, seq_offsets, token_mask))
     out = dict(loss=logits.new_empty(2), load=topk_idx.new_empty((S, E)), prob=logits.new_empty((S, E)),
                dlogits=torch.empty_like(logits) if need_grad else None)
     _on(dev, lc_moe_balance_loss, shape, BalanceCoef(balance_coef, z_coef), logits, topk_idx, seq_offsets, S,
@@ -257,8 +266,11 @@ def router_backward(x, w_router, logits, topk_idx, dgate, N, dlogits_aux=None, d
         _need(dx_add, "dx_add", (T, d), x.dtype, dev)
     if dx is not None:
         _need(dx, "dx", (T, d), x.dtype, dev)
+        same = dx_add is not None and dx_add.data_ptr() == dx.data_ptr()
+        _apart("dx", dx, (x, w_router, logits, topk_idx, dgate, dlogits_aux, None if same else dx_add))
     shape = Shape(T, d, N, E - N, K, 8, code)
-    ws = _space(lc_moe_router_backward_workspace_size(shape), workspace, dev, "lc_moe_router_backward_workspace_size")
+    ws = _space(lc_moe_router_backward_workspace_size(shape), workspace, dev, "lc_moe_router_backward_workspace_size",
+                (x, w_router, logits, topk_idx, dgate, dlogits_aux, dx_add, dx))
     out = {}
     if need_dx:
         out["dx"] = dx if dx is not None else torch.empty_like(x)
@@ -330,10 +342,21 @@ class AdamW:
         lists = (grads, m, v, m_scales, v_scales, masters, wd, ls)
         if any(a is None or len(a) != n for a in lists):
             raise ValueError(f"AdamW: every list needs {n} entries")
-        for name, ts in (("params", params), ("m", m), ("v", v)):
-            at = [t.data_ptr() for t in ts if t.numel()]
-            if len(set(at)) < len(at):
-                raise ValueError(f"AdamW: a tensor is twice in {name}")
+        # what a step writes shares no memory with anything else of it; gradients may be shared
+        spans = []
+        for name, ts in (("params", params), ("m", m), ("v", v), ("m_scales", m_scales), ("v_scales", v_scales),
+                         ("masters", masters), ("grads", grads)):
+            spans += [(t.data_ptr(), t.data_ptr() + t.nbytes, f"{name}[{i}]") for i, t in enumerate(ts)
+                      if t is not None and t.numel()]
+        end, last, grads_end, last_grad = 0, "", 0, ""
+        for lo, hi, name in sorted(spans):
+            written = not name.startswith("grads")
+            if lo < end or (written and lo < grads_end):
+                raise ValueError(f"AdamW: {name} overlaps {last if lo < end else last_grad}")
+            if written:
+                end, last = hi, name
+            elif hi > grads_end:
+                grads_end, last_grad = hi, name
         self.params, self.grads, self.m, self.v = list(params), list(grads), list(m), list(v)
         self.m_scales, self.v_scales, self.masters = list(m_scales), list(v_scales), list(masters)
         self.state_bits, self.device = state_bits, params[0].device

@@ -159,6 +159,46 @@ def test_wrapper_refusals():
             pytest.fail(f"call {i} was not refused")
 
 
+def test_wrappers_refuse_overlaps():
+    """What a call writes may not lie over what else it reads or writes, but for what the header
+    allows (the CPU tensors of the allowed calls are refused for being on the CPU)."""
+    import torch
+    T, E, K, d, n = 6, 8, 2, 16, 100
+    f = torch.zeros(4 * n)
+    p, g, m, v = (f[i * n:(i + 1) * n] for i in range(4))
+    b = torch.zeros(n, dtype=torch.uint8)
+    s = [torch.zeros(1, dtype=torch.uint8) for _ in range(2)]
+    lg, idx = torch.zeros(T, E), torch.zeros(T, K, dtype=torch.int32)
+    x, w, add, dg = torch.zeros(T, d), torch.zeros(E, d), torch.zeros(T, d), torch.zeros(T, K)
+    two = torch.zeros(2 * T * d)
+    space = lambda t: t.view(-1).view(torch.uint8)  # noqa: E731
+    bad = [lambda: lm.AdamW([p], [g], m=[m], v=[m]), lambda: lm.AdamW([p], [p], m=[m], v=[v]),
+           lambda: lm.AdamW([p], [g], m=[g], v=[v]), lambda: lm.AdamW([p], [g], masters=[p]),
+           lambda: lm.AdamW([f[:n], f[n - 1:2 * n - 1]], [v, v]), lambda: lm.AdamW([f[1:n]], [f[:n - 1]]),
+           lambda: lm.AdamW([p], [g], m=[b], v=[b.clone()], m_scales=s[:1], v_scales=s[:1], state_bits=8),
+           lambda: lm.AdamW([f[n:2 * n], f[2 * n:3 * n]], [f[:n], f[:n]], masters=[f[3 * n:], f[3 * n:]]),
+           # a long gradient in front of short weights
+           lambda: lm.AdamW([f[:1], f[2:3], f[:0]], [f[1:2], f[1:2], f[:0]], m=[f[4:5], f[5:6], p[:0]],
+                            v=[f[6:7], f[5:6], p[:0]]),
+           lambda: lm.router_backward(x, w, lg, idx, dg, 4, dx=x),
+           lambda: lm.router_backward(x, w, lg, idx, dg, 4, dx_add=two[:T * d].view(T, d), dx=two[4:T * d + 4].view(T, d)),
+           lambda: lm.router_backward(x, w, lg, idx, dg, 4, workspace=space(lg)),
+           lambda: lm.router_backward(x, w, lg, idx, dg, 4, dx_add=add, dx=add, workspace=space(add)),
+           lambda: lm.balance_loss(lg, idx, 4, 0.1, workspace=space(lg)),
+           lambda: lm.balance_loss(lg, idx, 4, 0.1, workspace=space(idx))]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError, match="overlaps"):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    good = [lambda: lm.AdamW([p, v], [g, g]), lambda: lm.AdamW([p], [g], m=[m], v=[v]),
+            lambda: lm.AdamW([p[:0], p, p[:0]], [g[:0], g, g[:0]]),
+            lambda: lm.router_backward(x, w, lg, idx, dg, 4, dx_add=add, dx=add),
+            lambda: lm.router_backward(x, w, lg, idx, dg, 4, dx_add=x, workspace=torch.zeros(4))]
+    for call in good:
+        with pytest.raises(ValueError, match="run on the GPU"):
+            call()
+
+
 PROGRAM = r"""
 #include <stdio.h>
 #include <string.h>
