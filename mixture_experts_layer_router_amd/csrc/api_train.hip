@@ -1,5 +1,7 @@
 // C-ABI entry points of the training operators: argument checks, workspace carving and the
 // launch sequence.  Every argument's meaning is documented in include/lc_moe_train.h.
+#include <cfloat>
+
 #include "checks.h"
 #include "train.h"
 
@@ -110,8 +112,8 @@ lc_moe_status lc_moe_adamw(const lc_moe_adamw_tensor* tensors, int32_t count, co
   const lc_moe_adamw_hyper& h = *hyper;
   if (count < 0 || (h.state_bits != 8 && h.state_bits != 32)) return LC_MOE_E_SHAPE;
   if (!h.step_dev && h.step < 1) return LC_MOE_E_SHAPE;
-  if (!(h.beta1 >= 0.f && h.beta1 < 1.f) || !(h.beta2 >= 0.f && h.beta2 < 1.f) || !(h.eps >= 0.f))
-    return LC_MOE_E_SHAPE;
+  if (!(h.beta1 >= 0.f && h.beta1 < 1.f) || !(h.beta2 >= 0.f && h.beta2 < 1.f)) return LC_MOE_E_SHAPE;
+  if (!(h.eps >= FLT_MIN || h.eps == 0.f)) return LC_MOE_E_SHAPE;  // (negative and NaN too)
   LCM_CHECK(check_ptr(h.step_dev, true));
   LCM_CHECK(check_ptr(h.grad_scale, true));
   if (count == 0) return LC_MOE_OK;

@@ -129,6 +129,13 @@ def test_adamw_refusals():
     assert call(h=dict(step_dev=MIS)) == 4 and call(h=dict(grad_scale=MIS)) == 4
 
 
+def test_adamw_refuses_a_subnormal_eps():
+    f = lt._lib().lc_moe_adamw
+    for eps, status in ((0.0, 0), (2.0 ** -126, 0), (2.0 ** -127, 2), (2.0 ** -149, 2)):
+        h = lt.AdamwHyper(1e-3, 0.9, 0.95, eps, 32, 1, None, None, 0)
+        assert f(None, 0, ctypes.byref(h), None) == status, eps
+
+
 def test_wrapper_refusals():
     """The checked wrappers refuse tensors of another type, shape or layout (on the CPU: they
     get no further than their checks)."""
