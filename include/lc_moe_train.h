@@ -191,7 +191,7 @@ typedef struct {
  * same bits for the same arguments (the value over 2^k may be an ulp off); and an r above 0
  * stays above 0, so that no m is ever divided by eps alone.  The update itself uses m and v
  * before they are rounded.  A state that becomes infinite (v, for a gradient above 1e19) takes
- * the exponent byte 254 and the largest code, which is infinite again when it is read; its
+ * the exponent byte 247 and the largest code, which is infinite again when it is read; its
  * block is lost, other blocks are not.
  * A state starts as zeros: codes 0 and exponent bytes 127.
  *

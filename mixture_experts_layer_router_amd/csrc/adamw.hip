@@ -1,10 +1,13 @@
 // One AdamW step over many tensors (formulas and the form of the 8-bit states in
 // include/lc_moe_train.h).  A step reads and writes every byte of the weights and states
 // once: it is bound by HBM.  403M bf16 weights with fp32 masters and 32-bit states (28 bytes a
-// weight) take 2.11 ms, 5.3 TB/s, where a copy reaches 4.9.  With 8-bit states and no masters
-// (10 bytes) 0.82 ms, 4.9 TB/s: there the arithmetic (about 60 operations a weight: the hash,
-// two random roundings, a root) takes nearly as long as the bytes.  Decoding in integer
-// arithmetic, and 1 - beta^step by expm1 in every thread, took 1.25 ms.
+// weight) take 1.88-2.12 ms, 5.3-6.0 TB/s, on different cards, where a copy reaches 4.9.  With
+// 8-bit states and no masters (10 bytes) 0.68-0.78 ms, 5.2-5.9 TB/s: there the arithmetic (the hash, two random roundings, a root)
+// counts beside the bytes.  Steps: 1.25 ms with codes decoded in integer arithmetic and
+// 1 - beta^step by expm1 in every thread, 0.84 without, 0.795 with strips typed by what the
+// tensors hold (0.826 if their loads are issued a strip ahead at 113 registers), 0.775 with the
+// hardware's random rounding, which also takes the registers from 94 to 67.  (On the fastest card
+// seen the last two together take it from 0.795 to 0.683.)
 // The tensors' addresses travel in the kernel's arguments, up to kMaxTensors a launch, so a
 // step of a few dozen tensors is one launch and needs no device table.
 #include <cmath>
@@ -92,21 +95,6 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
   x ^= x >> 15;
   x *= 0xBB67AE85u;
   return x ^ (x >> 16);
-}
-
-// E4M3 code of |y| <= 448 rounded down or up by the 20-bit fraction r: the digits below the
-// code's last place plus r carry into it with probability (their size) / (one step).  SMALL:
-// y may be below 2^-6, where the code's steps are 2^-9 whatever the exponent.
-template <bool SMALL>
-__device__ __forceinline__ uint32_t e4m3_random(float y, uint32_t r) {
-  const float a = fabsf(y);
-  uint32_t q = (__float_as_uint(a) + (r - (960u << 20))) >> 20;
-  if constexpr (SMALL) {
-    const uint32_t s = static_cast<uint32_t>(add(a * 512.f, static_cast<float>(r) * 9.5367431640625e-07f));
-    q = a < 0.015625f ? s : q;
-  }
-  q = q < 126u ? q : 126u;
-  return q | ((__float_as_uint(y) >> 24) & 128u);
 }
 
 // The square root rounded to nearest for 2^-100 <= v < infinity: v / sqrt(v) from the
@@ -218,33 +206,44 @@ __device__ __forceinline__ void store_codes(void* p, int64_t i, int cnt, uint2 v
     if (c < cnt) q[c] = uint8_t((c < 4 ? v.x : v.y) >> (8 * (c & 3)));
 }
 
-// Block exponent of the 8 values of each of a row of 16 lanes, within -127..127 (the exponent of an
-// infinity, as g^2 overflows to one, is far outside).
+// The largest magnitude of a row of 16 lanes' values, from each lane's.
 template <int CTRL>
 __device__ __forceinline__ float row_max(float v) {
   return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 15, 15, true)));
 }
-__device__ __forceinline__ int block_k(const float (&val)[8]) {
+__device__ __forceinline__ float block_max(const float (&val)[8]) {
   float amax = 0.f;
 #pragma unroll
   for (int c = 0; c < 8; ++c) amax = fmaxf(amax, fabsf(val[c]));
   // rotations of the row by 8, 4, 2, 1 lanes
-  amax = row_max<0x121>(row_max<0x122>(row_max<0x124>(row_max<0x128>(amax))));
-  const int k = block_exp(amax);
-  return k < -127 ? -127 : k > 127 ? 127 : k;
+  return row_max<0x121>(row_max<0x122>(row_max<0x124>(row_max<0x128>(amax))));
+}
+// Exponent byte of a block: 2^(byte - 127) is the smallest power of two p with amax <= 448 p,
+// at least 2^-127; 127 for zeros.  448 = 1.75 2^8, so a mantissa above 1.75 carries.
+__device__ __forceinline__ int block_byte(float amax) {
+  const uint32_t u = __float_as_uint(amax), k = (u + 0x1FFFFFu) >> 23;
+  return u == 0u ? 127 : k > 8u ? int(k) - 8 : 0;
 }
 
-template <bool SMALL>
-__device__ __forceinline__ void encode(const float (&m)[8], const float (&r)[8], float im, float iv, uint32_t first,
-                                       uint2& cm, uint2& cv) {
-  uint32_t qm[2] = {0, 0}, qv[2] = {0, 0};
+// E4M3 codes of 8 values y rounded down or up by chance (v_cvt_sr_fp8_f32): the digits below the
+// code's last place plus the top 20 of the 32 random bits carry into it with probability
+// (their size) / (one step); below 2^-6 the steps are 2^-9.
+__device__ __forceinline__ void encode(const float (&m)[8], const float (&r)[8], uint32_t first, uint2& cm, uint2& cv) {
+  int qm[2] = {0, 0}, qv[2] = {0, 0};
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const uint32_t u = mix(first + c);
-    qm[c >> 2] |= e4m3_random<SMALL>(m[c] * im, ((u & 0xFFFFu) << 4) + 8u) << (8 * (c & 3));
-    uint32_t q = e4m3_random<SMALL>(r[c] * iv, ((u >> 16) << 4) + 8u);
-    if (SMALL) q = r[c] > 0.f && q == 0u ? 1u : q;  // (a code of 8 or more else)
-    qv[c >> 2] |= q << (8 * (c & 3));
+  for (int c = 0; c < 2; ++c) {
+    uint32_t u[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) u[b] = mix(first + 4 * c + b);
+    // 16 bits each and half a unit of them
+    qm[c] = __builtin_amdgcn_cvt_sr_fp8_f32(m[4 * c], (u[0] << 16) | 0x8000u, qm[c], 0);
+    qm[c] = __builtin_amdgcn_cvt_sr_fp8_f32(m[4 * c + 1], (u[1] << 16) | 0x8000u, qm[c], 1);
+    qm[c] = __builtin_amdgcn_cvt_sr_fp8_f32(m[4 * c + 2], (u[2] << 16) | 0x8000u, qm[c], 2);
+    qm[c] = __builtin_amdgcn_cvt_sr_fp8_f32(m[4 * c + 3], (u[3] << 16) | 0x8000u, qm[c], 3);
+    qv[c] = __builtin_amdgcn_cvt_sr_fp8_f32(r[4 * c], (u[0] & 0xFFFF0000u) | 0x8000u, qv[c], 0);
+    qv[c] = __builtin_amdgcn_cvt_sr_fp8_f32(r[4 * c + 1], (u[1] & 0xFFFF0000u) | 0x8000u, qv[c], 1);
+    qv[c] = __builtin_amdgcn_cvt_sr_fp8_f32(r[4 * c + 2], (u[2] & 0xFFFF0000u) | 0x8000u, qv[c], 2);
+    qv[c] = __builtin_amdgcn_cvt_sr_fp8_f32(r[4 * c + 3], (u[3] & 0xFFFF0000u) | 0x8000u, qv[c], 3);
   }
   cm = make_uint2(qm[0], qm[1]);
   cv = make_uint2(qv[0], qv[1]);
@@ -287,37 +286,27 @@ __global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args 
   const Scalars sc = scalars(h, t.lrs, t.wd, p1, p2);
   const uint32_t key0 = mix(h.seed + 0x9E3779B9u * uint32_t(step)) + 0x3C6EF373u * ((t.flags >> 2) + 1u);
   const int64_t strip0 = int64_t(t.at) + int64_t(blockIdx.x - a.first[ti]) * h.strips;
-  // FULL: the strip lies inside the tensor, so no element's place is asked for
-  auto strip = [&](int64_t at, auto full) {
-    constexpr bool FULL = decltype(full)::value;
-    // 32 bits: groups of 4 with a strip's half between them, so that every load and store of
-    // fp32 values is one contiguous piece of a wave; 8 bits: 8 consecutive elements
-    constexpr int GAP = BITS == 32 ? kStrip / 2 : 4;
-    const int64_t i = at + threadIdx.x * (BITS == 32 ? 4 : 8);
-    auto left = [&](int64_t e) { return FULL || t.n - e >= 4 ? 4 : t.n > e ? int(t.n - e) : 0; };
-    const int two[2] = {left(i), left(i + GAP)};
-    const int cnt = two[0] + two[1];  // (8 bits: the thread's elements)
-    float g[8], w[8], m[8], v[8], r[8];
-    load8<GAP>(t.grad, t.flags & 2, i, two, g);
-    if (t.master) load8<GAP>(t.master, false, i, two, w);
-    else load8<GAP>(t.param, t.flags & 1, i, two, w);
-    if constexpr (BITS == 32) {
-      load8<GAP>(t.m, false, i, two, m);
-      load8<GAP>(t.v, false, i, two, v);
-    } else {
-      const uint2 cm = load_codes(t.m, i, cnt), cv = load_codes(t.v, i, cnt);
-      const float sm = cnt ? pow2(int(t.ms[i >> 7]) - 127) : 0.f, sv = cnt ? pow2(int(t.vs[i >> 7]) - 127) : 0.f;
+  // 32 bits: groups of 4 with a strip's half between them, so that every load and store of
+  // fp32 values is one contiguous piece of a wave; 8 bits: 8 consecutive elements
+  constexpr int GAP = BITS == 32 ? kStrip / 2 : 4;
+  const int mine = threadIdx.x * (BITS == 32 ? 4 : 8);  // the thread's place in a strip
+  // The update of a thread's elements from i on (two: how many of each group) from their
+  // gradients, weights and states (8 bits: codes cm, cv of scales sm, sv)
+  auto update = [&](int64_t i, const int (&two)[2], const float (&g)[8], float (&w)[8], float (&m)[8], float (&v)[8],
+                    uint2 cm, uint2 cv, float sm, float sv) {
+    const int cnt = two[0] + two[1];
+    float r[8];
+    if constexpr (BITS == 8) {
       const uint32_t um[2] = {cm.x, cm.y}, uv[2] = {cv.x, cv.y};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {  // two codes at a time (v_cvt_pk_f32_fp8: E4M3 on gfx950)
+      for (int c = 0; c < 4; ++c) {  // two codes and their scale at a time (v_cvt_scalef32_pk_f32_fp8)
         typedef float f32x2 __attribute__((ext_vector_type(2)));
-        const f32x2 dm = c & 1 ? __builtin_amdgcn_cvt_pk_f32_fp8(um[c >> 1], true) : __builtin_amdgcn_cvt_pk_f32_fp8(um[c >> 1], false);
-        const f32x2 dv = c & 1 ? __builtin_amdgcn_cvt_pk_f32_fp8(uv[c >> 1], true) : __builtin_amdgcn_cvt_pk_f32_fp8(uv[c >> 1], false);
-        m[2 * c] = dm[0] * sm;
-        m[2 * c + 1] = dm[1] * sm;
-        const float r0 = dv[0] * sv, r1 = dv[1] * sv;
-        v[2 * c] = mul(r0, r0);
-        v[2 * c + 1] = mul(r1, r1);
+        const f32x2 dm = c & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(um[c >> 1], sm, true)
+                               : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(um[c >> 1], sm, false);
+        const f32x2 dv = c & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(uv[c >> 1], sv, true)
+                               : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(uv[c >> 1], sv, false);
+        m[2 * c] = dm[0], m[2 * c + 1] = dm[1];
+        v[2 * c] = mul(dv[0], dv[0]), v[2 * c + 1] = mul(dv[1], dv[1]);
       }
     }
     if (BITS == 32 && !finite) return;
@@ -348,26 +337,92 @@ __global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args 
       store8<GAP>(t.v, false, i, two, v);
     } else {
       const uint32_t key = mix(key0 + 0x85A308D3u * uint32_t(uint64_t(i) >> 32));
-      const int km = block_k(m), kv = block_k(r);
-      const float im = inverse[km + 127], iv = inverse[kv + 127];
-      float low = INFINITY;  // the smallest quotient of the thread
+      const int bm = block_byte(block_max(m)), bv = block_byte(block_max(r));
+      const float im = inverse[bm], iv = inverse[bv];
+      // An r above 0 gets a code above 0: below 2^-9 that is 1, the code of 2^-9.  Infinities get
+      // the largest code.  Asked for by the smallest and largest v: r iv < 2^-9 only if v iv iv is
+      // below 2^-17.
+      if (__any((least * iv) * iv < 7.62939453125e-06f || most == INFINITY)) {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) low = fminf(low, fminf(fabsf(m[c]) * im, r[c] * iv));
-      uint2 cm, cv;
-      if (__any(low < 0.015625f)) encode<true>(m, r, im, iv, uint32_t(i) + key, cm, cv);
-      else encode<false>(m, r, im, iv, uint32_t(i) + key, cm, cv);
+        for (int c = 0; c < 8; ++c) {
+          m[c] = fminf(fmaxf(m[c] * im, -448.f), 448.f);
+          r[c] = r[c] > 0.f ? fminf(fmaxf(r[c] * iv, 0.001953125f), 448.f) : 0.f;
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) m[c] *= im, r[c] *= iv;
+      }
+      encode(m, r, uint32_t(i) + key, cm, cv);
       store_codes(t.m, i, cnt, cm);
       store_codes(t.v, i, cnt, cv);
       if ((threadIdx.x & 15) == 0 && cnt) {
-        t.ms[i >> 7] = uint8_t(km + 127);
-        t.vs[i >> 7] = uint8_t(kv + 127);
+        t.ms[i >> 7] = uint8_t(bm);
+        t.vs[i >> 7] = uint8_t(bv);
       }
     }
   };
-  for (int s = 0; s < h.strips; ++s) {
-    const int64_t at = (strip0 + s) * kStrip;
+  // FULL: the strip lies inside the tensor, so no element's place is asked for
+  auto strip = [&](int64_t at, auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    const int64_t i = at + mine;
+    auto left = [&](int64_t e) { return FULL || t.n - e >= 4 ? 4 : t.n > e ? int(t.n - e) : 0; };
+    const int two[2] = {left(i), left(i + GAP)};
+    const int cnt = two[0] + two[1];
+    float g[8], w[8], m[8], v[8];
+    load8<GAP>(t.grad, t.flags & 2, i, two, g);
+    if (t.master) load8<GAP>(t.master, false, i, two, w);
+    else load8<GAP>(t.param, t.flags & 1, i, two, w);
+    if constexpr (BITS == 32) {
+      load8<GAP>(t.m, false, i, two, m);
+      load8<GAP>(t.v, false, i, two, v);
+      update(i, two, g, w, m, v, uint2{}, uint2{}, 0.f, 0.f);
+    } else {
+      const uint2 cm = load_codes(t.m, i, cnt), cv = load_codes(t.v, i, cnt);
+      const float sm = cnt ? pow2(int(t.ms[i >> 7]) - 127) : 0.f, sv = cnt ? pow2(int(t.vs[i >> 7]) - 127) : 0.f;
+      update(i, two, g, w, m, v, cm, cv, sm, sv);
+    }
+  };
+  if constexpr (BITS == 32) {
+    const int64_t at = strip0 * kStrip;
     if (at + kStrip <= t.n) strip(at, std::true_type{});
     else if (at < t.n) strip(at, std::false_type{});
+  } else {
+    const int64_t whole = t.n / kStrip - strip0;
+    const int full = whole < 0 ? 0 : whole < h.strips ? int(whole) : h.strips;
+    // whole strips; GB, WB: gradients, weights in bf16
+    auto run = [&](auto gb, auto wb) {
+      constexpr bool GB = decltype(gb)::value, WB = decltype(wb)::value;
+      const char* gp = static_cast<const char*>(t.grad);
+      const char* wp = t.master ? reinterpret_cast<const char*>(t.master) : static_cast<const char*>(t.param);
+      auto load = [](const char* p, auto bf, float (&o)[8]) {
+        if constexpr (decltype(bf)::value) {
+          const uint4 q = *reinterpret_cast<const uint4*>(p);
+          const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[2 * c] = __uint_as_float(u[c] << 16), o[2 * c + 1] = __uint_as_float(u[c] & 0xFFFF0000u);
+        } else {
+          const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 16);
+          o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+        }
+      };
+      int64_t i = strip0 * kStrip + mine;
+      const int two[2] = {4, 4};
+#pragma unroll 1
+      for (int s = 0; s < full; ++s, i += kStrip) {
+        float g[8], w[8], m[8], v[8];
+        load(gp + i * (GB ? 2 : 4), gb, g);
+        load(wp + i * (WB ? 2 : 4), wb, w);
+        const uint2 cm = load_codes(t.m, i, 8), cv = load_codes(t.v, i, 8);
+        update(i, two, g, w, m, v, cm, cv, pow2(int(t.ms[i >> 7]) - 127), pow2(int(t.vs[i >> 7]) - 127));
+      }
+    };
+    if (full > 0) {
+      const bool wb = !t.master && (t.flags & 1);
+      if (t.flags & 2) wb ? run(std::true_type{}, std::true_type{}) : run(std::true_type{}, std::false_type{});
+      else wb ? run(std::false_type{}, std::true_type{}) : run(std::false_type{}, std::false_type{});
+    }
+    const int64_t at = (strip0 + full) * kStrip;
+    if (full < h.strips && at < t.n) strip(at, std::false_type{});
   }
 }
 
@@ -386,14 +441,14 @@ hipError_t launch_adamw(const lc_moe_adamw_tensor* tensors, int count, const lc_
   a.h.grad_scale = h.grad_scale;
   a.h.p1 = power(double(h.beta1), h.step_dev ? 1 : h.step);
   a.h.p2 = power(double(h.beta2), h.step_dev ? 1 : h.step);
-  // Strips of a workgroup.  8 bits: eight share its start (the table of scales) where that
-  // leaves enough workgroups to fill the chip several times (403M weights: 842 us with four,
-  // 815 with eight, 818 with sixteen; a step of few elements is done sooner with one each).
+  // Strips of a workgroup.  8 bits: four share its start (the table of scales) where that
+  // leaves enough workgroups to fill the chip several times (403M weights: 775 us with four,
+  // 782 with eight, 792 with sixteen; a step of few elements is done sooner with one each).
   // 32 bits: one, so that the workgroups in flight touch neighbouring memory (403M weights
   // with masters: 2109 us with one, 2126 with two, 2171 with four).
   int64_t total = 0;
   for (int i = 0; i < count; ++i) total += (tensors[i].n + kStrip - 1) / kStrip;
-  a.h.strips = h.state_bits == 8 && total >= 16384 ? 8 : 1;
+  a.h.strips = h.state_bits == 8 && total >= 16384 ? 4 : 1;
   // One launch covers up to kMaxTensors pieces and kMaxBlocks workgroups (the grid holds
   // 2^32 - 1 work-items); a tensor that needs more is cut at a multiple of its strips.
   constexpr int64_t kMaxBlocks = int64_t(1) << 23;
