@@ -9,10 +9,12 @@
 // there a launch's 5 us count.
 //
 // Bound by memory: T = 16384, E = 768, 8 sequences (50 MB of logits read twice, 50 MB of gradient
-// written) takes 39.5 us: 17.7 for the statistics, 4 for the sums, 20 for the gradient, which is
-// what its bytes take at the rate of a copy (4.9 TB/s).  The statistics run at 2.9 TB/s: a wave
-// has one row in flight beside the one it works on, and 512 blocks end together.  T = 64 takes
-// 13 us of kernels, T = 4096 with E = 96 17, less than the two or three calls' own time.
+// written) takes 35.3 us: 16.5 for the statistics, 4 for the sums, 17 for the gradient (5.9 TB/s).  The
+// statistics run at 3 TB/s: their arithmetic, about 17 operations a logit, takes 7 us, and 512
+// blocks begin and end together; four rows of a wave loaded at once made it 37.8.  T = 64 takes
+// 12.5 us of kernels, T = 4096 with E = 96 16, less than the two or three calls' own time.  Steps
+// of the last form: the sequence found by one look at 64 bounds and u kept from token to token
+// (38.4 -> 36.9), no question for -infinity beside the exponential's own (35.3).
 #include "train.h"
 #include "logit_row.h"
 
@@ -23,6 +25,20 @@ __device__ __forceinline__ int seq_bound(const int32_t* __restrict__ off, int i,
   const int v = off[i];
   return v < 0 ? 0 : v > T ? T : v;
 }
+
+// 64 of the sequences' bounds in the lanes of a wave, so that finding a token's sequence and the
+// ones behind it waits for memory once: lane l has bound base + l.
+struct Bounds {
+  int base, held;
+  __device__ __forceinline__ void hold(const int32_t* __restrict__ off, int i, int S, int T, int lane) {
+    base = i;
+    held = seq_bound(off, i + lane < S ? i + lane : S, T);
+  }
+  __device__ __forceinline__ int at(const int32_t* __restrict__ off, int i, int T) const {
+    const int l = __builtin_amdgcn_readfirstlane(i - base);
+    return unsigned(l) < 64u ? __builtin_amdgcn_readlane(held, l) : seq_bound(off, i, T);
+  }
+};
 
 struct BalArgs {
   const float* logits;
@@ -86,25 +102,15 @@ __device__ __forceinline__ void seq_blocks(const BalArgs& a, int s, int& b0, int
   b1 = up > lo ? (up - 1) / a.tok + 1 : b0;
 }
 
-// Gradient of token t by one wave.  n: the tokens of its sequence that count; live, total:
-// sequences with such tokens, and all of those.  ADD: the counts are added from the blocks'.
+// u of sequence `seq` (its tokens that count: n > 0) in a wave's lanes.  live: sequences with such
+// tokens.  ADD: the counts are added from the blocks'.
 template <int EPL, int V, bool ADD>
-__device__ __forceinline__ void token_grad(const BalArgs& a, int t, int lane, float (&p)[EPL], const TokStat& ts, int n,
-                                           int live, long long total) {
-  float* out = a.dlogits + size_t(t) * a.E;
-  if (ts.seq < 0) {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) p[i] = 0.f;
-    store_row<EPL, V>(out, a.E, lane, p);
-    return;
-  }
+__device__ __forceinline__ void load_u(const BalArgs& a, int seq, int n, int live, int lane, float (&u)[EPL]) {
   const long long kn = static_cast<long long>(a.K) * n;
   const float scale = a.balance / (static_cast<float>(live) * static_cast<float>(kn) * static_cast<float>(n));
-  const float zl = a.z != 0.f ? 2.f * a.z / static_cast<float>(total) * ts.lse : 0.f;
-  float u[EPL], dot = 0.f;
   int b0 = 0, b1 = 1;
-  if (ADD) seq_blocks(a, ts.seq, b0, b1);
-  const int32_t* cnt = ADD ? a.part_c + (size_t(b0) + ts.seq) * a.E : a.load + size_t(ts.seq) * a.E;
+  if (ADD) seq_blocks(a, seq, b0, b1);
+  const int32_t* cnt = ADD ? a.part_c + (size_t(b0) + seq) * a.E : a.load + size_t(seq) * a.E;
 #pragma unroll
   for (int j = 0; j < EPL / V; ++j) {
     const int e = (j * 64 + lane) * V;
@@ -124,9 +130,24 @@ __device__ __forceinline__ void token_grad(const BalArgs& a, int t, int lane, fl
     for (int w = 0; w < V; ++w)
       u[j * V + w] = static_cast<float>(static_cast<long long>(a.E) * c[w] - kn) * scale;
   }
+}
+
+// Gradient of token t by one wave, p its logits.  total: all tokens that count.
+template <int EPL, int V>
+__device__ __forceinline__ void token_grad(const BalArgs& a, int t, int lane, float (&p)[EPL], const float (&u)[EPL],
+                                           const TokStat& ts, float total) {
+  float* out = a.dlogits + size_t(t) * a.E;
+  if (ts.seq < 0) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) p[i] = 0.f;
+    store_row<EPL, V>(out, a.E, lane, p);
+    return;
+  }
+  const float zl = a.z != 0.f ? 2.f * a.z / total * ts.lse : 0.f;
+  float dot = 0.f;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    p[i] = p[i] > -INFINITY ? exp_neg(p[i] - ts.m) * ts.rs : 0.f;
+    p[i] = exp_neg(p[i] - ts.m) * ts.rs;
     dot += p[i] * u[i];
   }
   dot = __ockl_wfred_add_f32(dot);
@@ -143,22 +164,35 @@ __global__ __launch_bounds__(WAVES * 64) void balance_tokens_kernel(BalArgs a) {
   __shared__ int32_t cnt[EPL * 64];
   __shared__ int wn[WAVES];
   __shared__ float wz[WAVES], wl[WAVES];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int T = a.T, E = a.E, K = a.K;
   const int waves = blockDim.x >> 6, threads = blockDim.x;
   const int t0 = blockIdx.x * a.tok, t1 = t0 + a.tok < T ? t0 + a.tok : T;
+  // bit l: token t0 + l is not masked (a workgroup has at most 64)
+  const unsigned long long marked = __ballot(t0 + lane < t1 && (!a.mask || a.mask[t0 + lane]));
   int s = 0;
-  if (!ONE) {  // the first sequence that ends behind t0
-    int hi = a.S;
-    while (s < hi) {
-      const int mid = (s + hi) >> 1;
-      if (seq_bound(a.off, mid + 1, T) > t0) hi = mid;
-      else s = mid + 1;
+  Bounds bounds;
+  if (!ONE) {  // the first sequence that ends behind t0 (S: none), 64 ends at a time
+    int last = a.S;
+    while (last - s > 62) {
+      const int step = (last - s + 63) >> 6, e = s + (lane + 1) * step;
+      const unsigned long long b = __ballot(seq_bound(a.off, e < last ? e : last, T) > t0);
+      if (!b) {
+        s = last;
+        break;
+      }
+      s += __builtin_ctzll(b) * step;
+      last = s + step - 1 < last ? s + step - 1 : last;
     }
+    bounds.hold(a.off, s, a.S, T, lane);
+    const unsigned long long b = __ballot(lane > 0 && s + lane <= a.S && bounds.held > t0);
+    s = b ? s + __builtin_ctzll(b) - 1 : a.S;
+  } else {
+    bounds.hold(a.off, 0, a.S, T, lane);
   }
   int done = t0;  // tokens before this one are dealt with
   for (; s < a.S; ++s) {
-    const int lo = seq_bound(a.off, s, T), up = seq_bound(a.off, s + 1, T);
+    const int lo = bounds.at(a.off, s, T), up = bounds.at(a.off, s + 1, T);
     if (!ONE && lo >= t1) break;
     const int first = lo > done ? lo : done, b = up < t1 ? up : t1;
     const int tokens = b > first ? b - first : 0;
@@ -172,24 +206,23 @@ __global__ __launch_bounds__(WAVES * 64) void balance_tokens_kernel(BalArgs a) {
     for (int i = 0; i < EPL; ++i) acc[i] = 0.f;
     int n = 0;
     float z = 0.f;
-    // the next token's row is on its way while this one's is worked on
+    // the next token's row and picks are on their way while this one's are worked on
     float nxt[EPL];
     bool take = false;
-    int t = first + wave;
-    if (t < b) {
-      take = !a.mask || a.mask[t];
-      if (take) load_row<EPL, V>(a.logits + size_t(t) * E, E, lane, -INFINITY, nxt);
-    }
+    int t = first + wave, npick = -1;
+    auto fetch = [&](int at) {
+      take = marked >> (at - t0) & 1;
+      if (!take) return;
+      load_row<EPL, V>(a.logits + size_t(at) * E, E, lane, -INFINITY, nxt);
+      if (lane < K) npick = a.idx[size_t(at) * K + lane];
+    };
+    if (t < b) fetch(t);
     for (; t < b; t += waves) {
       const bool now = take;
+      const int pick = lane < K ? npick : -1;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) v[i] = nxt[i];
-      int pick = -1;
-      if (now && lane < K) pick = a.idx[size_t(t) * K + lane];
-      if (t + waves < b) {
-        take = !a.mask || a.mask[t + waves];
-        if (take) load_row<EPL, V>(a.logits + size_t(t + waves) * E, E, lane, -INFINITY, nxt);
-      }
+      if (t + waves < b) fetch(t + waves);
       TokStat ts{0.f, 0.f, 0.f, -1};
       if (now) {
         const RowSum r = softmax_row<EPL>(v);
@@ -263,11 +296,14 @@ __global__ __launch_bounds__(WAVES * 64) void balance_tokens_kernel(BalArgs a) {
         total += n;
         live += n > 0;
       }
+      int have = -1;  // the sequence that u belongs to
+      float u[EPL];
       for (int t = wave; t < T; t += waves) {
         const TokStat ts = a.stat[t];
         float v[EPL];
         if (ts.seq >= 0) load_row<EPL, V>(a.logits + size_t(t) * E, E, lane, -INFINITY, v);
-        token_grad<EPL, V, false>(a, t, lane, v, ts, ts.seq >= 0 ? a.seq_n[ts.seq] : 0, live, total);
+        if (ts.seq >= 0 && ts.seq != have) load_u<EPL, V, false>(a, have = ts.seq, a.seq_n[ts.seq], live, lane, u);
+        token_grad<EPL, V>(a, t, lane, v, u, ts, static_cast<float>(total));
       }
     }
     write_losses<WAVES * 64>(a);
@@ -376,15 +412,19 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalArgs a) {
     return;
   }
   __shared__ int wt[4], wl[4], ns[FEW ? kFewSeqs : 1];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int t = (int(blockIdx.x) - 1) * a.grad_tok + wave;
   const int t1 = int(blockIdx.x) * a.grad_tok < a.T ? int(blockIdx.x) * a.grad_tok : a.T;
-  float nxt[EPL], v[EPL];
-  TokStat nts{0.f, 0.f, 0.f, -1};
-  if (t < t1) {
-    nts = a.stat[t];
-    if (nts.seq >= 0) load_row<EPL, V>(a.logits + size_t(t) * a.E, a.E, lane, -INFINITY, nxt);
-  }
+  // the wave's tokens t, t + 4, ..: lane l has the statistics of the l-th
+  TokStat held{0.f, 0.f, 0.f, -1};
+  if (t + 4 * lane < t1) held = a.stat[t + 4 * lane];
+  auto stat_of = [&](int l) {
+    auto f = [&](float x) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), l)); };
+    return TokStat{f(held.m), f(held.rs), f(held.lse), __builtin_amdgcn_readlane(held.seq, l)};
+  };
+  float nxt[EPL], v[EPL], u[EPL];
+  TokStat nts = stat_of(0);
+  if (nts.seq >= 0) load_row<EPL, V>(a.logits + size_t(t) * a.E, a.E, lane, -INFINITY, nxt);
   int total = 0, live = 0;  // tokens that count: at most T
   for (int s = tid; s < a.S; s += 256) {
     int n = 0;
@@ -406,24 +446,25 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalArgs a) {
   __syncthreads();
   total = wt[0] + wt[1] + wt[2] + wt[3];
   live = wl[0] + wl[1] + wl[2] + wl[3];
-  for (; t < t1; t += 4) {
+  int have = -1;  // the sequence that u belongs to
+  for (int l = 0; t < t1; t += 4) {
     const TokStat ts = nts;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) v[i] = nxt[i];
     if (t + 4 < t1) {
-      nts = a.stat[t + 4];
+      nts = stat_of(++l);
       if (nts.seq >= 0) load_row<EPL, V>(a.logits + size_t(t + 4) * a.E, a.E, lane, -INFINITY, nxt);
     }
-    const int n = ts.seq < 0 ? 0 : FEW ? ns[ts.seq] : a.seq_n[ts.seq];
-    token_grad<EPL, V, FEW>(a, t, lane, v, ts, n, live, total);
+    if (ts.seq >= 0 && ts.seq != have)
+      load_u<EPL, V, FEW>(a, have = ts.seq, FEW ? ns[ts.seq] : a.seq_n[ts.seq], live, lane, u);
+    token_grad<EPL, V>(a, t, lane, v, u, ts, static_cast<float>(total));
   }
 }
 
 template <int EPL, int V>
 static void launch_passes(const BalArgs& a, const BalPlan& p, hipStream_t st) {
   // most waves of a workgroup: LDS holds one row of sums for each, at most 64 KB in all
-  // (T = 16384, E = 768: 38.7 us with 8 waves and 32 tokens, 39.8 with 16 and 64, 41 with 8 and
-  // 64 or 4 and 16)
+  // (T = 16384, E = 768: 35.3 us with 8 waves and 32 tokens, 36.3 with 4 waves, 39 with 16)
   constexpr int WAVES = EPL <= 32 ? 8 : 4;
   if (p.one) {
     hipLaunchKernelGGL((balance_tokens_kernel<EPL, V, WAVES, true>), dim3(1), dim3(WAVES * 64), 0, st, a);
@@ -457,7 +498,8 @@ hipError_t launch_balance_loss(const lc_moe_shape& s, const BalPlan& p, void* ws
   a.K = s.K;
   a.n_eb = p.one ? 1 : p.n_eb;
   a.tok = p.tok;
-  // enough workgroups to fill the chip, then four tokens a wave
+  // enough workgroups to fill the chip, then four tokens a wave (T = 16384, E = 768: 35.3 us; two
+  // 36.5, eight 36.9)
   a.grad_tok = s.T < 8192 ? 4 : 16;
   a.balance = balance;
   a.z = z;

@@ -37,7 +37,7 @@ __device__ __forceinline__ void store_row(float* row, int E, int lane, const flo
 }
 
 // e^x for x <= 0 within 2 ulps: x log2(e) in two floats, the hardware's base-2 exponential
-// (1 ulp) of the first, and the second to first order.  Below 2^-126 it is 0.
+// (1 ulp) of the first, and the second to first order.  Below 2^-126, and of -infinity, it is 0.
 __device__ __forceinline__ float exp_neg(float x) {
   x = fmaxf(x, -150.f);
   const float t = x * 1.44269502f;
@@ -61,7 +61,7 @@ __device__ __forceinline__ RowSum softmax_row(float (&v)[EPL]) {
   const float top = m > -INFINITY ? m : 0.f;  // every v is -infinity else: e^v = 0
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    v[i] = v[i] > -INFINITY ? exp_neg(v[i] - top) : 0.f;
+    v[i] = exp_neg(v[i] - top);
     sum += v[i];
   }
   return RowSum{m, __ockl_wfred_add_f32(sum)};

@@ -118,6 +118,26 @@ def test_balance(kw, a, z):
         assert torch.equal(r[k], again[k]), k
 
 
+@pytest.mark.parametrize("T,S,kind", [(1500, 1500, "one"), (900, 4000, "sparse"), (900, 65535, "sparse"),
+                                      (2000, 63, "even"), (2000, 64, "even"), (2000, 129, "even"), (600, 300, "late")])
+def test_balance_many_sequences(T, S, kind):
+    """More sequences than a wave has lanes: of one token each, mostly empty ones, as many as
+    fill the lanes, and tokens in front of the first and behind the last."""
+    say(f"balance T={T} S={S} {kind}")
+    rng = np.random.default_rng(S)
+    E, K = 12, 3
+    lg = rng.standard_normal((T, E)).astype(np.float32)
+    idx = rng.integers(0, E, (T, K)).astype(np.int32)
+    if kind in ("one", "even"):
+        off = np.linspace(0, T, S + 1).astype(np.int32)
+    elif kind == "sparse":
+        off = np.sort(rng.choice(np.arange(0, T + 1, 7), S + 1)).astype(np.int32)
+    else:
+        off = np.linspace(400, 580, S + 1).astype(np.int32)
+    ref = reference(lg, idx, off, None, 0.5, float(np.float32(1e-3)))
+    check_balance(run_balance(lg, idx, off, None, 0.5, float(np.float32(1e-3))), ref, 0.5, float(np.float32(1e-3)), T)
+
+
 def test_balance_masked_rows_may_hold_anything():
     """NaN and infinities in rows that the mask or the offsets leave out, picks out of range,
     logits of -infinity and of the lowest value, a row of nothing but -infinity."""
