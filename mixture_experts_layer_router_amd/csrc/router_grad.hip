@@ -578,8 +578,20 @@ template <int NP, typename Tx>
 __device__ __forceinline__ void dx_few(const ProdArgs& p, const float* __restrict__ w, int E, unsigned block, float* sums) {
   const int n0 = block * 32;
   if (n0 >= p.N) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l32 = lane & 31, half = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = n0 + l32 < p.N ? n0 + l32 : n0;
+  // dx_add of the thread's 16 bytes of output (two of them for fp32), loaded beside the products:
+  // it may be dx itself, so behind them each piece would wait for the last one's store
+  constexpr int CH = 16 / sizeof(Tx), PIECES = 64 * 32 / CH / 256;
+  const Tx* add = static_cast<const Tx*>(p.add);
+  Tx* out = static_cast<Tx*>(p.c);
+  uint4 q[PIECES];
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const int at = i * 256 + tid, m = at / (32 / CH), c = n0 + at % (32 / CH) * CH;
+    q[i] = add && m < p.M && c < p.N ? *reinterpret_cast<const uint4*>(add + size_t(m) * p.N + c) : make_uint4(0, 0, 0, 0);
+  }
   const bf16_t* arow[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -592,33 +604,34 @@ __device__ __forceinline__ void dx_few(const ProdArgs& p, const float* __restric
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
   constexpr int B = NP == 2 ? 6 : 3;  // steps whose loads are in flight together
-  for (int k0 = wave * 16; k0 < p.Kdim; k0 += 64 * B) {
-    float wv[B][8];
-    bf16x8 fa[B][NP][2];
+  float wv[B][8];
+  bf16x8 fa[B][NP][2];
+  auto load = [&](int b, int k) {
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const int k = k0 + 64 * b < p.Kdim ? k0 + 64 * b : k0;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int e = k + 8 * half + q;
-        wv[b][q] = w[size_t(e < E ? e : E - 1) * p.N + n];  // dlogits' columns past E are zero
-      }
-#pragma unroll
-      for (int q = 0; q < NP; ++q)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) fa[b][q][i] = *reinterpret_cast<const bf16x8*>(arow[i] + q * p.plane_a + k);
+    for (int j = 0; j < 8; ++j) {
+      const int e = k + 8 * half + j;
+      wv[b][j] = w[size_t(e < E ? e : E - 1) * p.N + n];  // dlogits' columns past E are zero
     }
+#pragma unroll
+    for (int z = 0; z < NP; ++z)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) fa[b][z][i] = *reinterpret_cast<const bf16x8*>(arow[i] + z * p.plane_a + k);
+  };
+#pragma unroll
+  for (int b = 0; b < B; ++b)
+    if (wave * 16 + 64 * b < p.Kdim) load(b, wave * 16 + 64 * b);
+  for (int k0 = wave * 16; k0 < p.Kdim; k0 += 64 * B) {
 #pragma unroll
     for (int b = 0; b < B; ++b) {
       if (k0 + 64 * b >= p.Kdim) break;
       typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
       u16x8 h[NP];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
+      for (int j = 0; j < 8; ++j) {
         bf16_t c[3];
-        cut3(wv[b][q], c);
+        cut3(wv[b][j], c);
 #pragma unroll
-        for (int z = 0; z < NP; ++z) h[z][q] = c[z];
+        for (int z = 0; z < NP; ++z) h[z][j] = c[z];
       }
 #pragma unroll
       for (int qa = 0; qa < NP; ++qa)
@@ -627,6 +640,7 @@ __device__ __forceinline__ void dx_few(const ProdArgs& p, const float* __restric
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[b][qa][i], __builtin_bit_cast(bf16x8, h[qb]), acc[i], 0, 0, 0);
+      if (k0 + 64 * (b + B) < p.Kdim) load(b, k0 + 64 * (b + B));
     }
   }
   float(*s)[64][33] = reinterpret_cast<float(*)[64][33]>(sums);  // [4][64 rows][32 columns + 1]
@@ -635,19 +649,26 @@ __device__ __forceinline__ void dx_few(const ProdArgs& p, const float* __restric
 #pragma unroll
     for (int r = 0; r < 16; ++r) s[wave][i * 32 + 8 * (r >> 2) + 4 * half + (r & 3)][l32] = acc[i][r];
   __syncthreads();
-  const Tx* add = static_cast<const Tx*>(p.add);
-  Tx* out = static_cast<Tx*>(p.c);
-  for (int i = tid; i < 64 * 32; i += 256) {
-    const int m = i >> 5, c = i & 31;
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const int at = i * 256 + tid, m = at / (32 / CH), c = at % (32 / CH) * CH;
     if (m >= p.M || n0 + c >= p.N) continue;
-    float v = (s[0][m][c] + s[1][m][c]) + (s[2][m][c] + s[3][m][c]);
-    const size_t o = size_t(m) * p.N + n0 + c;
+    const uint32_t u[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+    float v[CH];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      v[j] = (s[0][m][c + j] + s[1][m][c + j]) + (s[2][m][c + j] + s[3][m][c + j]);
+      if constexpr (sizeof(Tx) == 2) v[j] += __uint_as_float(j & 1 ? u[j >> 1] & 0xFFFF0000u : u[j >> 1] << 16);
+      else v[j] += __uint_as_float(u[j]);
+    }
+    Tx* o = out + size_t(m) * p.N + n0 + c;
     if constexpr (sizeof(Tx) == 2) {
-      if (add) v += bf2f(add[o]);
-      out[o] = f2bf(v);
+      uint32_t w2[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w2[j] = f2bf(v[2 * j]) | (uint32_t(f2bf(v[2 * j + 1])) << 16);
+      *reinterpret_cast<uint4*>(o) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
     } else {
-      if (add) v += add[o];
-      out[o] = v;
+      *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
     }
   }
 }
