@@ -17,8 +17,9 @@
 // tiles, 0.95 on bf16 parts, 0.77 with dx from fp16 rows, 0.71 with two workgroups a CU and dx
 // through LDS, 0.66 with constant waits, dx_add loaded early and lane offsets kept.
 // Few tokens and narrow pools are bound by their launches and by a few memory latencies
-// each: T = 64, d = 6144, E = 768 takes 23 us (operands 6.5, products 18), T = 4096, d = 2048,
-// E = 96 takes 31 (6.6, 21.5, sum 4), fp32 T = 1777, d = 1028, E = 77 takes 25 (9, 14, 3).
+// each: T = 64, d = 6144, E = 768 takes 20.3 us (operands 6, products 15, of which each alone
+// would take 11), T = 4096, d = 2048, E = 96 takes 31 (6.6, 21.5, sum 4), fp32 T = 1777,
+// d = 1028, E = 77 takes 25 (9, 14, 3).
 //
 // Precision.  dW is an fp32 output: dlogits is cut into three bf16 parts (24 bits), the tokens
 // are bf16 already (or cut the same way), every product of parts is exact and the matrix cores
@@ -572,7 +573,9 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
 }
 
 // dx of at most 64 tokens: 32 columns a workgroup, every fourth 16-step of the reduction a
-// wave, the four sums added through LDS in wave order.  W_r is read as it lies, once, and cut
+// wave, the four sums added through LDS in wave order (T = 64, d = 6144, E = 768: 20.3 us for the
+// call; 22.4 with the six steps loaded anew when all are worked off, 22.9 with dx_add loaded at
+// the end).  W_r is read as it lies, once, and cut
 // into NP parts in registers: lane (l32, half) holds column n0 + l32 of rows 8 half + 0..7.
 template <int NP, typename Tx>
 __device__ __forceinline__ void dx_few(const ProdArgs& p, const float* __restrict__ w, int E, unsigned block, float* sums) {
@@ -684,7 +687,7 @@ struct ProductsArgs {
 };
 
 template <int FORM, bool BF>
-__global__ __launch_bounds__(256, 2) void products_kernel(ProductsArgs a) {
+__global__ __launch_bounds__(256, BF ? 2 : 1) void products_kernel(ProductsArgs a) {
   typedef typename std::conditional<BF, bf16_t, float>::type Tx;
   constexpr int X = BF ? 1 : 3, W = BF ? 2 : 3;  // parts of the tokens; of W_r (and dlogits for dx)
   // ring: big 2 x 40 KB for dW, 3 x 24 KB for dx; else 2 x 32 KB (fp32 layers 2 x 48 KB)
