@@ -130,8 +130,7 @@ lc_moe_status lc_moe_gate_backward(const lc_moe_shape* shape, const void* x, con
  *   dx           [T][d] dtype (out), or NULL: not computed
  *   dw_router    [N+Z][d] fp32 (out), or NULL: not computed
  *   dlogits      [T][N+Z] fp32 (out), or NULL; may be dlogits_aux itself
- * Reads T, d, N, Z, K and dtype of shape (LC_MOE_E_SHAPE also for fp32 layers of about 1.7e10
- * token elements and more).  Outputs and inputs may overlap only as said. */
+ * Reads T, d, N, Z, K and dtype of shape.  Outputs and inputs may overlap only as said. */
 size_t lc_moe_router_backward_workspace_size(const lc_moe_shape* shape);
 lc_moe_status lc_moe_router_backward(const lc_moe_shape* shape, const void* x,
                                      const float* w_router, const float* logits,

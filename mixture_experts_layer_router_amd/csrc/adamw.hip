@@ -133,16 +133,11 @@ __device__ __forceinline__ void load4(const void* p, bool bf, int64_t i, int cnt
     }
   }
 }
-// Two values to bf16, nearest even (v_cvt_pk_bf16_f32).
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
-}
 __device__ __forceinline__ void store4(void* p, bool bf, int64_t i, int cnt, const float* o) {
   if (bf) {
     bf16_t* q = static_cast<bf16_t*>(p) + i;
     if (cnt >= 4) {
-      *reinterpret_cast<uint2*>(q) = make_uint2(pack2(o[0], o[1]), pack2(o[2], o[3]));
+      *reinterpret_cast<uint2*>(q) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
     } else {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -179,7 +174,7 @@ template <int GAP>
 __device__ __forceinline__ void store8(void* p, bool bf, int64_t i, const int (&cnt)[2], const float (&o)[8]) {
   if (GAP == 4 && bf && cnt[1] == 4) {
     *reinterpret_cast<uint4*>(static_cast<bf16_t*>(p) + i) =
-        make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
+        make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
     return;
   }
   store4(p, bf, i, cnt[0], o);

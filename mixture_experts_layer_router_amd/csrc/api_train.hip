@@ -79,8 +79,7 @@ lc_moe_status lc_moe_gate_backward(const lc_moe_shape* shape, const void* x, con
 
 size_t lc_moe_router_backward_workspace_size(const lc_moe_shape* shape) {
   if (check_shape(shape) != LC_MOE_OK) return 0;
-  const RouterBwPlan p = plan_router_backward(*shape);
-  return router_grid_fits(*shape, p) ? p.total : 0;
+  return plan_router_backward(*shape).total;
 }
 
 lc_moe_status lc_moe_router_backward(const lc_moe_shape* shape, const void* x, const float* w_router,
@@ -89,7 +88,6 @@ lc_moe_status lc_moe_router_backward(const lc_moe_shape* shape, const void* x, c
                                      float* dlogits, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   LCM_CHECK(check_shape(shape));
   const RouterBwPlan p = plan_router_backward(*shape);
-  if (!router_grid_fits(*shape, p)) return LC_MOE_E_SHAPE;
   LCM_CHECK(check_ptr(x, !dw_router));
   LCM_CHECK(check_ptr(w_router, !dx));
   LCM_CHECK(check_ptr(dgate, true));

@@ -3,8 +3,7 @@
 // include/lc_moe_train.h).
 //
 //   weight_f16_kernel  big layers of bf16 tokens: W_r as fp16, scaled row by row
-//   operands_kernel    dlogits, one wave per token, cut into the products' operands; W_r and
-//                      fp32 tokens cut into parts
+//   operands_kernel    dlogits, one wave per token, cut into the products' operands
 //   products_kernel    dx = dlogits W_r (+ dx_add) and dW = dlogits^T x on the matrix cores, side
 //                      by side in one grid
 //   sum_parts_kernel   the pieces of dW's reduction over the tokens, added in order
@@ -17,9 +16,9 @@
 // tiles, 0.95 on bf16 parts, 0.77 with dx from fp16 rows, 0.71 with two workgroups a CU and dx
 // through LDS, 0.66 with constant waits, dx_add loaded early and lane offsets kept.
 // Few tokens and narrow pools are bound by their launches and by a few memory latencies
-// each: T = 64, d = 6144, E = 768 takes 20.3 us (operands 6, products 15, of which each alone
-// would take 11), T = 4096, d = 2048, E = 96 takes 31 (6.6, 21.5, sum 4), fp32 T = 1777,
-// d = 1028, E = 77 takes 25 (9, 14, 3).
+// each: T = 64, d = 6144, E = 768 takes 19.6 us (operands 6, products 14, of which each alone
+// would take 11), T = 4096, d = 2048, E = 96 takes 32 (6.5, 22, sum 4), fp32 T = 1777,
+// d = 1028, E = 77 takes 20.
 //
 // Precision.  dW is an fp32 output: dlogits is cut into three bf16 parts (24 bits), the tokens
 // are bf16 already (or cut the same way), every product of parts is exact and the matrix cores
@@ -48,6 +47,26 @@ __device__ __forceinline__ void cut3(float v, bf16_t (&o)[3]) {
   o[2] = f2bf(r1 - bf2f(o[1]));
 }
 
+// The same of 8 values, NP parts, as operands of the matrix cores.
+template <int NP>
+__device__ __forceinline__ void cut8(const float (&v)[8], bf16x8 (&o)[NP]) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  u32x4 u[NP];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float a = v[2 * j], b = v[2 * j + 1];
+#pragma unroll
+    for (int z = 0; z < NP; ++z) {
+      const uint32_t w = pack_bf16(a, b);
+      u[z][j] = w;
+      a -= __uint_as_float(w << 16);
+      b -= __uint_as_float(w & 0xFFFF0000u);
+    }
+  }
+#pragma unroll
+  for (int z = 0; z < NP; ++z) o[z] = __builtin_bit_cast(bf16x8, u[z]);
+}
+
 __device__ __forceinline__ bf16_t f16_bits(float v) { return __builtin_bit_cast(bf16_t, static_cast<_Float16>(v)); }
 
 // Exponent of the largest magnitude, so that 2^(14 - it) brings it into [2^14, 2^15), well inside
@@ -57,7 +76,7 @@ __device__ __forceinline__ int top_exp(float amax) { return amax > 0.f ? ilogbf(
 // W_r row by row as fp16: w16[e] = 2^(14 - x) w[e], wexp[e] = x.  One workgroup per row; rows
 // from E on are zeros.
 __global__ __launch_bounds__(256) void weight_f16_kernel(const float* __restrict__ w, bf16_t* __restrict__ w16,
-                                                         int32_t* __restrict__ wexp, int E, int d, int dp) {
+                                                         int32_t* __restrict__ wexp, int E, int d) {
   __shared__ float wm[4];
   const int e = blockIdx.x, tid = threadIdx.x;
   const float* row = w + size_t(e) * d;
@@ -73,10 +92,10 @@ __global__ __launch_bounds__(256) void weight_f16_kernel(const float* __restrict
   __syncthreads();
   const int x = top_exp(fmaxf(fmaxf(wm[0], wm[1]), fmaxf(wm[2], wm[3])));
   if (tid == 0) wexp[e] = x;
-  for (int c = tid * 4; c < dp; c += 1024) {
+  for (int c = tid * 4; c < d; c += 1024) {
     float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (e < E && c < d) q = *reinterpret_cast<const float4*>(row + c);
-    *reinterpret_cast<uint2*>(w16 + size_t(e) * dp + c) =
+    if (e < E) q = *reinterpret_cast<const float4*>(row + c);
+    *reinterpret_cast<uint2*>(w16 + size_t(e) * d + c) =
         make_uint2(f16_bits(ldexpf(q.x, 14 - x)) | (uint32_t(f16_bits(ldexpf(q.y, 14 - x))) << 16),
                    f16_bits(ldexpf(q.z, 14 - x)) | (uint32_t(f16_bits(ldexpf(q.w, 14 - x))) << 16));
   }
@@ -93,51 +112,14 @@ struct OperandArgs {
   float* rscale;     // [T] 2^(x - 28)
   const int32_t* wexp;
   int T, E, K, Ep;
-  // matrices [R][C] fp32 to cut into np bf16 planes [Rp][Cp], zeros past R and C
-  struct Matrix {
-    const float* src;
-    bf16_t* dst;
-    int R, C, Cp, np;
-    size_t n4;       // Rp Cp / 4
-    unsigned blocks;
-  } mat[2];
-  unsigned dl_blocks;
   uint4* zero;       // 16 zero bytes: the source of operand chunks past the data
 };
 
-__device__ __forceinline__ void cut_matrix(const OperandArgs::Matrix& m, unsigned block) {
-  const size_t i = size_t(block) * 256 + threadIdx.x;
-  if (i >= m.n4) return;
-  const unsigned c4 = m.Cp / 4;
-  const size_t r = m.n4 >> 32 ? i / c4 : unsigned(i) / c4;
-  const int c = int(i - r * c4) * 4;
-  const float4 v = r < size_t(m.R) && c < m.C ? *reinterpret_cast<const float4*>(m.src + r * m.C + c)
-                                              : make_float4(0.f, 0.f, 0.f, 0.f);
-  bf16_t h[4][3];
-  cut3(v.x, h[0]);
-  cut3(v.y, h[1]);
-  cut3(v.z, h[2]);
-  cut3(v.w, h[3]);
-#pragma unroll
-  for (int q = 0; q < 3; ++q) {
-    if (q >= m.np) break;
-    *reinterpret_cast<uint2*>(m.dst + q * m.n4 * 4 + i * 4) =
-        make_uint2(h[0][q] | (uint32_t(h[1][q]) << 16), h[2][q] | (uint32_t(h[3][q]) << 16));
-  }
-}
-
-// Workgroups 0 .. dl_blocks-1: dlogits of four tokens, one per wave, the row in its registers as
-// in logit_row.h; the picks' gradients are added in pick order by the lane that holds the
-// expert.  The others cut matrices, 4 columns a thread.
+// dlogits of four tokens, one per wave, the row in its registers as in logit_row.h; the picks'
+// gradients are added in pick order by the lane that holds the expert.
 template <int EPL, int V>
 __global__ __launch_bounds__(256) void operands_kernel(OperandArgs a) {
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.zero = make_uint4(0, 0, 0, 0);
-  if (blockIdx.x >= a.dl_blocks) {
-    const unsigned b = blockIdx.x - a.dl_blocks;
-    if (b < a.mat[0].blocks) cut_matrix(a.mat[0], b);
-    else cut_matrix(a.mat[1], b - a.mat[0].blocks);
-    return;
-  }
   constexpr int J = EPL / V;  // runs of 64 V experts
   const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int E = a.E, K = a.K;
@@ -241,40 +223,50 @@ __global__ __launch_bounds__(256) void operands_kernel(OperandArgs a) {
 // v_mfma_f32_32x32x16.  A stage holds BK reduction steps of NA parts of A and NB parts of B, so
 // a loaded part serves every product it takes part in: with the pairs a + b < max(NA, NB)
 // (h h, h m, m h of two parts each; h x, m x, l x of three and one; the six largest of three
-// and three) the NA + NB operand tiles of a stage carry 1, 3 or 6 products.
+// and three) the operand tiles of a stage carry 1, 3 or 6 products.
 //   DX: A(m, k) = dlogits, row m, K-contiguous; B(k, n) = W_r, row k.
 //   DW: A(m, k) = dlogits, row k (a token), M-contiguous; B(k, n) = tokens, row k.
+// CUT: B is fp32 (W_r; fp32 tokens) and lies in LDS as such; a wave cuts its fragments into the
+// NB parts in registers.  (Parts cut by a launch before take 6 bytes a value, so 96 KB of LDS and
+// one workgroup a CU, and a pass over x and W_r: fp32 T = 4096, d = 2048, E = 96 took 69 us, now 51;
+// T = 4096, d = 2800, E = 384 184, now 144.  bf16 T = 4096, d = 2048, E = 96, whose W_r is small,
+// took 31.3, now 32.2.)
 // Tile BM x BN, 64 x (BN / 2) outputs per wave, BM / 32 waves, a ring of NST stages in LDS
 // filled by direct global->LDS loads.  Operands whose output index is contiguous lie in LDS
 // as in memory ([BK][columns]) and are read by the transposing LDS read; 16-byte chunk c of
 // row r sits in the 32-byte granule (c / 2) ^ 2 (r % 4), which spreads the four rows of a
-// read over the banks.  K-contiguous rows are 64 bytes, chunk c in slot c ^ swz4(r).
+// read over the banks; fp32 chunk c of row r sits in c ^ 8 (r / 8 % 2), so that the two halves of
+// a wave, 8 rows apart, read different banks.  K-contiguous rows are 64 bytes, chunk c in slot
+// c ^ swz4(r).
 // ---------------------------------------------------------------------------------------
 struct ProdArgs {
   const bf16_t* a;  // [NA][T][Ep] (or its fp16 form)
-  const bf16_t* b;  // DX: [NB][Ep][ldb]; DW: [NB][T][ldb]
-  size_t plane_a, plane_b;
+  const void* b;    // DX: [krows][ldb]; DW: [T][ldb]
+  size_t plane_a;
   const bf16_t* zero;
   const void* add;
   void* c;
   const float* rscale;  // fp16: units of the rows' sums
   int M, N, Kdim, lda, ldb;
+  int krows;            // rows of B: the reduction's steps behind them have zeros in A
   int chunk;            // reduction steps of a piece (a multiple of 32)
   int n_mt, n_nt, splits;
 };
 
-template <bool DX, bool F16, int BM, int BN, int NA, int NB, int BK, int NST, typename Tc>
+template <bool DX, bool F16, bool CUT, int BM, int BN, int NA, int NB, int BK, int NST, typename Tc>
 __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, unsigned char* smem) {
   constexpr int WAVES = BM / 32, WN = 2, WC = BN / WN;  // wave tile: 64 x WC
   constexpr int NBL = WC / 32;                          // 32-wide column blocks of a wave
-  constexpr int A_OP = BM * BK * 2, B_OP = BN * BK * 2;  // bytes of one part in a stage
-  constexpr int STAGE = NA * A_OP + NB * B_OP;
+  constexpr int EB = CUT ? 4 : 2, CC = 16 / EB;            // bytes of an element of B, columns of a chunk
+  constexpr int A_OP = BM * BK * 2, B_OP = BN * BK * EB;  // bytes of A's parts (each) and of B in a stage
+  constexpr int STAGE = NA * A_OP + B_OP;
   constexpr int NP = NA > NB ? NA : NB;
-  constexpr int LA = A_OP / 1024 / WAVES, LB = B_OP / 1024 / WAVES;  // direct loads of a wave per part
-  constexpr int LOADS = NA * LA + NB * LB;                           // and per stage
+  constexpr int LA = A_OP / 1024 / WAVES, LB = B_OP / 1024 / WAVES;  // direct loads of a wave
+  constexpr int LOADS = NA * LA + LB;                                // and per stage
   static_assert(A_OP % (1024 * WAVES) == 0 && B_OP % (1024 * WAVES) == 0, "whole loads");
   static_assert(!DX || BK == 32, "K-contiguous rows are staged 64 bytes at a time");
   static_assert(NBL == 2 || NBL == 4, "wave tiles of 64 or 128 columns");
+  static_assert(CUT || NB == 1, "B comes in parts only if it is cut here");
 
   // unit: pieces of the reduction, in them groups of 8 M-tiles, in a group column tiles, in them
   // its M-tiles; each XCD takes a contiguous eighth, so workgroups side by side share operand
@@ -291,17 +283,27 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
   const int m0 = (grp * 8 + r0 % gm) * BM, n0 = (r0 / gm) * BN;
   const int kbeg = sp * p.chunk, kend = kbeg + p.chunk < p.Kdim ? kbeg + p.chunk : p.Kdim;
   const int nk = (kend - kbeg + BK - 1) / BK;
+  const int krows = kend < p.krows ? kend : p.krows;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
 
-  // A wave's load i of an operand with contiguous columns (BC of them) fills bytes
+  // A wave's load i of an operand with contiguous columns (BC of 2 bytes) fills bytes
   // 1024 (wave + WAVES i) of its part: 512 / BC rows of 2 BC bytes.
   auto col_place = [&](int BC, int i, int& kr, int& ch) {  // the lane's row and 16-byte chunk
     const int rpl = 512 / BC, cpr = BC / 8;  // rows of a load, chunks of a row
     const int sl = lane % cpr;
     kr = rpl * (wave + WAVES * i) + lane / cpr;
     ch = 2 * ((sl >> 1) ^ (2 * (kr & 3))) + (sl & 1);
+  };
+  auto b_place = [&](int i, int& kr, int& ch) {
+    if constexpr (CUT) {
+      constexpr int RPL = 256 / BN, CPR = BN / 4;
+      kr = RPL * (wave + WAVES * i) + lane / CPR;
+      ch = (lane % CPR) ^ (8 * (kr >> 3 & 1));
+    } else {
+      col_place(BN, i, kr, ch);
+    }
   };
   // Whole stages: the lane's byte offset from the stage's first element does not change, so a
   // load is a scalar base and that offset.  Columns past the operand repeat a valid column and
@@ -321,17 +323,17 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
 #pragma unroll
   for (int i = 0; i < LB; ++i) {
     int kr, ch;
-    col_place(BN, i, kr, ch);
-    off_b[i] = uint32_t(kr) * p.ldb * 2 + (n0 + ch * 8 < p.ldb ? ch * 16 : 0);
+    b_place(i, kr, ch);
+    off_b[i] = uint32_t(kr) * p.ldb * EB + (n0 + ch * CC < p.ldb ? ch * 16 : 0);
   }
-  const bool near = p.ldb < (1 << 25);  // 32 rows within 2^32 bytes
+  const bool near = p.ldb < (1 << 24);  // 32 rows within 2^32 bytes
   auto issue = [&](int kt) {
     unsigned char* st = smem + (kt % NST) * STAGE;
     unsigned char* sb = st + NA * A_OP;
     const int k0 = kbeg + kt * BK;
     const bf16_t* a0 = DX ? p.a + size_t(m0) * p.lda + k0 : p.a + size_t(k0) * p.lda + m0;
-    const bf16_t* b0 = p.b + size_t(k0) * p.ldb + n0;
-    if (near && k0 + BK <= kend) {
+    const char* b0 = static_cast<const char*>(p.b) + (size_t(k0) * p.ldb + n0) * EB;
+    if (near && k0 + BK <= krows) {
 #pragma unroll
       for (int q = 0; q < NA; ++q) {
         const char* g = reinterpret_cast<const char*>(a0 + q * p.plane_a);
@@ -339,14 +341,10 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
         for (int i = 0; i < LA; ++i) dma16(g + off_a[i], st + q * A_OP + (wave + WAVES * i) * 1024);
       }
 #pragma unroll
-      for (int q = 0; q < NB; ++q) {
-        const char* g = reinterpret_cast<const char*>(b0 + q * p.plane_b);
-#pragma unroll
-        for (int i = 0; i < LB; ++i) dma16(g + off_b[i], sb + q * B_OP + (wave + WAVES * i) * 1024);
-      }
+      for (int i = 0; i < LB; ++i) dma16(b0 + off_b[i], sb + (wave + WAVES * i) * 1024);
       return;
     }
-    // a piece's last, partial stage (the tokens of dW): rows past its end are zeros
+    // a piece's last, partial stage: rows past its end (the tokens of dW, W_r's last) are zeros
     for (int q = 0; q < NA; ++q)
       for (int i = 0; i < LA; ++i) {
         const bf16_t* g;
@@ -360,13 +358,12 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
         }
         dma16(g, st + q * A_OP + (wave + WAVES * i) * 1024);
       }
-    for (int q = 0; q < NB; ++q)
-      for (int i = 0; i < LB; ++i) {
-        int kr, ch;
-        col_place(BN, i, kr, ch);
-        const bool in = k0 + kr < kend && n0 + ch * 8 < p.ldb;
-        dma16(in ? b0 + q * p.plane_b + size_t(kr) * p.ldb + ch * 8 : p.zero, sb + q * B_OP + (wave + WAVES * i) * 1024);
-      }
+    for (int i = 0; i < LB; ++i) {
+      int kr, ch;
+      b_place(i, kr, ch);
+      const bool in = k0 + kr < krows && n0 + ch * CC < p.ldb;
+      dma16(in ? b0 + size_t(kr) * p.ldb * EB + ch * 16 : reinterpret_cast<const char*>(p.zero), sb + (wave + WAVES * i) * 1024);
+    }
   };
 
   const int l32 = lane & 31, khalf = lane >> 5;
@@ -419,6 +416,18 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
     if (kt > 0 && kt + NST - 1 < nk) issue(kt + NST - 1);  // into stage kt - 1's slot
     const unsigned char* st = smem + (kt % NST) * STAGE;
     const unsigned char* sb = st + NA * A_OP;
+    float bv[CUT ? BK / 16 : 1][NBL][8];  // the stage's fp32 values, read before any is waited for
+    if constexpr (CUT) {
+#pragma unroll
+      for (int ks = 0; ks < BK; ks += 16)
+#pragma unroll
+        for (int j = 0; j < NBL; ++j) {
+          const int c = wn * WC + 32 * j + l32;
+          const float* f = reinterpret_cast<const float*>(sb + (ks + 8 * khalf) * (BN * 4) + (((c >> 2) ^ (8 * khalf)) << 4)) + (c & 3);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) bv[ks / 16][j][q] = f[q * BN];
+        }
+    }
 #pragma unroll
     for (int ks = 0; ks < BK; ks += 16) {
       bf16x8 fa[NA][2], fb[NB][NBL];
@@ -471,17 +480,22 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
           tr4(std::integral_constant<int, BM * 2>{}, tr_addr(st + q * A_OP, BM * 2, wm * 64, ks),
               tr_addr(st + q * A_OP, BM * 2, wm * 64 + 32, ks), fa[q][0], fa[q][1]);
       }
+      if constexpr (CUT) {
 #pragma unroll
-      for (int q = 0; q < NB; ++q) {
-        if constexpr (NBL == 4) {
-          uint32_t ad[4];
+        for (int j = 0; j < NBL; ++j) {
+          bf16x8 h[NB];
+          cut8<NB>(bv[ks / 16][j], h);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) ad[j] = tr_addr(sb + q * B_OP, BN * 2, wn * WC + 32 * j, ks);
-          tr8(std::integral_constant<int, BN * 2>{}, ad, fb[q]);
-        } else {
-          tr4(std::integral_constant<int, BN * 2>{}, tr_addr(sb + q * B_OP, BN * 2, wn * WC, ks),
-              tr_addr(sb + q * B_OP, BN * 2, wn * WC + 32, ks), fb[q][0], fb[q][1]);
+          for (int q = 0; q < NB; ++q) fb[q][j] = h[q];
         }
+      } else if constexpr (NBL == 4) {
+        uint32_t ad[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ad[j] = tr_addr(sb, BN * 2, wn * WC + 32 * j, ks);
+        tr8(std::integral_constant<int, BN * 2>{}, ad, fb[0]);
+      } else {
+        tr4(std::integral_constant<int, BN * 2>{}, tr_addr(sb, BN * 2, wn * WC, ks),
+            tr_addr(sb, BN * 2, wn * WC + 32, ks), fb[0][0], fb[0][1]);
       }
 #pragma unroll
       for (int qa = 0; qa < NA; ++qa)
@@ -627,22 +641,15 @@ __device__ __forceinline__ void dx_few(const ProdArgs& p, const float* __restric
 #pragma unroll
     for (int b = 0; b < B; ++b) {
       if (k0 + 64 * b >= p.Kdim) break;
-      typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
-      u16x8 h[NP];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        bf16_t c[3];
-        cut3(wv[b][j], c);
-#pragma unroll
-        for (int z = 0; z < NP; ++z) h[z][j] = c[z];
-      }
+      bf16x8 h[NP];
+      cut8<NP>(wv[b], h);
 #pragma unroll
       for (int qa = 0; qa < NP; ++qa)
 #pragma unroll
         for (int qb = 0; qb + qa < NP; ++qb)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[b][qa][i], __builtin_bit_cast(bf16x8, h[qb]), acc[i], 0, 0, 0);
+            acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[b][qa][i], h[qb], acc[i], 0, 0, 0);
       if (k0 + 64 * (b + B) < p.Kdim) load(b, k0 + 64 * (b + B));
     }
   }
@@ -687,20 +694,20 @@ struct ProductsArgs {
 };
 
 template <int FORM, bool BF>
-__global__ __launch_bounds__(256, BF ? 2 : 1) void products_kernel(ProductsArgs a) {
+__global__ __launch_bounds__(256, 2) void products_kernel(ProductsArgs a) {
   typedef typename std::conditional<BF, bf16_t, float>::type Tx;
   constexpr int X = BF ? 1 : 3, W = BF ? 2 : 3;  // parts of the tokens; of W_r (and dlogits for dx)
-  // ring: big 2 x 40 KB for dW, 3 x 24 KB for dx; else 2 x 32 KB (fp32 layers 2 x 48 KB)
-  constexpr int LDS = FORM == kRbBig ? 81920 : BF ? 65536 : 98304;
+  // ring: big 2 x 40 KB for dW, 3 x 24 KB for dx; else 2 x 32 KB (fp32 layers 2 x 40 KB)
+  constexpr int LDS = FORM == kRbBig || !BF ? 81920 : 65536;
   __shared__ __attribute__((aligned(1024))) unsigned char smem[LDS];
   if (blockIdx.x < a.dw_blocks) {
-    if constexpr (FORM == kRbBig) product_tile<false, false, 128, 256, 3, 1, 32, 2, float>(a.dw, blockIdx.x, smem);
-    else product_tile<false, false, 128, 128, 3, X, 32, 2, float>(a.dw, blockIdx.x, smem);
+    if constexpr (FORM == kRbBig) product_tile<false, false, false, 128, 256, 3, 1, 32, 2, float>(a.dw, blockIdx.x, smem);
+    else product_tile<false, false, !BF, 128, 128, 3, X, 32, 2, float>(a.dw, blockIdx.x, smem);
   } else {
     const unsigned b = blockIdx.x - a.dw_blocks;
     if constexpr (FORM == kRbFew) dx_few<W, Tx>(a.dx, a.w, a.E, b, reinterpret_cast<float*>(smem));
-    else if constexpr (FORM == kRbSmall) product_tile<true, false, 128, 128, W, W, 32, 2, Tx>(a.dx, b, smem);
-    else product_tile<true, true, 128, 256, 1, 1, 32, 3, Tx>(a.dx, b, smem);
+    else if constexpr (FORM == kRbSmall) product_tile<true, false, true, 128, 128, W, W, 32, 2, Tx>(a.dx, b, smem);
+    else product_tile<true, true, false, 128, 256, 1, 1, 32, 3, Tx>(a.dx, b, smem);
   }
 }
 
@@ -747,7 +754,6 @@ hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, 
   const bool bf = s.dtype == LC_MOE_BF16, f16 = p.form == kRbBig;
   char* w = static_cast<char*>(ws);
   bf16_t* wp = reinterpret_cast<bf16_t*>(w + p.wp);
-  bf16_t* xp = reinterpret_cast<bf16_t*>(w + p.xp);
   OperandArgs o{};
   o.logits = logits;
   o.idx = idx;
@@ -760,27 +766,14 @@ hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, 
   o.E = E;
   o.K = s.K;
   o.Ep = p.Ep;
-  o.dl_blocks = unsigned((s.T + 3) / 4);
   if (dx && f16) {
     o.dl16 = reinterpret_cast<bf16_t*>(w + p.dl16);
     o.rscale = reinterpret_cast<float*>(w + p.rscale);
     int32_t* wexp = reinterpret_cast<int32_t*>(w + p.wexp);
     o.wexp = wexp;
-    hipLaunchKernelGGL(weight_f16_kernel, dim3(p.Ep), dim3(256), 0, st, w_router, wp, wexp, E, s.d, p.dp);
+    hipLaunchKernelGGL(weight_f16_kernel, dim3(p.Ep), dim3(256), 0, st, w_router, wp, wexp, E, s.d);
   }
-  auto matrix = [&](int i, const float* src, bf16_t* dst, int R, int Rp, int np) {
-    o.mat[i].src = src;
-    o.mat[i].dst = dst;
-    o.mat[i].R = R;
-    o.mat[i].C = s.d;
-    o.mat[i].Cp = p.dp;
-    o.mat[i].np = np;
-    o.mat[i].n4 = size_t(Rp) * p.dp / 4;
-    o.mat[i].blocks = unsigned((o.mat[i].n4 + 255) / 256);
-  };
-  if (dx && !f16 && p.form != kRbFew) matrix(0, w_router, wp, E, p.Ep, bf ? 2 : 3);
-  if (dw && !bf) matrix(1, static_cast<const float*>(x), xp, s.T, s.T, 3);
-  const dim3 grid(o.dl_blocks + o.mat[0].blocks + o.mat[1].blocks);
+  const dim3 grid(unsigned((s.T + 3) / 4));
 #define LCM_DL(n, v) hipLaunchKernelGGL((operands_kernel<n, v>), grid, dim3(256), 0, st, o)
   if (E % 4 == 0) {
     if (epl <= 4) LCM_DL(4, 4);
@@ -803,14 +796,14 @@ hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, 
   a.E = E;
   ProdArgs q{};
   q.lda = p.Ep;
-  q.ldb = p.dp;
+  q.ldb = s.d;
   q.zero = reinterpret_cast<const bf16_t*>(o.zero);
   q.N = s.d;
   a.dx = a.dw = q;
   a.dx.a = f16 ? o.dl16 : o.parts;
   a.dx.plane_a = size_t(s.T) * p.Ep;
-  a.dx.b = wp;
-  a.dx.plane_b = size_t(p.Ep) * p.dp;
+  a.dx.b = f16 ? static_cast<const void*>(wp) : w_router;
+  a.dx.krows = f16 ? p.Ep : E;
   a.dx.rscale = o.rscale;
   a.dx.M = s.T;
   a.dx.Kdim = a.dx.chunk = p.Ep;
@@ -819,8 +812,8 @@ hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, 
   a.dx.c = dx;
   a.dw.a = o.parts;
   a.dw.plane_a = size_t(s.T) * p.Ep;
-  a.dw.b = bf ? static_cast<const bf16_t*>(x) : xp;
-  a.dw.plane_b = size_t(s.T) * p.dp;
+  a.dw.b = x;
+  a.dw.krows = s.T;
   a.dw.M = E;
   a.dw.Kdim = s.T;
   a.dw.chunk = p.chunk;

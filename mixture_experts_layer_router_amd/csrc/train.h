@@ -57,13 +57,13 @@ hipError_t launch_gate_backward(const lc_moe_shape& s, const void* x, const void
 // ---- router backward -----------------------------------------------------------------
 // The two products run on the matrix cores, their fp32 operands cut into parts (router_grad.hip).
 //   few    at most 64 tokens: dx straight from the fp32 weight
-//   small  128 x 128 tiles, operands as bf16 parts
+//   small  128 x 128 tiles, dlogits as bf16 parts, fp32 W_r and tokens cut in registers
 //   big    bf16 layers: 128 x 256 tiles, dx from scaled fp16
-// Ep and dp: E and d rounded up to whole operand rows (32 experts; 16 bytes).
+// Ep: E rounded up to whole operand rows (32 experts).
 enum RbForm { kRbFew, kRbSmall, kRbBig };
 struct RouterBwPlan {
-  size_t dl, dl16, rscale, wp, wexp, xp, part, zero, total;
-  int Ep, dp;
+  size_t dl, dl16, rscale, wp, wexp, part, zero, total;
+  int Ep;
   RbForm form;
   int splits, chunk;  // dW: pieces of the reduction over the tokens, tokens of each (x 32)
 };
@@ -72,7 +72,6 @@ inline RouterBwPlan plan_router_backward(const lc_moe_shape& s) {
   const size_t T = s.T, E = size_t(s.N) + s.Z;
   const bool bf = s.dtype == LC_MOE_BF16;
   p.Ep = int((E + 31) / 32 * 32);
-  p.dp = (s.d + 7) / 8 * 8;
   auto tiles = [](size_t m, size_t n, size_t bm, size_t bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
   // wide tiles where they fill the chip one and a half times (T = 8192, d = 6144, E = 128: 117 us
   // against 135 with the small ones; T = 4096, d = 2048, E = 96, 256 tiles: 35 against 32)
@@ -92,25 +91,23 @@ inline RouterBwPlan plan_router_backward(const lc_moe_shape& s) {
   p.dl = take(3 * T * p.Ep * 2);
   p.dl16 = take(big ? T * p.Ep * 2 : 0);
   p.rscale = take(big ? T * 4 : 0);
-  p.wp = take(p.form == kRbFew ? 0 : size_t(big ? 1 : bf ? 2 : 3) * p.Ep * p.dp * 2);
+  p.wp = take(big ? size_t(p.Ep) * s.d * 2 : 0);
   p.wexp = take(big ? size_t(p.Ep) * 4 : 0);
-  p.xp = take(bf ? 0 : 3 * T * p.dp * 2);
   p.part = take(p.splits > 1 ? size_t(p.splits) * E * s.d * 4 : 0);
   p.zero = take(16);
   p.total = o;
   return p;
 }
-// operands_kernel's grid (four tokens a workgroup, then 1024 elements of W_r and of fp32
-// tokens a workgroup) within 2^32 - 1 work-items.
-inline bool router_grid_fits(const lc_moe_shape& s, const RouterBwPlan& p) {
-  const unsigned long long T = s.T, w = (size_t(p.Ep) * p.dp / 4 + 255) / 256,
-                           x = s.dtype == LC_MOE_BF16 ? 0 : (T * p.dp / 4 + 255) / 256;
-  return ((T + 3) / 4 + w + x) * 256 <= 0xFFFFFFFFull;
-}
 hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, void* ws, const void* x,
                                   const float* w_router, const float* logits, const int32_t* idx,
                                   const float* dgate, const float* aux, const void* dx_add, void* dx, float* dw,
                                   float* dlogits, hipStream_t st);
+
+// Two values to bf16, nearest even, the first in the low half (v_cvt_pk_bf16_f32).
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
+}
 
 // ---- AdamW ---------------------------------------------------------------------------
 hipError_t launch_adamw(const lc_moe_adamw_tensor* tensors, int count, const lc_moe_adamw_hyper& h, hipStream_t st);

@@ -88,9 +88,9 @@ def test_router_backward_refusals():
     s = shape()
     n = lt.lc_moe_router_backward_workspace_size(s)
     assert n > 0 and lt.lc_moe_router_backward_workspace_size(shape(d=4)) == 0
-    # one work-item per 4 fp32 token elements: 2^20 tokens of 16384 are 2^32
+    # as large as the layer itself may be
     huge = shape(T=1 << 20, d=1 << 14, K=1, dtype=lm.F32)
-    assert lm.lc_moe_workspace_size(huge) > 0 and lt.lc_moe_router_backward_workspace_size(huge) == 0
+    assert lm.lc_moe_workspace_size(huge) > 0 and lt.lc_moe_router_backward_workspace_size(huge) > 0
 
     def call(sh=s, x=P, w=P, lg=P, idx=P, dg=P, aux=P, add=P, dx=P, dw=P, dl=P, ws=P, nb=n):
         return lt._lib().lc_moe_router_backward(ctypes.byref(sh) if sh is not None else None, x, w, lg, idx, dg, aux,
@@ -101,7 +101,6 @@ def test_router_backward_refusals():
     for k in ("x", "w", "lg", "idx", "dg", "aux", "add", "dx", "dw", "dl", "ws"):
         assert call(**{k: MIS}) == 4, k
     assert call(nb=n - 1) == 5 and call(sh=shape(K=13)) == 2 and call(sh=shape(dtype=2)) == 3
-    assert call(sh=huge, nb=1 << 62) == 2
 
 
 def test_adamw_refusals():
