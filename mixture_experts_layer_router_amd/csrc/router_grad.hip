@@ -8,9 +8,9 @@
 //                      by side in one grid
 //   sum_parts_kernel   the pieces of dW's reduction over the tokens, added in order
 //
-// What bounds it.  T = 16384, d = 6144, E = 768, bf16: 0.66 ms.  dW's three products of
+// What bounds it.  T = 16384, d = 6144, E = 768, bf16: 0.97 ms.  dW's three products of
 // 155 GFLOP take 0.37-0.40 ms, 1.15-1.25 PFLOP/s, the rate of a large library product (1.2
-// measured on this card); dx's one takes 0.20-0.22 for 0.4 GB of dx_add and dx and 155 GFLOP;
+// measured on this card); dx's three take 0.5 with 0.4 GB of dx_add and dx (one took 0.20-0.22);
 // the operands 0.045, W_r 0.01, the sum of dW's three pieces 0.014.  One 155 GFLOP product
 // each in fp32 (150 TFLOP/s) would take 1.0 ms.  Steps that got it there: 8.0 ms on plain fp32
 // tiles, 0.95 on bf16 parts, 0.77 with dx from fp16 rows, 0.71 with two workgroups a CU and dx
@@ -23,10 +23,14 @@
 // Precision.  dW is an fp32 output: dlogits is cut into three bf16 parts (24 bits), the tokens
 // are bf16 already (or cut the same way), every product of parts is exact and the matrix cores
 // add them in fp32.  dx of an fp32 layer is made the same way.  dx of a bf16 layer is rounded
-// to bf16, so its operands keep 16 bits (two bf16 parts each, three products), or 11 in the
-// form for many tokens: fp16 with a power of two taken out of every row, one product.  An
-// operand rounded to fp16 is off by at most 2^-11 of its value (2^-25 of its row's largest
-// below 2^-29 of that); the result's own rounding is 2^-8.
+// to bf16, but the rows of W_r may share a part that cancels in it (a row of the gates' dlogits
+// sums to 0), so digits that its operands lose can show many times as large.  The form for many
+// tokens takes two fp16 parts of each operand, a power of two taken out of every row, and three
+// products: an operand is off by at most 2^-23 of its value (2^-39 of its row's largest below
+// 2^-17 of that), a product by 2^-21, less than its sums in fp32.  (One fp16 part of each, 11 bits,
+// took 0.66 ms for the whole call; with rows of W_r that are ten parts shared to one part
+// different, dx was off by 3.4e-3, where bf16's rounding alone is 1.7e-3.)  The small forms keep 16
+// bits, two bf16 parts each and three products.
 #include <type_traits>
 
 #include "train.h"
@@ -67,14 +71,20 @@ __device__ __forceinline__ void cut8(const float (&v)[8], bf16x8 (&o)[NP]) {
   for (int z = 0; z < NP; ++z) o[z] = __builtin_bit_cast(bf16x8, u[z]);
 }
 
-__device__ __forceinline__ bf16_t f16_bits(float v) { return __builtin_bit_cast(bf16_t, static_cast<_Float16>(v)); }
+// v as the sum of two fp16 numbers, the value to nearest and what is left of it: off by 2^-23 of v
+// (a unit of fp32's last place), or by 2^-25 where the second falls below fp16's normal numbers.
+__device__ __forceinline__ void cut16(float v, bf16_t (&o)[2]) {
+  const _Float16 h = static_cast<_Float16>(v);
+  o[0] = __builtin_bit_cast(bf16_t, h);
+  o[1] = __builtin_bit_cast(bf16_t, static_cast<_Float16>(v - static_cast<float>(h)));
+}
 
 // Exponent of the largest magnitude, so that 2^(14 - it) brings it into [2^14, 2^15), well inside
 // fp16; 0 for a row of zeros.
 __device__ __forceinline__ int top_exp(float amax) { return amax > 0.f ? ilogbf(amax) : 0; }
 
-// W_r row by row as fp16: w16[e] = 2^(14 - x) w[e], wexp[e] = x.  One workgroup per row; rows
-// from E on are zeros.
+// W_r row by row as two fp16 parts: the sum of w16[0][e] and w16[1][e] is 2^(14 - x) w[e], wexp[e]
+// = x.  One workgroup per row; rows from E on are zeros.  [2][rows][d], a row per workgroup.
 __global__ __launch_bounds__(256) void weight_f16_kernel(const float* __restrict__ w, bf16_t* __restrict__ w16,
                                                          int32_t* __restrict__ wexp, int E, int d) {
   __shared__ float wm[4];
@@ -95,9 +105,13 @@ __global__ __launch_bounds__(256) void weight_f16_kernel(const float* __restrict
   for (int c = tid * 4; c < d; c += 1024) {
     float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
     if (e < E) q = *reinterpret_cast<const float4*>(row + c);
-    *reinterpret_cast<uint2*>(w16 + size_t(e) * d + c) =
-        make_uint2(f16_bits(ldexpf(q.x, 14 - x)) | (uint32_t(f16_bits(ldexpf(q.y, 14 - x))) << 16),
-                   f16_bits(ldexpf(q.z, 14 - x)) | (uint32_t(f16_bits(ldexpf(q.w, 14 - x))) << 16));
+    bf16_t h[4][2];
+    cut16(ldexpf(q.x, 14 - x), h[0]), cut16(ldexpf(q.y, 14 - x), h[1]);
+    cut16(ldexpf(q.z, 14 - x), h[2]), cut16(ldexpf(q.w, 14 - x), h[3]);
+#pragma unroll
+    for (int z = 0; z < 2; ++z)
+      *reinterpret_cast<uint2*>(w16 + (size_t(z) * gridDim.x + e) * d + c) =
+          make_uint2(h[0][z] | (uint32_t(h[1][z]) << 16), h[2][z] | (uint32_t(h[3][z]) << 16));
   }
 }
 
@@ -108,7 +122,7 @@ struct OperandArgs {
   const float* aux;
   float* out;        // dlogits in fp32, or NULL
   bf16_t* parts;     // [3][T][Ep]
-  bf16_t* dl16;      // [T][Ep] fp16: 2^(wexp[e] + 14 - x) dlogits, x the row's exponent; or NULL
+  bf16_t* dl16;      // [2][T][Ep] fp16 parts of 2^(wexp[e] + 14 - x) dlogits, x the row's exponent; or NULL
   float* rscale;     // [T] 2^(x - 28)
   const int32_t* wexp;
   int T, E, K, Ep;
@@ -209,10 +223,15 @@ __global__ __launch_bounds__(256) void operands_kernel(OperandArgs a) {
     x = x < -98 ? -98 : x;  // 2^(x - 28) is a normal fp32 number
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      bf16_t h[V];
+      bf16_t h[2][V];
 #pragma unroll
-      for (int w = 0; w < V; ++w) h[w] = f16_bits(ldexpf(v[j * V + w], 14 - x));
-      put(a.dl16 + size_t(t) * a.Ep, j, h);
+      for (int w = 0; w < V; ++w) {
+        bf16_t c[2];
+        cut16(ldexpf(v[j * V + w], 14 - x), c);
+        h[0][w] = c[0], h[1][w] = c[1];
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) put(a.dl16 + q * plane + size_t(t) * a.Ep, j, h[q]);
     }
     if (lane == 0) a.rscale[t] = ldexpf(1.f, x - 28);
   }
@@ -226,6 +245,9 @@ __global__ __launch_bounds__(256) void operands_kernel(OperandArgs a) {
 // and three) the operand tiles of a stage carry 1, 3 or 6 products.
 //   DX: A(m, k) = dlogits, row m, K-contiguous; B(k, n) = W_r, row k.
 //   DW: A(m, k) = dlogits, row k (a token), M-contiguous; B(k, n) = tokens, row k.
+// F16: A and B are two fp16 parts each.  Their products (h h, h m, m h; the one of two low parts is
+// 2^-22 of the product) are taken one after another along a reduction three times as long, so a
+// stage holds one part of each (NA = NB = 1).
 // CUT: B is fp32 (W_r; fp32 tokens) and lies in LDS as such; a wave cuts its fragments into the
 // NB parts in registers.  (Parts cut by a launch before take 6 bytes a value, so 96 KB of LDS and
 // one workgroup a CU, and a pass over x and W_r: fp32 T = 4096, d = 2048, E = 96 took 69 us, now 51;
@@ -240,8 +262,8 @@ __global__ __launch_bounds__(256) void operands_kernel(OperandArgs a) {
 // c ^ swz4(r).
 // ---------------------------------------------------------------------------------------
 struct ProdArgs {
-  const bf16_t* a;  // [NA][T][Ep] (or its fp16 form)
-  const void* b;    // DX: [krows][ldb]; DW: [T][ldb]
+  const bf16_t* a;  // [NA][T][Ep] (F16: [2][T][Ep])
+  const void* b;    // DX: [krows][ldb] (F16: [2][krows][ldb]); DW: [T][ldb]
   size_t plane_a;
   const bf16_t* zero;
   const void* add;
@@ -267,6 +289,7 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
   static_assert(!DX || BK == 32, "K-contiguous rows are staged 64 bytes at a time");
   static_assert(NBL == 2 || NBL == 4, "wave tiles of 64 or 128 columns");
   static_assert(CUT || NB == 1, "B comes in parts only if it is cut here");
+  static_assert(!F16 || (DX && NA == 1 && NB == 1), "fp16 parts follow one another");
 
   // unit: pieces of the reduction, in them groups of 8 M-tiles, in a group column tiles, in them
   // its M-tiles; each XCD takes a contiguous eighth, so workgroups side by side share operand
@@ -330,9 +353,17 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
   auto issue = [&](int kt) {
     unsigned char* st = smem + (kt % NST) * STAGE;
     unsigned char* sb = st + NA * A_OP;
-    const int k0 = kbeg + kt * BK;
-    const bf16_t* a0 = DX ? p.a + size_t(m0) * p.lda + k0 : p.a + size_t(k0) * p.lda + m0;
-    const char* b0 = static_cast<const char*>(p.b) + (size_t(k0) * p.ldb + n0) * EB;
+    int k0 = kbeg + kt * BK;
+    const bf16_t* pa = p.a;
+    size_t brow = k0;
+    if constexpr (F16) {  // krows, a multiple of BK, steps of each pair of parts
+      const int pair = (k0 >= p.krows) + (k0 >= 2 * p.krows);
+      k0 -= pair * p.krows;
+      brow = k0 + (pair == 1 ? p.krows : 0);
+      if (pair == 2) pa += p.plane_a;
+    }
+    const bf16_t* a0 = DX ? pa + size_t(m0) * p.lda + k0 : pa + size_t(k0) * p.lda + m0;
+    const char* b0 = static_cast<const char*>(p.b) + (brow * p.ldb + n0) * EB;
     if (near && k0 + BK <= krows) {
 #pragma unroll
       for (int q = 0; q < NA; ++q) {
@@ -806,7 +837,7 @@ hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, 
   a.dx.krows = f16 ? p.Ep : E;
   a.dx.rscale = o.rscale;
   a.dx.M = s.T;
-  a.dx.Kdim = a.dx.chunk = p.Ep;
+  a.dx.Kdim = a.dx.chunk = f16 ? 3 * p.Ep : p.Ep;
   a.dx.splits = 1;
   a.dx.add = dx_add;
   a.dx.c = dx;

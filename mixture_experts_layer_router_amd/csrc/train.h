@@ -58,7 +58,7 @@ hipError_t launch_gate_backward(const lc_moe_shape& s, const void* x, const void
 // The two products run on the matrix cores, their fp32 operands cut into parts (router_grad.hip).
 //   few    at most 64 tokens: dx straight from the fp32 weight
 //   small  128 x 128 tiles, dlogits as bf16 parts, fp32 W_r and tokens cut in registers
-//   big    bf16 layers: 128 x 256 tiles, dx from scaled fp16
+//   big    bf16 layers: 128 x 256 tiles, dx from two scaled fp16 parts
 // Ep: E rounded up to whole operand rows (32 experts).
 enum RbForm { kRbFew, kRbSmall, kRbBig };
 struct RouterBwPlan {
@@ -89,9 +89,9 @@ inline RouterBwPlan plan_router_backward(const lc_moe_shape& s) {
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align256(o + bytes); return at; };
   p.dl = take(3 * T * p.Ep * 2);
-  p.dl16 = take(big ? T * p.Ep * 2 : 0);
+  p.dl16 = take(big ? 2 * T * p.Ep * 2 : 0);
   p.rscale = take(big ? T * 4 : 0);
-  p.wp = take(big ? size_t(p.Ep) * s.d * 2 : 0);
+  p.wp = take(big ? 2 * size_t(p.Ep) * s.d * 2 : 0);
   p.wexp = take(big ? size_t(p.Ep) * 4 : 0);
   p.part = take(p.splits > 1 ? size_t(p.splits) * E * s.d * 4 : 0);
   p.zero = take(16);

@@ -1,0 +1,78 @@
+"""Digits of the training operators' results where common inputs do not show them: router
+weights whose rows share a large part, that part cancelling in dx.
+
+u = 2^-24 is half an fp32 step relative to the value; a bf16 result is rounded by 2^-8 at most.
+"""
+import numpy as np
+import pytest
+
+from gpu_common import device, rel_l2, say, to_np
+from oracle import train as ot
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+def put(a, dtype=None):
+    import torch
+    t = torch.tensor(np.ascontiguousarray(a))
+    return (t if dtype is None else t.to(dtype)).to(device())
+
+
+# ---- router backward: dx ----------------------------------------------------------------------
+
+# wide tiles (384 of 128 x 256); fp32: few tokens, tiles of 128 x 128
+FORMS = [dict(T=2048, d=6144), dict(T=40, d=516, f32=True), dict(T=600, d=516, f32=True)]
+
+
+def cancelling(rng, T):
+    """[T,3] fp32 of 24 digits each, rows that sum to exactly 0: a, b and -(a + b)."""
+    a = rng.integers(1 << 22, 1 << 23, (T, 2)).astype(np.float64)
+    return (np.stack([a[:, 0], a[:, 1], -(a[:, 0] + a[:, 1])], axis=1) * 2.0 ** -23).astype(np.float32)
+
+
+@pytest.mark.parametrize("kw", FORMS, ids=lambda k: f"T{k['T']}_d{k['d']}_{'f32' if k.get('f32') else 'bf16'}")
+def test_router_dx_where_the_rows_share_a_large_part(kw):
+    """W_r = 4096 c + noise, dlogits that sum to 0 over the experts: dx is made of the noise
+    alone, and every digit that dlogits or W_r lose shows 4096 times as large.  No softmax is
+    in the way (dlogits = dlogits_aux).  Two fp16 parts are off by 2^-23 of a value, the product
+    of two low parts, left out, is 2^-22: 8 u of a product, and 3 E partial products are added;
+    three bf16 parts leave out 4 u, with 6 E additions."""
+    import torch
+    import mixture_experts_layer_router_amd as lm
+    T, d, E, half = kw["T"], kw["d"], 3, not kw.get("f32")
+    say(f"router dx, rows with a shared part {kw}")
+    rng = np.random.default_rng(T + d)
+    aux = cancelling(rng, T)
+    w = (4096.0 * rng.standard_normal(d) + rng.standard_normal((E, d))).astype(np.float32)
+    x = torch.zeros(T, d, dtype=torch.bfloat16 if half else torch.float32, device=device())
+    got = to_np(lm.router_backward(x, put(w), None, None, None, E, dlogits_aux=put(aux), need_dw=False)["dx"])
+    w64, a64 = w.astype(np.float64), aux.astype(np.float64)
+    want = a64 @ w64
+    tol = (6 * E + 8 + 8) * U * (np.abs(a64) @ np.abs(w64))
+    tol += 2.0 ** -8 * (np.abs(want) + tol) if half else U * np.abs(want)
+    worst = (np.abs(got - want) / tol).max()
+    assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("kw", [dict(T=40, d=1032), dict(T=600, d=520), dict(T=2048, d=6144)],
+                         ids=lambda k: f"T{k['T']}_d{k['d']}")
+def test_router_dx_of_a_bf16_layer_is_off_by_its_rounding_alone(kw):
+    """Rows of W_r with a shared part ten times the rest, gradients of the gates through the
+    softmax.  Rounding to nearest is uniform within half a step, so its root mean square is at
+    most 2^-8 / sqrt(3) of the value; dlogits in fp32 are off by at most 336 u of terms of either
+    sign (see test_gpu_train.py), which the shared part shows ten times as large: 2^-12 at most."""
+    import torch
+    import mixture_experts_layer_router_amd as lm
+    T, d, E, K = kw["T"], kw["d"], 96, 6
+    say(f"router dx, rms error {kw}")
+    rng = np.random.default_rng(T)
+    w = ((10.0 * rng.standard_normal(d) + rng.standard_normal((E, d))) / np.sqrt(d)).astype(np.float32)
+    lg = rng.standard_normal((T, E)).astype(np.float32)
+    idx = np.argsort(rng.random((T, E)), axis=1)[:, :K].astype(np.int32)
+    dg = rng.standard_normal((T, K)).astype(np.float32)
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device=device())
+    got = to_np(lm.router_backward(x, put(w), put(lg), put(idx), put(dg), E, need_dw=False)["dx"])
+    want = ot.router_backward(np.zeros((T, d)), w.astype(np.float64), lg, idx, dg)["dx"]
+    assert rel_l2(got, want) <= 2.0 ** -8 / np.sqrt(3) + 2.0 ** -12
