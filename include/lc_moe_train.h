@@ -115,9 +115,8 @@ lc_moe_status lc_moe_gate_backward(const lc_moe_shape* shape, const void* x, con
  *   dx          = dlogits W_r + dx_add
  *   dw_router   = dlogits^T x
  * with fp32 sums.  For the matrix cores dlogits, W_r and fp32 tokens are cut into parts of 8
- * bits whose products are exact; dw_router, and dx of an fp32 layer, keep 24 bits of every
- * operand.  dx of a bf16 layer, which is rounded to bf16, keeps 16 bits of dlogits and W_r; in
- * layers of many tokens two fp16 parts with a power of two taken out of every row: 23 bits, of
+ * bits whose products are exact, three of every operand: 24 bits.  dx of a bf16 layer of many
+ * tokens is made of two fp16 parts instead, a power of two taken out of every row: 23 bits, of
  * values below 2^-17 of their row's largest down to 2^-39 of it.  dx is rounded once.
  * A pick outside 0..N+Z-1 has no gradient.  A token whose logits are all -infinity has
  * dlogits = dlogits_aux.

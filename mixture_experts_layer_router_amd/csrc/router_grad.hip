@@ -16,21 +16,20 @@
 // tiles, 0.95 on bf16 parts, 0.77 with dx from fp16 rows, 0.71 with two workgroups a CU and dx
 // through LDS, 0.66 with constant waits, dx_add loaded early and lane offsets kept.
 // Few tokens and narrow pools are bound by their launches and by a few memory latencies
-// each: T = 64, d = 6144, E = 768 takes 19.6 us (operands 6, products 14, of which each alone
-// would take 11), T = 4096, d = 2048, E = 96 takes 32 (6.5, 22, sum 4), fp32 T = 1777,
-// d = 1028, E = 77 takes 20.
+// each: T = 64, d = 6144, E = 768 takes 22.1 us (operands 6, products 16), T = 4096, d = 2048,
+// E = 96 takes 34 (6.5, 24, sum 4), fp32 T = 1777, d = 1028, E = 77 takes 20.
 //
 // Precision.  dW is an fp32 output: dlogits is cut into three bf16 parts (24 bits), the tokens
 // are bf16 already (or cut the same way), every product of parts is exact and the matrix cores
-// add them in fp32.  dx of an fp32 layer is made the same way.  dx of a bf16 layer is rounded
-// to bf16, but the rows of W_r may share a part that cancels in it (a row of the gates' dlogits
-// sums to 0), so digits that its operands lose can show many times as large.  The form for many
+// add them in fp32.  dx is made the same way.  That of a bf16 layer is rounded to bf16, but the
+// rows of W_r may share a part that cancels in it (a row of the gates' dlogits sums to 0), so
+// digits that its operands lose can show many times as large (two bf16 parts each, 16 bits, took
+// 19.7 us at T = 64 and 31.1 at T = 4096).  The form for many
 // tokens takes two fp16 parts of each operand, a power of two taken out of every row, and three
 // products: an operand is off by at most 2^-23 of its value (2^-39 of its row's largest below
 // 2^-17 of that), a product by 2^-21, less than its sums in fp32.  (One fp16 part of each, 11 bits,
 // took 0.66 ms for the whole call; with rows of W_r that are ten parts shared to one part
-// different, dx was off by 3.4e-3, where bf16's rounding alone is 1.7e-3.)  The small forms keep 16
-// bits, two bf16 parts each and three products.
+// different, dx was off by 3.4e-3, where bf16's rounding alone is 1.7e-3.)
 #include <type_traits>
 
 #include "train.h"
@@ -241,8 +240,8 @@ __global__ __launch_bounds__(256) void operands_kernel(OperandArgs a) {
 // One tile of C[M][N] = sum over pairs of parts (a, b) of A_a B_b, fp32 accumulation on
 // v_mfma_f32_32x32x16.  A stage holds BK reduction steps of NA parts of A and NB parts of B, so
 // a loaded part serves every product it takes part in: with the pairs a + b < max(NA, NB)
-// (h h, h m, m h of two parts each; h x, m x, l x of three and one; the six largest of three
-// and three) the operand tiles of a stage carry 1, 3 or 6 products.
+// (h x, m x, l x of three and one; the six largest of three and three) the operand tiles of a
+// stage carry 1, 3 or 6 products.
 //   DX: A(m, k) = dlogits, row m, K-contiguous; B(k, n) = W_r, row k.
 //   DW: A(m, k) = dlogits, row k (a token), M-contiguous; B(k, n) = tokens, row k.
 // F16: A and B are two fp16 parts each.  Their products (h h, h m, m h; the one of two low parts is
@@ -251,8 +250,7 @@ __global__ __launch_bounds__(256) void operands_kernel(OperandArgs a) {
 // CUT: B is fp32 (W_r; fp32 tokens) and lies in LDS as such; a wave cuts its fragments into the
 // NB parts in registers.  (Parts cut by a launch before take 6 bytes a value, so 96 KB of LDS and
 // one workgroup a CU, and a pass over x and W_r: fp32 T = 4096, d = 2048, E = 96 took 69 us, now 51;
-// T = 4096, d = 2800, E = 384 184, now 144.  bf16 T = 4096, d = 2048, E = 96, whose W_r is small,
-// took 31.3, now 32.2.)
+// T = 4096, d = 2800, E = 384 184, now 144.)
 // Tile BM x BN, 64 x (BN / 2) outputs per wave, BM / 32 waves, a ring of NST stages in LDS
 // filled by direct global->LDS loads.  Operands whose output index is contiguous lie in LDS
 // as in memory ([BK][columns]) and are read by the transposing LDS read; 16-byte chunk c of
@@ -618,10 +616,8 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
 }
 
 // dx of at most 64 tokens: 32 columns a workgroup, every fourth 16-step of the reduction a
-// wave, the four sums added through LDS in wave order (T = 64, d = 6144, E = 768: 20.3 us for the
-// call; 22.4 with the six steps loaded anew when all are worked off, 22.9 with dx_add loaded at
-// the end).  W_r is read as it lies, once, and cut
-// into NP parts in registers: lane (l32, half) holds column n0 + l32 of rows 8 half + 0..7.
+// wave, the four sums added through LDS in wave order (T = 64, d = 6144, E = 768: 22.1 us for the
+// call).  W_r is read as it lies, once, and cut into NP parts in registers: lane (l32, half) holds column n0 + l32 of rows 8 half + 0..7.
 template <int NP, typename Tx>
 __device__ __forceinline__ void dx_few(const ProdArgs& p, const float* __restrict__ w, int E, unsigned block, float* sums) {
   const int n0 = block * 32;
@@ -651,7 +647,7 @@ __device__ __forceinline__ void dx_few(const ProdArgs& p, const float* __restric
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
-  constexpr int B = NP == 2 ? 6 : 3;  // steps whose loads are in flight together
+  constexpr int B = 3;  // steps whose loads are in flight together (T = 64, E = 768: 22.1 us; four 22.2, six 24.2)
   float wv[B][8];
   bf16x8 fa[B][NP][2];
   auto load = [&](int b, int k) {
@@ -727,9 +723,9 @@ struct ProductsArgs {
 template <int FORM, bool BF>
 __global__ __launch_bounds__(256, 2) void products_kernel(ProductsArgs a) {
   typedef typename std::conditional<BF, bf16_t, float>::type Tx;
-  constexpr int X = BF ? 1 : 3, W = BF ? 2 : 3;  // parts of the tokens; of W_r (and dlogits for dx)
-  // ring: big 2 x 40 KB for dW, 3 x 24 KB for dx; else 2 x 32 KB (fp32 layers 2 x 40 KB)
-  constexpr int LDS = FORM == kRbBig || !BF ? 81920 : 65536;
+  constexpr int X = BF ? 1 : 3, W = 3;  // parts of the tokens; of W_r (and dlogits for dx)
+  // ring: big 2 x 40 KB for dW, 3 x 24 KB for dx; else 2 x 40 KB (few bf16 tokens 2 x 32 KB)
+  constexpr int LDS = FORM == kRbFew && BF ? 65536 : 81920;
   __shared__ __attribute__((aligned(1024))) unsigned char smem[LDS];
   if (blockIdx.x < a.dw_blocks) {
     if constexpr (FORM == kRbBig) product_tile<false, false, false, 128, 256, 3, 1, 32, 2, float>(a.dw, blockIdx.x, smem);

@@ -22,8 +22,9 @@ def put(a, dtype=None):
 
 # ---- router backward: dx ----------------------------------------------------------------------
 
-# wide tiles (384 of 128 x 256); fp32: few tokens, tiles of 128 x 128
-FORMS = [dict(T=2048, d=6144), dict(T=40, d=516, f32=True), dict(T=600, d=516, f32=True)]
+# few tokens, tiles of 128 x 128, wide tiles (384 of 128 x 256); fp32 beside them
+FORMS = [dict(T=40, d=1032), dict(T=600, d=520), dict(T=2048, d=6144), dict(T=40, d=516, f32=True),
+         dict(T=600, d=516, f32=True)]
 
 
 def cancelling(rng, T):
