@@ -79,8 +79,9 @@ __device__ __forceinline__ void cut16(float v, bf16_t (&o)[2]) {
 }
 
 // Exponent of the largest magnitude, so that 2^(14 - it) brings it into [2^14, 2^15), well inside
-// fp16; 0 for a row of zeros.
-__device__ __forceinline__ int top_exp(float amax) { return amax > 0.f ? ilogbf(amax) : 0; }
+// fp16; -300 for a row of zeros, so that 2^it times any fp32 number is 0 and the scale of a token's
+// row is taken from the experts whose W_r is not zero.
+__device__ __forceinline__ int top_exp(float amax) { return amax > 0.f ? ilogbf(amax) : -300; }
 
 // W_r row by row as two fp16 parts: the sum of w16[0][e] and w16[1][e] is 2^(14 - x) w[e], wexp[e]
 // = x.  One workgroup per row; rows from E on are zeros.  [2][rows][d], a row per workgroup.

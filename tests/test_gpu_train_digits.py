@@ -1,5 +1,5 @@
 """Digits of the training operators' results where common inputs do not show them: router
-weights whose rows share a large part, that part cancelling in dx.
+weights whose rows share a large part, that part cancelling in dx, and ones with rows of zeros.
 
 u = 2^-24 is half an fp32 step relative to the value; a bf16 result is rounded by 2^-8 at most.
 """
@@ -77,3 +77,23 @@ def test_router_dx_of_a_bf16_layer_is_off_by_its_rounding_alone(kw):
     got = to_np(lm.router_backward(x, put(w), put(lg), put(idx), put(dg), E, need_dw=False)["dx"])
     want = ot.router_backward(np.zeros((T, d)), w.astype(np.float64), lg, idx, dg)["dx"]
     assert rel_l2(got, want) <= 2.0 ** -8 / np.sqrt(3) + 2.0 ** -12
+
+
+def test_router_dx_with_a_row_of_zeros():
+    """Many tokens: a row of zeros among small rows of W_r, an expert that is not in use yet, takes
+    no digits from the others."""
+    import torch
+    import mixture_experts_layer_router_amd as lm
+    T, d, E = 2048, 6144, 3
+    say("router dx, a row of zeros")
+    rng = np.random.default_rng(11)
+    aux = cancelling(rng, T)
+    w = np.ldexp(rng.standard_normal((E, d)), -40).astype(np.float32)
+    w[1] = 0
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device=device())
+    got = to_np(lm.router_backward(x, put(w), None, None, None, E, dlogits_aux=put(aux), need_dw=False)["dx"])
+    w64, a64 = w.astype(np.float64), aux.astype(np.float64)
+    want = a64 @ w64
+    tol = (6 * E + 8 + 8) * U * (np.abs(a64) @ np.abs(w64))
+    tol += 2.0 ** -8 * (np.abs(want) + tol)
+    assert (np.abs(got - want) / tol).max() <= 1
