@@ -186,7 +186,7 @@ typedef struct {
  * which E4M3 could not span.  Rounded to nearest, a state that moves by less than half a
  * step per update would never move; so the codes are rounded up or down at random with the
  * right mean, from 16 bits each of a hash of (seed, step, place in `tensors`, element), the
- * same bits for the same arguments (the value over 2^k may be an ulp off); and an r above 0
+ * same bits for the same arguments; and an r above 0
  * stays above 0, so that no m is ever divided by eps alone.  The update itself uses m and v
  * before they are rounded.  A state that becomes infinite (v, for a gradient above 1e19) takes
  * the exponent byte 247 and the largest code, which is infinite again when it is read; its

@@ -252,14 +252,6 @@ template <int BITS>
 __global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args a) {
   using namespace aw;
   const Hyper& h = a.h;
-  // 8 bits: 2^-k of every exponent byte, from the math library's powf.  It may be an ulp off
-  // the power of two, 2^-20 of a code's step; tensor libraries scale by it too, so the codes
-  // equal those of a program that computes the step with elementary tensor operations.
-  __shared__ float inverse[BITS == 8 ? 256 : 1];
-  if constexpr (BITS == 8) {
-    inverse[threadIdx.x] = powf(2.f, 127.f - static_cast<float>(threadIdx.x));
-    __syncthreads();
-  }
   int ti = 0;
   for (int i = 1; i < a.count; ++i) ti = a.first[i] <= blockIdx.x ? i : ti;
   const Desc& t = a.t[ti];
@@ -333,7 +325,8 @@ __global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args 
     } else {
       const uint32_t key = mix(key0 + 0x85A308D3u * uint32_t(uint64_t(i) >> 32));
       const int bm = block_byte(block_max(m)), bv = block_byte(block_max(r));
-      const float im = inverse[bm], iv = inverse[bv];
+      // 2^-k from its exponent bits: bytes are at most 247, so these are normal numbers
+      const float im = __uint_as_float(uint32_t(254 - bm) << 23), iv = __uint_as_float(uint32_t(254 - bv) << 23);
       // An r above 0 gets a code above 0: below 2^-9 that is 1, the code of 2^-9.  Infinities get
       // the largest code.  Asked for by the smallest and largest v: r iv < 2^-9 only if v iv iv is
       // below 2^-17.
@@ -436,7 +429,7 @@ hipError_t launch_adamw(const lc_moe_adamw_tensor* tensors, int count, const lc_
   a.h.grad_scale = h.grad_scale;
   a.h.p1 = power(double(h.beta1), h.step_dev ? 1 : h.step);
   a.h.p2 = power(double(h.beta2), h.step_dev ? 1 : h.step);
-  // Strips of a workgroup.  8 bits: four share its start (the table of scales) where that
+  // Strips of a workgroup.  8 bits: four share its start where that
   // leaves enough workgroups to fill the chip several times (403M weights: 775 us with four,
   // 782 with eight, 792 with sixteen; a step of few elements is done sooner with one each).
   // 32 bits: one, so that the workgroups in flight touch neighbouring memory (403M weights

@@ -1,5 +1,6 @@
 """Digits of the training operators' results where common inputs do not show them: router
-weights whose rows share a large part, that part cancelling in dx, and ones with rows of zeros.
+weights whose rows share a large part, that part cancelling in dx, and ones with rows of zeros;
+the scales of 8-bit states.
 
 u = 2^-24 is half an fp32 step relative to the value; a bf16 result is rounded by 2^-8 at most.
 """
@@ -97,3 +98,33 @@ def test_router_dx_with_a_row_of_zeros():
     tol = (6 * E + 8 + 8) * U * (np.abs(a64) @ np.abs(w64))
     tol += 2.0 ** -8 * (np.abs(want) + tol)
     assert (np.abs(got - want) / tol).max() <= 1
+
+
+# ---- AdamW ------------------------------------------------------------------------------------
+
+def test_8bit_codes_at_the_border_of_the_random_rounding():
+    """The codes are those of the value over 2^k, exactly: with beta1 = beta2 = 0, m = g and
+    sqrt(v) = |g|, so a gradient can put the quotient right at, and one fp32 step below, the
+    point where the random bits carry into the code.  Blocks of 2^k from k = -40 to 40."""
+    import torch
+    import mixture_experts_layer_router_amd as lm
+    say("adamw, codes at the border")
+    ks = np.arange(-40, 41)
+    n = ks.size * 128
+    u = ot.random_bits(5, 1, 0, np.arange(n))
+    rng = np.random.default_rng(1)
+    for half, low in ((u & np.uint64(0xFFFF), False), (u >> np.uint64(16), True)):
+        r = (half.astype(np.int64) << 4) + 8
+        border = (1 << 20) - r - rng.integers(0, 2, n)  # the digits below the code's last place
+        # a normal code in [2^-6, 256): exponent and three digits at random
+        y = ((rng.integers(121, 135, n) << 23) | (rng.integers(0, 8, n) << 20) | border).astype(np.int32).view(np.float32)
+        y[::128] = 448.0  # every block's largest: its exponent is k
+        g = np.ldexp(y, np.repeat(ks, 128)).astype(np.float32)
+        grad = put(g if low else np.where(np.arange(n) % 3 == 0, -g, g))
+        opt = lm.AdamW([torch.zeros(n, device=device())], [grad], state_bits=8)
+        opt.step(1e-3, beta1=0.0, beta2=0.0, eps=1e-8, step=1, seed=5)
+        q, s = (opt.v[0], opt.v_scales[0]) if low else (opt.m[0], opt.m_scales[0])
+        want, k = ot.round_random(to_np(grad), half, low)
+        np.testing.assert_array_equal(k, ks)
+        np.testing.assert_array_equal(to_np(s), ks + 127)
+        np.testing.assert_array_equal(to_np(q), want)
