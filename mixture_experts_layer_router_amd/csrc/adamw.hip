@@ -1,13 +1,12 @@
 // One AdamW step over many tensors (formulas and the form of the 8-bit states in
 // include/lc_moe_train.h).  A step reads and writes every byte of the weights and states
 // once: it is bound by HBM.  403M bf16 weights with fp32 masters and 32-bit states (28 bytes a
-// weight) take 1.88-2.12 ms, 5.3-6.0 TB/s, on different cards, where a copy reaches 4.9.  With
-// 8-bit states and no masters (10 bytes) 0.68-0.78 ms, 5.2-5.9 TB/s: there the arithmetic (the hash, two random roundings, a root)
+// weight) take 2.13 ms, 5.3 TB/s, where a copy reaches 4.9.  With 8-bit states and no masters (10
+// bytes) 0.75-0.77 ms, 5.3 TB/s: there the arithmetic (the hash, two random roundings, a root)
 // counts beside the bytes.  Steps: 1.25 ms with codes decoded in integer arithmetic and
 // 1 - beta^step by expm1 in every thread, 0.84 without, 0.795 with strips typed by what the
-// tensors hold (0.826 if their loads are issued a strip ahead at 113 registers), 0.775 with the
-// hardware's random rounding, which also takes the registers from 94 to 67.  (On the fastest card
-// seen the last two together take it from 0.795 to 0.683.)
+// tensors hold, 0.78 with the hardware's random rounding, which also takes the registers from 94
+// to 67, 0.765 with one strip a workgroup instead of four.
 // The tensors' addresses travel in the kernel's arguments, up to kMaxTensors a launch, so a
 // step of a few dozen tensors is one launch and needs no device table.
 #include <cmath>
@@ -40,7 +39,7 @@ struct Hyper {
   float lr, beta1, omb1, beta2, omb2, eps;
   double p1, p2;  // beta1^step, beta2^step
   uint32_t seed;
-  int step, strips;  // strips of a workgroup
+  int step;
   const int32_t* step_dev;
   const float* grad_scale;
 };
@@ -246,8 +245,10 @@ __device__ __forceinline__ void encode(const float (&m)[8], const float (&r)[8],
 
 }  // namespace aw
 
-// One workgroup takes h.strips strips of one tensor, one after another; a thread has 8
-// consecutive elements of a strip, a row of 16 lanes one block of the 8-bit states.
+// One workgroup takes one strip of one tensor, so that the workgroups in flight touch neighbouring
+// memory (403M weights: 32-bit states and masters 2109 us, 2126 with two strips, 2171 with four;
+// 8-bit states 765, 778, 781).  A thread has 8 elements of it, with 8-bit states consecutive ones,
+// a row of 16 lanes one block of the states.
 template <int BITS>
 __global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args a) {
   using namespace aw;
@@ -258,8 +259,8 @@ __global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args 
   float gs = 1.f;
   if (h.grad_scale) gs = *h.grad_scale;
   // A scale that is not finite leaves the step out.  32 bits: asked for behind the strip's loads,
-  // which it would hold up (40 small tensors: 9.7 us before, 7.2 behind); 8 bits: once for all
-  // strips (403M weights: 880 us behind every strip's loads, 815 before).
+  // which it would hold up (40 small tensors: 9.7 us before, 7.2 behind); 8 bits: either way takes
+  // 765 us for 403M weights.
   const bool finite = fabsf(gs) < INFINITY;
   if (BITS == 8 && !finite) return;
   int step = h.step;
@@ -272,7 +273,7 @@ __global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args 
   }
   const Scalars sc = scalars(h, t.lrs, t.wd, p1, p2);
   const uint32_t key0 = mix(h.seed + 0x9E3779B9u * uint32_t(step)) + 0x3C6EF373u * ((t.flags >> 2) + 1u);
-  const int64_t strip0 = int64_t(t.at) + int64_t(blockIdx.x - a.first[ti]) * h.strips;
+  const int64_t strip0 = int64_t(t.at) + int64_t(blockIdx.x - a.first[ti]);
   // 32 bits: groups of 4 with a strip's half between them, so that every load and store of
   // fp32 values is one contiguous piece of a wave; 8 bits: 8 consecutive elements
   constexpr int GAP = BITS == 32 ? kStrip / 2 : 4;
@@ -370,14 +371,13 @@ __global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args 
       update(i, two, g, w, m, v, cm, cv, sm, sv);
     }
   };
-  if constexpr (BITS == 32) {
-    const int64_t at = strip0 * kStrip;
-    if (at + kStrip <= t.n) strip(at, std::true_type{});
-    else if (at < t.n) strip(at, std::false_type{});
+  const int64_t at = strip0 * kStrip;
+  if (at + kStrip > t.n) {
+    if (at < t.n) strip(at, std::false_type{});
+  } else if constexpr (BITS == 32) {
+    strip(at, std::true_type{});
   } else {
-    const int64_t whole = t.n / kStrip - strip0;
-    const int full = whole < 0 ? 0 : whole < h.strips ? int(whole) : h.strips;
-    // whole strips; GB, WB: gradients, weights in bf16
+    // GB, WB: gradients, weights in bf16
     auto run = [&](auto gb, auto wb) {
       constexpr bool GB = decltype(gb)::value, WB = decltype(wb)::value;
       const char* gp = static_cast<const char*>(t.grad);
@@ -393,24 +393,17 @@ __global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args 
           o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
         }
       };
-      int64_t i = strip0 * kStrip + mine;
+      const int64_t i = at + mine;
       const int two[2] = {4, 4};
-#pragma unroll 1
-      for (int s = 0; s < full; ++s, i += kStrip) {
-        float g[8], w[8], m[8], v[8];
-        load(gp + i * (GB ? 2 : 4), gb, g);
-        load(wp + i * (WB ? 2 : 4), wb, w);
-        const uint2 cm = load_codes(t.m, i, 8), cv = load_codes(t.v, i, 8);
-        update(i, two, g, w, m, v, cm, cv, pow2(int(t.ms[i >> 7]) - 127), pow2(int(t.vs[i >> 7]) - 127));
-      }
+      float g[8], w[8], m[8], v[8];
+      load(gp + i * (GB ? 2 : 4), gb, g);
+      load(wp + i * (WB ? 2 : 4), wb, w);
+      const uint2 cm = load_codes(t.m, i, 8), cv = load_codes(t.v, i, 8);
+      update(i, two, g, w, m, v, cm, cv, pow2(int(t.ms[i >> 7]) - 127), pow2(int(t.vs[i >> 7]) - 127));
     };
-    if (full > 0) {
-      const bool wb = !t.master && (t.flags & 1);
-      if (t.flags & 2) wb ? run(std::true_type{}, std::true_type{}) : run(std::true_type{}, std::false_type{});
-      else wb ? run(std::false_type{}, std::true_type{}) : run(std::false_type{}, std::false_type{});
-    }
-    const int64_t at = (strip0 + full) * kStrip;
-    if (full < h.strips && at < t.n) strip(at, std::false_type{});
+    const bool wb = !t.master && (t.flags & 1);
+    if (t.flags & 2) wb ? run(std::true_type{}, std::true_type{}) : run(std::true_type{}, std::false_type{});
+    else wb ? run(std::false_type{}, std::true_type{}) : run(std::false_type{}, std::false_type{});
   }
 }
 
@@ -429,16 +422,8 @@ hipError_t launch_adamw(const lc_moe_adamw_tensor* tensors, int count, const lc_
   a.h.grad_scale = h.grad_scale;
   a.h.p1 = power(double(h.beta1), h.step_dev ? 1 : h.step);
   a.h.p2 = power(double(h.beta2), h.step_dev ? 1 : h.step);
-  // Strips of a workgroup.  8 bits: four share its start where that
-  // leaves enough workgroups to fill the chip several times (403M weights: 775 us with four,
-  // 782 with eight, 792 with sixteen; a step of few elements is done sooner with one each).
-  // 32 bits: one, so that the workgroups in flight touch neighbouring memory (403M weights
-  // with masters: 2109 us with one, 2126 with two, 2171 with four).
-  int64_t total = 0;
-  for (int i = 0; i < count; ++i) total += (tensors[i].n + kStrip - 1) / kStrip;
-  a.h.strips = h.state_bits == 8 && total >= 16384 ? 4 : 1;
   // One launch covers up to kMaxTensors pieces and kMaxBlocks workgroups (the grid holds
-  // 2^32 - 1 work-items); a tensor that needs more is cut at a multiple of its strips.
+  // 2^32 - 1 work-items); a tensor that needs more is cut between strips.
   constexpr int64_t kMaxBlocks = int64_t(1) << 23;
   int64_t blocks = 0;
   auto flush = [&]() -> hipError_t {
@@ -457,7 +442,7 @@ hipError_t launch_adamw(const lc_moe_adamw_tensor* tensors, int count, const lc_
         const hipError_t err = flush();
         if (err != hipSuccess) return err;
       }
-      int64_t take = (strips - at + a.h.strips - 1) / a.h.strips;
+      int64_t take = strips - at;
       if (take > kMaxBlocks - blocks) take = kMaxBlocks - blocks;
       a.first[a.count] = uint32_t(blocks);
       Desc& d = a.t[a.count++];
@@ -474,7 +459,7 @@ hipError_t launch_adamw(const lc_moe_adamw_tensor* tensors, int count, const lc_
       d.at = uint32_t(at);
       d.flags = (t.param_dtype == LC_MOE_BF16 ? 1u : 0u) | (t.grad_dtype == LC_MOE_BF16 ? 2u : 0u) | (uint32_t(i) << 2);
       blocks += take;
-      at += take * a.h.strips;
+      at += take;
     }
   }
   return flush();
