@@ -382,9 +382,14 @@ class AdamW:
                                            _dtype_code(self.grads[i], f"grads[{i}]"), wd[i], ls[i])
         _on_gpu(self.device)
 
-    def step(self, lr, beta1=0.9, beta2=0.95, eps=1e-8, step=1, seed=0, grad_scale=None, step_dev=None):
-        """One step on the current stream.  step: its number, from 1 on, or step_dev: an int32
-        tensor of one element to read it from; grad_scale: an fp32 tensor of one element."""
+    def step(self, lr, beta1=0.9, beta2=0.95, eps=1e-8, step=None, seed=0, grad_scale=None, step_dev=None):
+        """One step on the current stream.  step: its number, from 1 on (the object does not count),
+        or step_dev: an int32 tensor of one element to read it from; one of the two is needed.
+        grad_scale: an fp32 tensor of one element."""
+        if step_dev is not None:
+            step = 1  # not read
+        elif step is None or not 1 <= step < 1 << 31:
+            raise ValueError(f"AdamW: step {step}: the number of the step, from 1 on, or step_dev is needed")
         for name, t, dtype in (("grad_scale", grad_scale, torch.float32), ("step_dev", step_dev, torch.int32)):
             if t is not None and (t.dtype != dtype or t.numel() != 1 or t.device != self.device):
                 raise ValueError(f"{name}: one {dtype} on {self.device} is needed")
