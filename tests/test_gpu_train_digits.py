@@ -1,6 +1,6 @@
 """Digits of the training operators' results where common inputs do not show them: router
 weights whose rows share a large part, that part cancelling in dx, and ones with rows of zeros;
-the scales of 8-bit states.
+the scales of 8-bit states; the step number on the device.
 
 u = 2^-24 is half an fp32 step relative to the value; a bf16 result is rounded by 2^-8 at most.
 """
@@ -128,3 +128,130 @@ def test_8bit_codes_at_the_border_of_the_random_rounding():
         np.testing.assert_array_equal(k, ks)
         np.testing.assert_array_equal(to_np(s), ks + 127)
         np.testing.assert_array_equal(to_np(q), want)
+
+
+HYPER = dict(beta1=0.9, beta2=0.95, eps=1e-8, seed=7)
+
+
+def optimizer(bits, master=True):
+    """Two tensors (one ends inside a strip and a block) whose states are not zero."""
+    import torch
+    import mixture_experts_layer_router_amd as lm
+    rng = np.random.default_rng(bits)
+    w = [rng.standard_normal(n).astype(np.float32) for n in (5000, 2048)]
+    opt = lm.AdamW([put(a, torch.bfloat16) for a in w], [put(rng.standard_normal(a.size), torch.bfloat16) for a in w],
+                   masters=[put(w[0]), None] if master else None, state_bits=bits, weight_decay=0.1)
+    opt.step(1e-2, step=3, **HYPER)
+    return opt
+
+
+def state(opt):
+    return [t for x in (opt.params, opt.masters, opt.m, opt.v, opt.m_scales, opt.v_scales) for t in x if t is not None]
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("number", [1, 2, 7, 1000, 0, -3])
+def test_a_step_number_on_the_device_is_the_one_of_the_host(bits, number):
+    """Bias corrections and random bits alike; values below 1 are 1.  (Step 5 has another bias
+    correction than each of these numbers, so one that is not read shows; the numbers next to 1000 have
+    none, since 1 - 0.95^1000 is 1 in 64 bits.)"""
+    import torch
+    say(f"adamw {bits} bits, step {number} on the device")
+    a, b, c = (optimizer(bits) for _ in range(3))
+    a.step(1e-2, step=max(number, 1), **HYPER)
+    b.step(1e-2, step_dev=put(np.array([number], np.int32)), **HYPER)
+    c.step(1e-2, step=5, **HYPER)
+    for s, t in zip(state(a), state(b)):
+        assert torch.equal(s, t)
+    assert not torch.equal(a.params[0], c.params[0])
+    if bits == 8:
+        assert not torch.equal(a.m[0], c.m[0]) and not torch.equal(a.v[0], c.v[0])
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_replays_of_a_captured_step_are_the_numbered_steps(bits):
+    """A step captured with its number on the device, replayed with other work between, against
+    eager steps that are given the number by the host."""
+    import torch
+    say(f"adamw {bits} bits, captured")
+    a, b = optimizer(bits), optimizer(bits)
+    number = torch.full((1,), 4, dtype=torch.int32, device=device())
+    keep = [t.clone() for t in state(b)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        b.step(1e-2, step_dev=number, **HYPER)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.step(1e-2, step_dev=number, **HYPER)
+    for t, s in zip(state(b), keep):
+        t.copy_(s)
+    for i in range(4, 8):
+        number.fill_(i)
+        for o in (a, b):
+            o.grads[0].mul_(-0.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        a.step(1e-2, step=i, **HYPER)
+        torch.cuda.synchronize()
+        for s, t in zip(state(a), state(b)):
+            assert torch.equal(s, t), i
+
+
+def test_8bit_step_of_several_large_tensors():
+    """The first and last 1000 or so elements of tensors of many strips (of 2048) and odd ends, against
+    the oracle, codes to the bit; a tensor of one element between them."""
+    import torch
+    import mixture_experts_layer_router_amd as lm
+    sizes = [2048 * 9001 + 5, 1, 2048 * 4002 + 129, 2048 * 3403, 2048 * 2000 + 2047]
+    say(f"adamw 8 bits, {sizes}")
+    gen = torch.Generator(device=device())
+    gen.manual_seed(3)
+    g = [torch.randn(n, generator=gen, device=device()).to(torch.bfloat16) for n in sizes]
+    opt = lm.AdamW([torch.ones(n, dtype=torch.bfloat16, device=device()) for n in sizes], g, state_bits=8)
+    h = dict(lr=float(np.float32(1e-2)), beta1=float(np.float32(0.9)), beta2=float(np.float32(0.95)), eps=float(np.float32(1e-8)))
+    opt.step(step=2, seed=6, **h)
+    for i, n in enumerate(sizes):
+        first = max(n - 1000, 0) // 128 * 128
+        for a, z in ((0, min(n, 1024)), (first, n)):
+            gr, zero = to_np(g[i][a:z]), np.zeros(z - a, np.float32)
+            m32, _, r32 = ot.adamw_fp32(zero, gr, zero, zero, wd=0.0, step=2, **h)
+            u = ot.random_bits(6, 2, i, np.arange(a, z))
+            for val, b, low, q, s in ((m32, u & np.uint64(0xFFFF), False, opt.m[i], opt.m_scales[i]),
+                                      (r32, u >> np.uint64(16), True, opt.v[i], opt.v_scales[i])):
+                want, k = ot.round_random(val, b, low)
+                np.testing.assert_array_equal(to_np(s[a // 128:-(-z // 128)]), k + 127)
+                np.testing.assert_array_equal(to_np(q[a:z]), want)
+            w = ot.adamw(np.ones(z - a), gr, zero.astype(np.float64), zero.astype(np.float64), h["lr"], h["beta1"], h["beta2"],
+                         h["eps"], 0.0, 2)[0]
+            assert (np.abs(to_np(opt.params[i][a:z]) - w) <= 2.0 ** -8 * np.abs(w) * (1 + 2.0 ** -7)).all()
+
+
+# ---- one expert -------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("aux", [False, True])
+def test_router_backward_of_one_expert(f32, aux):
+    """E = 1: p = 1, so the gates' gradient does not reach the logits (p is off by 128 u, see
+    test_gpu_train.py, and dlogits by 336 u of 2 |dp|); what the losses give passes through."""
+    import torch
+    import mixture_experts_layer_router_amd as lm
+    T, d, K = 70, 40, 1
+    say(f"router, one expert, f32={f32} aux={aux}")
+    rng = np.random.default_rng(8)
+    dt = torch.float32 if f32 else torch.bfloat16
+    x, w = put(rng.standard_normal((T, d)), dt), put(rng.standard_normal((1, d)).astype(np.float32))
+    lg, dg = put(rng.standard_normal((T, 1)).astype(np.float32)), put(rng.standard_normal((T, K)).astype(np.float32))
+    au = put(rng.standard_normal((T, 1)).astype(np.float32)) if aux else None
+    r = lm.router_backward(x, w, lg, put(np.zeros((T, K), np.int32)), dg, 1, dlogits_aux=au, need_dlogits=True)
+    f = lambda t: to_np(t).astype(np.float64)  # noqa: E731
+    dl = f(au) if aux else np.zeros((T, 1))
+    err = 336 * U * 2 * np.abs(f(dg)) + U * np.abs(dl)
+    assert (np.abs(f(r["dlogits"]) - dl) <= err).all()
+    want = dl @ f(w)
+    tol = err @ np.abs(f(w)) + 16 * U * np.abs(want)
+    assert (np.abs(f(r["dx"]) - want) <= tol + (U if f32 else 2.0 ** -8) * (np.abs(want) + tol)).all()
+    tol = err.T @ np.abs(f(x)) + (6 * T + 12) * U * (np.abs(dl).T @ np.abs(f(x)))
+    assert (np.abs(f(r["dw_router"]) - dl.T @ f(x)) <= tol).all()
