@@ -8,9 +8,9 @@
 //                      by side in one grid
 //   sum_parts_kernel   the pieces of dW's reduction over the tokens, added in order
 //
-// What bounds it.  T = 16384, d = 6144, E = 768, bf16: 0.97 ms.  dW's three products of
+// What bounds it.  T = 16384, d = 6144, E = 768, bf16: 0.91 ms.  dW's three products of
 // 155 GFLOP take 0.37-0.40 ms, 1.15-1.25 PFLOP/s, the rate of a large library product (1.2
-// measured on this card); dx's three take 0.5 with 0.4 GB of dx_add and dx (one took 0.20-0.22);
+// measured on this card); dx's three take 0.45 with 0.4 GB of dx_add and dx (one took 0.20-0.22);
 // the operands 0.045, W_r 0.01, the sum of dW's three pieces 0.014.  One 155 GFLOP product
 // each in fp32 (150 TFLOP/s) would take 1.0 ms.  Steps that got it there: 8.0 ms on plain fp32
 // tiles, 0.95 on bf16 parts, 0.77 with dx from fp16 rows, 0.71 with two workgroups a CU and dx
@@ -241,13 +241,14 @@ __global__ __launch_bounds__(256) void operands_kernel(OperandArgs a) {
 // One tile of C[M][N] = sum over pairs of parts (a, b) of A_a B_b, fp32 accumulation on
 // v_mfma_f32_32x32x16.  A stage holds BK reduction steps of NA parts of A and NB parts of B, so
 // a loaded part serves every product it takes part in: with the pairs a + b < max(NA, NB)
-// (h x, m x, l x of three and one; the six largest of three and three) the operand tiles of a
-// stage carry 1, 3 or 6 products.
+// (h x, m x, l x of three and one; h h, h m, m h of two each; the six largest of three and three)
+// the operand tiles of a stage carry 3 or 6 products.
 //   DX: A(m, k) = dlogits, row m, K-contiguous; B(k, n) = W_r, row k.
 //   DW: A(m, k) = dlogits, row k (a token), M-contiguous; B(k, n) = tokens, row k.
-// F16: A and B are two fp16 parts each.  Their products (h h, h m, m h; the one of two low parts is
-// 2^-22 of the product) are taken one after another along a reduction three times as long, so a
-// stage holds one part of each (NA = NB = 1).
+// F16: A and B are two fp16 parts each; the product of two low parts, left out, is 2^-22 of the
+// whole.  A stage of 16 steps with both parts of both reads 94 bytes of LDS a clock at the matrix
+// cores' full rate; the three products one after another, 32 steps of one part of each a stage,
+// would need 140, more than the 128 there are (0.91 ms against 0.97 for the call).
 // CUT: B is fp32 (W_r; fp32 tokens) and lies in LDS as such; a wave cuts its fragments into the
 // NB parts in registers.  (Parts cut by a launch before take 6 bytes a value, so 96 KB of LDS and
 // one workgroup a CU, and a pass over x and W_r: fp32 T = 4096, d = 2048, E = 96 took 69 us, now 51;
@@ -258,10 +259,10 @@ __global__ __launch_bounds__(256) void operands_kernel(OperandArgs a) {
 // row r sits in the 32-byte granule (c / 2) ^ 2 (r % 4), which spreads the four rows of a
 // read over the banks; fp32 chunk c of row r sits in c ^ 8 (r / 8 % 2), so that the two halves of
 // a wave, 8 rows apart, read different banks.  K-contiguous rows are 64 bytes, chunk c in slot
-// c ^ swz4(r).
+// c ^ swz4(r), or 32 bytes, c ^ (r / 4 % 2).
 // ---------------------------------------------------------------------------------------
 struct ProdArgs {
-  const bf16_t* a;  // [NA][T][Ep] (F16: [2][T][Ep])
+  const bf16_t* a;  // [NA][T][Ep]
   const void* b;    // DX: [krows][ldb] (F16: [2][krows][ldb]); DW: [T][ldb]
   size_t plane_a;
   const bf16_t* zero;
@@ -280,15 +281,14 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
   constexpr int NBL = WC / 32;                          // 32-wide column blocks of a wave
   constexpr int EB = CUT ? 4 : 2, CC = 16 / EB;            // bytes of an element of B, columns of a chunk
   constexpr int A_OP = BM * BK * 2, B_OP = BN * BK * EB;  // bytes of A's parts (each) and of B in a stage
-  constexpr int STAGE = NA * A_OP + B_OP;
+  constexpr int NL = CUT ? 1 : NB;                        // parts of B that are loaded
+  constexpr int STAGE = NA * A_OP + NL * B_OP;
   constexpr int NP = NA > NB ? NA : NB;
   constexpr int LA = A_OP / 1024 / WAVES, LB = B_OP / 1024 / WAVES;  // direct loads of a wave
-  constexpr int LOADS = NA * LA + LB;                                // and per stage
+  constexpr int LOADS = NA * LA + NL * LB;                           // and per stage
   static_assert(A_OP % (1024 * WAVES) == 0 && B_OP % (1024 * WAVES) == 0, "whole loads");
-  static_assert(!DX || BK == 32, "K-contiguous rows are staged 64 bytes at a time");
+  static_assert(!DX || BK == 32 || BK == 16, "K-contiguous rows are staged 64 or 32 bytes at a time");
   static_assert(NBL == 2 || NBL == 4, "wave tiles of 64 or 128 columns");
-  static_assert(CUT || NB == 1, "B comes in parts only if it is cut here");
-  static_assert(!F16 || (DX && NA == 1 && NB == 1), "fp16 parts follow one another");
 
   // unit: pieces of the reduction, in them groups of 8 M-tiles, in a group column tiles, in them
   // its M-tiles; each XCD takes a contiguous eighth, so workgroups side by side share operand
@@ -330,12 +330,14 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
   // Whole stages: the lane's byte offset from the stage's first element does not change, so a
   // load is a scalar base and that offset.  Columns past the operand repeat a valid column and
   // rows past M a valid row; neither is stored.
+  auto swz = [](int r) { return BK == 32 ? swz4(r) : r >> 2 & 1; };  // K-contiguous row r
   uint32_t off_a[LA], off_b[LB];
 #pragma unroll
   for (int i = 0; i < LA; ++i) {
     if constexpr (DX) {
-      const int r = 16 * (wave + WAVES * i) + (lane >> 2);
-      off_a[i] = uint32_t(m0 + r < p.M ? r : 0) * p.lda * 2 + ((lane & 3) ^ swz4(r)) * 16;
+      constexpr int CPR = BK / 8;  // chunks of a row
+      const int r = 64 / CPR * (wave + WAVES * i) + lane / CPR;
+      off_a[i] = uint32_t(m0 + r < p.M ? r : 0) * p.lda * 2 + ((lane % CPR) ^ swz(r)) * 16;
     } else {
       int kr, ch;
       col_place(BM, i, kr, ch);
@@ -352,17 +354,10 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
   auto issue = [&](int kt) {
     unsigned char* st = smem + (kt % NST) * STAGE;
     unsigned char* sb = st + NA * A_OP;
-    int k0 = kbeg + kt * BK;
-    const bf16_t* pa = p.a;
-    size_t brow = k0;
-    if constexpr (F16) {  // krows, a multiple of BK, steps of each pair of parts
-      const int pair = (k0 >= p.krows) + (k0 >= 2 * p.krows);
-      k0 -= pair * p.krows;
-      brow = k0 + (pair == 1 ? p.krows : 0);
-      if (pair == 2) pa += p.plane_a;
-    }
-    const bf16_t* a0 = DX ? pa + size_t(m0) * p.lda + k0 : pa + size_t(k0) * p.lda + m0;
-    const char* b0 = static_cast<const char*>(p.b) + (brow * p.ldb + n0) * EB;
+    const int k0 = kbeg + kt * BK;
+    const bf16_t* a0 = DX ? p.a + size_t(m0) * p.lda + k0 : p.a + size_t(k0) * p.lda + m0;
+    const char* b0 = static_cast<const char*>(p.b) + (size_t(k0) * p.ldb + n0) * EB;
+    const size_t plane_b = size_t(p.krows) * p.ldb * EB;  // bytes of a part of B
     if (near && k0 + BK <= krows) {
 #pragma unroll
       for (int q = 0; q < NA; ++q) {
@@ -371,7 +366,9 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
         for (int i = 0; i < LA; ++i) dma16(g + off_a[i], st + q * A_OP + (wave + WAVES * i) * 1024);
       }
 #pragma unroll
-      for (int i = 0; i < LB; ++i) dma16(b0 + off_b[i], sb + (wave + WAVES * i) * 1024);
+      for (int q = 0; q < NL; ++q)
+#pragma unroll
+        for (int i = 0; i < LB; ++i) dma16(b0 + q * plane_b + off_b[i], sb + q * B_OP + (wave + WAVES * i) * 1024);
       return;
     }
     // a piece's last, partial stage: rows past its end (the tokens of dW, W_r's last) are zeros
@@ -388,12 +385,14 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
         }
         dma16(g, st + q * A_OP + (wave + WAVES * i) * 1024);
       }
-    for (int i = 0; i < LB; ++i) {
-      int kr, ch;
-      b_place(i, kr, ch);
-      const bool in = k0 + kr < krows && n0 + ch * CC < p.ldb;
-      dma16(in ? b0 + size_t(kr) * p.ldb * EB + ch * 16 : reinterpret_cast<const char*>(p.zero), sb + (wave + WAVES * i) * 1024);
-    }
+    for (int q = 0; q < NL; ++q)
+      for (int i = 0; i < LB; ++i) {
+        int kr, ch;
+        b_place(i, kr, ch);
+        const bool in = k0 + kr < krows && n0 + ch * CC < p.ldb;
+        dma16(in ? b0 + q * plane_b + size_t(kr) * p.ldb * EB + ch * 16 : reinterpret_cast<const char*>(p.zero),
+              sb + q * B_OP + (wave + WAVES * i) * 1024);
+      }
   };
 
   const int l32 = lane & 31, khalf = lane >> 5;
@@ -466,8 +465,8 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
         for (int q = 0; q < NA; ++q)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            fa[q][i] = *reinterpret_cast<const bf16x8*>(st + q * A_OP + (wm * 64 + i * 32 + l32) * 64 +
-                                                        (((ks / 8 + khalf) ^ swz4(l32)) << 4));
+            fa[q][i] = *reinterpret_cast<const bf16x8*>(st + q * A_OP + (wm * 64 + i * 32 + l32) * (2 * BK) +
+                                                        (((ks / 8 + khalf) ^ swz(l32)) << 4));
       }
       // Each block of transposing reads waits for itself (see ffn_wgrad_kernel).
       auto tr4 = [&](auto pitch, uint32_t a0, uint32_t a1, bf16x8& f0, bf16x8& f1) {
@@ -519,13 +518,18 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
           for (int q = 0; q < NB; ++q) fb[q][j] = h[q];
         }
       } else if constexpr (NBL == 4) {
-        uint32_t ad[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) ad[j] = tr_addr(sb, BN * 2, wn * WC + 32 * j, ks);
-        tr8(std::integral_constant<int, BN * 2>{}, ad, fb[0]);
+        for (int q = 0; q < NB; ++q) {
+          uint32_t ad[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) ad[j] = tr_addr(sb + q * B_OP, BN * 2, wn * WC + 32 * j, ks);
+          tr8(std::integral_constant<int, BN * 2>{}, ad, fb[q]);
+        }
       } else {
-        tr4(std::integral_constant<int, BN * 2>{}, tr_addr(sb, BN * 2, wn * WC, ks),
-            tr_addr(sb, BN * 2, wn * WC + 32, ks), fb[0][0], fb[0][1]);
+#pragma unroll
+        for (int q = 0; q < NB; ++q)
+          tr4(std::integral_constant<int, BN * 2>{}, tr_addr(sb + q * B_OP, BN * 2, wn * WC, ks),
+              tr_addr(sb + q * B_OP, BN * 2, wn * WC + 32, ks), fb[q][0], fb[q][1]);
       }
 #pragma unroll
       for (int qa = 0; qa < NA; ++qa)
@@ -725,7 +729,7 @@ template <int FORM, bool BF>
 __global__ __launch_bounds__(256, 2) void products_kernel(ProductsArgs a) {
   typedef typename std::conditional<BF, bf16_t, float>::type Tx;
   constexpr int X = BF ? 1 : 3, W = 3;  // parts of the tokens; of W_r (and dlogits for dx)
-  // ring: big 2 x 40 KB for dW, 3 x 24 KB for dx; else 2 x 40 KB (few bf16 tokens 2 x 32 KB)
+  // ring: big 2 x 40 KB for dW, 3 x 24 KB for dx (16 steps each); else 2 x 40 KB (few bf16 tokens 2 x 32 KB)
   constexpr int LDS = FORM == kRbFew && BF ? 65536 : 81920;
   __shared__ __attribute__((aligned(1024))) unsigned char smem[LDS];
   if (blockIdx.x < a.dw_blocks) {
@@ -735,7 +739,7 @@ __global__ __launch_bounds__(256, 2) void products_kernel(ProductsArgs a) {
     const unsigned b = blockIdx.x - a.dw_blocks;
     if constexpr (FORM == kRbFew) dx_few<W, Tx>(a.dx, a.w, a.E, b, reinterpret_cast<float*>(smem));
     else if constexpr (FORM == kRbSmall) product_tile<true, false, true, 128, 128, W, W, 32, 2, Tx>(a.dx, b, smem);
-    else product_tile<true, true, false, 128, 256, 1, 1, 32, 3, Tx>(a.dx, b, smem);
+    else product_tile<true, true, false, 128, 256, 2, 2, 16, 3, Tx>(a.dx, b, smem);
   }
 }
 
@@ -834,7 +838,7 @@ hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, 
   a.dx.krows = f16 ? p.Ep : E;
   a.dx.rscale = o.rscale;
   a.dx.M = s.T;
-  a.dx.Kdim = a.dx.chunk = f16 ? 3 * p.Ep : p.Ep;
+  a.dx.Kdim = a.dx.chunk = p.Ep;
   a.dx.splits = 1;
   a.dx.add = dx_add;
   a.dx.c = dx;

@@ -73,13 +73,14 @@ inline RouterBwPlan plan_router_backward(const lc_moe_shape& s) {
   const bool bf = s.dtype == LC_MOE_BF16;
   p.Ep = int((E + 31) / 32 * 32);
   auto tiles = [](size_t m, size_t n, size_t bm, size_t bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
-  // wide tiles where they fill the chip one and a half times (T = 8192, d = 6144, E = 128: 117 us
-  // against 135 with the small ones; T = 4096, d = 2048, E = 96, 256 tiles: 35 against 32)
+  // wide tiles where they fill the chip one and a half times (T = 8192, d = 6144, E = 128: 131 us
+  // against 147 with the small ones; T = 2048, d = 6144, E = 768, 384 tiles: 154 against 184;
+  // T = 4096, d = 2048, E = 96, 256 tiles: 43 against 34)
   const bool big = bf && T > 64 && tiles(T, s.d, 128, 256) >= 384;
   p.form = T <= 64 ? kRbFew : big ? kRbBig : kRbSmall;
   // dW: wide tiles in pieces of at least 512 tokens for two workgroups a CU (T = 2048, d = 6144,
   // E = 768: 123 us against 132 for one), small ones in pieces of at least 128 for one, beside
-  // dx's (T = 4096, d = 2048, E = 96: 32 us against 35 for two)
+  // dx's (T = 4096, d = 2048, E = 96: 34 us against 36 for two)
   const size_t t = tiles(E, s.d, 128, big ? 256 : 128);
   size_t want = (big ? 512 : 256) / t;
   const size_t least = big ? 512 : 128, most = (T + least - 1) / least;
