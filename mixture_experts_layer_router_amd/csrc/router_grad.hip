@@ -11,7 +11,7 @@
 // What bounds it.  T = 16384, d = 6144, E = 768, bf16: 0.91 ms.  dW's three products of
 // 155 GFLOP take 0.37-0.40 ms, 1.15-1.25 PFLOP/s, the rate of a large library product (1.2
 // measured on this card); dx's three take 0.45 with 0.4 GB of dx_add and dx (one took 0.20-0.22);
-// the operands 0.045, W_r 0.01, the sum of dW's three pieces 0.014.  One 155 GFLOP product
+// the operands 0.045, W_r 0.01, the sum of dW's four pieces 0.016.  One 155 GFLOP product
 // each in fp32 (150 TFLOP/s) would take 1.0 ms.  Steps that got it there: 8.0 ms on plain fp32
 // tiles, 0.95 on bf16 parts, 0.77 with dx from fp16 rows, 0.71 with two workgroups a CU and dx
 // through LDS, 0.66 with constant waits, dx_add loaded early and lane offsets kept.

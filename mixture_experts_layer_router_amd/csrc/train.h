@@ -78,11 +78,14 @@ inline RouterBwPlan plan_router_backward(const lc_moe_shape& s) {
   // T = 4096, d = 2048, E = 96, 256 tiles: 43 against 34)
   const bool big = bf && T > 64 && tiles(T, s.d, 128, 256) >= 384;
   p.form = T <= 64 ? kRbFew : big ? kRbBig : kRbSmall;
-  // dW: wide tiles in pieces of at least 512 tokens for two workgroups a CU (T = 2048, d = 6144,
-  // E = 768: 123 us against 132 for one), small ones in pieces of at least 128 for one, beside
-  // dx's (T = 4096, d = 2048, E = 96: 34 us against 36 for two)
-  const size_t t = tiles(E, s.d, 128, big ? 256 : 128);
-  size_t want = (big ? 512 : 256) / t;
+  // dW: pieces for one workgroup a CU, beside dx's.  Wide tiles: of at least 512 tokens, and of at
+  // most 4096 while that is for no more than four workgroups a CU, since a long piece ends behind
+  // everything else (T = 2048, d = 6144, E = 768, one piece: 133 us against 154 for three; T = 4096,
+  // E = 384, three: 142 against 160 for seven; T = 16384, E = 768, four: 0.946 ms against 0.990 for
+  // one).  Small ones: of at least 128 (T = 4096, d = 2048, E = 96: 34 us against 36 for twice as many).
+  const size_t t = tiles(E, s.d, 128, big ? 256 : 128), of4096 = (T + 4095) / 4096;
+  size_t want = 256 / t;
+  if (big && want < of4096) want = of4096 < 1024 / t ? of4096 : 1024 / t;
   const size_t least = big ? 512 : 128, most = (T + least - 1) / least;
   want = want > most ? most : want < 1 ? 1 : want;
   p.chunk = int((T + want - 1) / want + 31) / 32 * 32;
