@@ -186,17 +186,17 @@ typedef struct {
  * which E4M3 could not span.  Rounded to nearest, a state that moves by less than half a
  * step per update would never move; so the codes are rounded up or down at random with the
  * right mean, from 16 bits each of a hash of (seed, step, place in `tensors`, element), the
- * same bits for the same arguments; and an r above 0
- * stays above 0, so that no m is ever divided by eps alone.  The update itself uses m and v
- * before they are rounded.  A state that becomes infinite (v, for a gradient above 1e19) takes
- * the exponent byte 247 and the largest code, which is infinite again when it is read; its
- * block is lost, other blocks are not.
+ * same bits for the same arguments, and of m and r before their rounding to fp32 (but where m's
+ * two terms cancel); and an r above 0 stays above 0, so that no m is ever divided by eps alone.
+ * The update itself uses m and v before they are rounded to codes.  A state that becomes infinite
+ * (v, for a gradient above 1e19) takes the exponent byte 247 and the largest code, which is
+ * infinite again when it is read; its block is lost, other blocks are not.
  * A state starts as zeros: codes 0 and exponent bytes 127.
  *
  * state_bits = 32: m and v are fp32, m_scale and v_scale are not read (may be NULL).
- * Tensors with n = 0 are skipped and their pointers not read.  What a call
- * writes may overlap nothing else of it; gradients may be shared.  count = 0 does nothing; count < 0, n out of range, state_bits other than 8
- * and 32, step < 1 without step_dev, a beta outside [0, 1), eps < 0 or an eps between 0 and
+ * Tensors with n = 0 are skipped and their pointers not read.  What a call writes may overlap
+ * nothing else of it; gradients may be shared.  count = 0 does nothing; count < 0, n out of range,
+ * state_bits other than 8 and 32, step < 1 without step_dev, a beta outside [0, 1), eps < 0 or an eps between 0 and
  * 2^-126 (the quotient's reciprocal takes such numbers as 0): LC_MOE_E_SHAPE; an unknown
  * dtype: LC_MOE_E_DTYPE.  With eps = 0 an element whose v is 0 follows the formula: 0 / 0. */
 lc_moe_status lc_moe_adamw(const lc_moe_adamw_tensor* tensors, int32_t count,

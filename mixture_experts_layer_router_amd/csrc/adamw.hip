@@ -6,7 +6,8 @@
 // counts beside the bytes.  Steps: 1.25 ms with codes decoded in integer arithmetic and
 // 1 - beta^step by expm1 in every thread, 0.84 without, 0.795 with strips typed by what the
 // tensors hold, 0.78 with the hardware's random rounding, which also takes the registers from 94
-// to 67, 0.765 with one strip a workgroup instead of four.
+// to 67, 0.735 with one strip a workgroup instead of four; codes settled in fp64 where fp32 would
+// decide them took it to 0.765 (80 registers; the fp64 values of every element, unrolled, 0.83).
 // The tensors' addresses travel in the kernel's arguments, up to kMaxTensors a launch, so a
 // step of a few dozen tensors is one launch and needs no device table.
 #include <cmath>
@@ -219,35 +220,55 @@ __device__ __forceinline__ int block_byte(float amax) {
   return u == 0u ? 127 : k > 8u ? int(k) - 8 : 0;
 }
 
+// 8 codes times their scale, two at a time (v_cvt_scalef32_pk_f32_fp8)
+__device__ __forceinline__ void decode(uint2 q, float scale, float (&o)[8]) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const uint32_t u[2] = {q.x, q.y};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const f32x2 d = c & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(u[c >> 1], scale, true)
+                          : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(u[c >> 1], scale, false);
+    o[2 * c] = d[0], o[2 * c + 1] = d[1];
+  }
+}
+
+// The random words of a value's two codes, 16 bits each and half a unit of them.
+__device__ __forceinline__ uint32_t word_m(uint32_t u) { return (u << 16) | 0x8000u; }
+__device__ __forceinline__ uint32_t word_v(uint32_t u) { return (u & 0xFFFF0000u) | 0x8000u; }
+
 // E4M3 codes of 8 values y rounded down or up by chance (v_cvt_sr_fp8_f32): the digits below the
 // code's last place plus the top 20 of the 32 random bits carry into it with probability
 // (their size) / (one step); below 2^-6 the steps are 2^-9.
-__device__ __forceinline__ void encode(const float (&m)[8], const float (&r)[8], uint32_t first, uint2& cm, uint2& cv) {
+__device__ __forceinline__ void encode(const float (&m)[8], const float (&r)[8], const uint32_t (&u)[8], uint2& cm, uint2& cv) {
   int qm[2] = {0, 0}, qv[2] = {0, 0};
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    uint32_t u[4];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) u[b] = mix(first + 4 * c + b);
-    // 16 bits each and half a unit of them
-    qm[c] = __builtin_amdgcn_cvt_sr_fp8_f32(m[4 * c], (u[0] << 16) | 0x8000u, qm[c], 0);
-    qm[c] = __builtin_amdgcn_cvt_sr_fp8_f32(m[4 * c + 1], (u[1] << 16) | 0x8000u, qm[c], 1);
-    qm[c] = __builtin_amdgcn_cvt_sr_fp8_f32(m[4 * c + 2], (u[2] << 16) | 0x8000u, qm[c], 2);
-    qm[c] = __builtin_amdgcn_cvt_sr_fp8_f32(m[4 * c + 3], (u[3] << 16) | 0x8000u, qm[c], 3);
-    qv[c] = __builtin_amdgcn_cvt_sr_fp8_f32(r[4 * c], (u[0] & 0xFFFF0000u) | 0x8000u, qv[c], 0);
-    qv[c] = __builtin_amdgcn_cvt_sr_fp8_f32(r[4 * c + 1], (u[1] & 0xFFFF0000u) | 0x8000u, qv[c], 1);
-    qv[c] = __builtin_amdgcn_cvt_sr_fp8_f32(r[4 * c + 2], (u[2] & 0xFFFF0000u) | 0x8000u, qv[c], 2);
-    qv[c] = __builtin_amdgcn_cvt_sr_fp8_f32(r[4 * c + 3], (u[3] & 0xFFFF0000u) | 0x8000u, qv[c], 3);
+    qm[c] = __builtin_amdgcn_cvt_sr_fp8_f32(m[4 * c], word_m(u[4 * c]), qm[c], 0);
+    qm[c] = __builtin_amdgcn_cvt_sr_fp8_f32(m[4 * c + 1], word_m(u[4 * c + 1]), qm[c], 1);
+    qm[c] = __builtin_amdgcn_cvt_sr_fp8_f32(m[4 * c + 2], word_m(u[4 * c + 2]), qm[c], 2);
+    qm[c] = __builtin_amdgcn_cvt_sr_fp8_f32(m[4 * c + 3], word_m(u[4 * c + 3]), qm[c], 3);
+    qv[c] = __builtin_amdgcn_cvt_sr_fp8_f32(r[4 * c], word_v(u[4 * c]), qv[c], 0);
+    qv[c] = __builtin_amdgcn_cvt_sr_fp8_f32(r[4 * c + 1], word_v(u[4 * c + 1]), qv[c], 1);
+    qv[c] = __builtin_amdgcn_cvt_sr_fp8_f32(r[4 * c + 2], word_v(u[4 * c + 2]), qv[c], 2);
+    qv[c] = __builtin_amdgcn_cvt_sr_fp8_f32(r[4 * c + 3], word_v(u[4 * c + 3]), qv[c], 3);
   }
   cm = make_uint2(qm[0], qm[1]);
   cv = make_uint2(qv[0], qv[1]);
+}
+
+// Steps of fp32 from the value at which the random word just carries up to y, in the top 20 bits
+// (whole numbers modulo 2^20, as digits below the code's last place are).
+__device__ __forceinline__ uint32_t past(float y, uint32_t word) { return (__float_as_uint(y) << 12) + word; }
+// Whether y lies within two steps of that value; below 2^-6 codes have other borders.
+__device__ __forceinline__ bool at_border(float y, uint32_t word) {
+  return past(y, word) + 0x2000u <= 0x3000u && fabsf(y) >= 0.015625f && fabsf(y) <= 448.f;
 }
 
 }  // namespace aw
 
 // One workgroup takes one strip of one tensor, so that the workgroups in flight touch neighbouring
 // memory (403M weights: 32-bit states and masters 2109 us, 2126 with two strips, 2171 with four;
-// 8-bit states 765, 778, 781).  A thread has 8 elements of it, with 8-bit states consecutive ones,
+// 8-bit states 748, 778, 781).  A thread has 8 elements of it, with 8-bit states consecutive ones,
 // a row of 16 lanes one block of the states.
 template <int BITS>
 __global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args a) {
@@ -259,8 +280,8 @@ __global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args 
   float gs = 1.f;
   if (h.grad_scale) gs = *h.grad_scale;
   // A scale that is not finite leaves the step out.  32 bits: asked for behind the strip's loads,
-  // which it would hold up (40 small tensors: 9.7 us before, 7.2 behind); 8 bits: either way takes
-  // 765 us for 403M weights.
+  // which it would hold up (40 small tensors: 9.7 us before, 7.2 behind); 8 bits: no difference for
+  // 403M weights.
   const bool finite = fabsf(gs) < INFINITY;
   if (BITS == 8 && !finite) return;
   int step = h.step;
@@ -285,17 +306,10 @@ __global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args 
     const int cnt = two[0] + two[1];
     float r[8];
     if constexpr (BITS == 8) {
-      const uint32_t um[2] = {cm.x, cm.y}, uv[2] = {cv.x, cv.y};
+      decode(cm, sm, m);
+      decode(cv, sv, r);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {  // two codes and their scale at a time (v_cvt_scalef32_pk_f32_fp8)
-        typedef float f32x2 __attribute__((ext_vector_type(2)));
-        const f32x2 dm = c & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(um[c >> 1], sm, true)
-                               : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(um[c >> 1], sm, false);
-        const f32x2 dv = c & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(uv[c >> 1], sv, true)
-                               : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(uv[c >> 1], sv, false);
-        m[2 * c] = dm[0], m[2 * c + 1] = dm[1];
-        v[2 * c] = mul(dv[0], dv[0]), v[2 * c + 1] = mul(dv[1], dv[1]);
-      }
+      for (int c = 0; c < 8; ++c) v[c] = mul(r[c], r[c]);
     }
     if (BITS == 32 && !finite) return;
     float least = INFINITY, most = 0.f;
@@ -341,7 +355,47 @@ __global__ __launch_bounds__(256, BITS == 8 ? 5 : 6) void adamw_kernel(aw::Args 
 #pragma unroll
         for (int c = 0; c < 8; ++c) m[c] *= im, r[c] *= iv;
       }
-      encode(m, r, uint32_t(i) + key, cm, cv);
+      uint32_t u[8], near = ~0u;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        u[c] = mix(uint32_t(i) + key + c);
+        near = min(near, min(past(m[c], word_m(u[c]) + 0x2000u), past(r[c], word_v(u[c]) + 0x2000u)));
+      }
+      // One element of 2^18 lies so near a border that its roundings to fp32 would decide which
+      // code it gets: there the state is taken in fp64.
+      if (__any(near <= 0x3000u)) {
+        uint32_t left = 0;  // bit c: m[c], bit 8 + c: r[c]
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          left |= uint32_t(at_border(m[c], word_m(u[c]))) << c | uint32_t(at_border(r[c], word_v(u[c]))) << (8 + c);
+        while (left) {
+          const int at = __builtin_ctz(left), root = at >> 3;
+          const int64_t e = i + (at & 7);
+          left &= left - 1;
+          float y = 0.f;
+          uint32_t word = 0;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            if (at == c) y = m[c], word = word_m(u[c]);
+            if (at == 8 + c) y = r[c], word = word_v(u[c]);
+          }
+          // gradient and state anew from memory, so that neither is kept for this in registers
+          const double g64 = double(t.flags & 2 ? bf2f(static_cast<const bf16_t*>(t.grad)[e]) : static_cast<const float*>(t.grad)[e]) * gs;
+          const double s64 = ldexp(double(__builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(root ? t.v : t.m)[e], 0)),
+                                   (root ? t.vs : t.ms)[e >> 7] - 127);
+          const float border = __uint_as_float(__float_as_uint(fabsf(y)) - uint32_t(int(past(y, word)) >> 12));
+          const double b = root ? h.beta2 : h.beta1;
+          const double now = root ? (b * (s64 * s64) + (1. - b) * g64 * g64) * iv * iv : fabs(b * s64 + (1. - b) * g64) * im;
+          const bool up = now >= (root ? double(border) * border : double(border));
+          y = copysignf(up ? border : __uint_as_float(__float_as_uint(border) - 1u), y);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            if (at == c) m[c] = y;
+            if (at == 8 + c) r[c] = y;
+          }
+        }
+      }
+      encode(m, r, u, cm, cv);
       store_codes(t.m, i, cnt, cm);
       store_codes(t.v, i, cnt, cv);
       if ((threadIdx.x & 15) == 0 && cnt) {

@@ -130,6 +130,45 @@ def test_8bit_codes_at_the_border_of_the_random_rounding():
         np.testing.assert_array_equal(to_np(q), want)
 
 
+def test_8bit_codes_are_those_of_the_state_in_64_bits():
+    """2^26 elements against the formula in fp64, the random rounding among it: sqrt(v) to the bit
+    (from v in fp32, 1 in 2^21 lies on the other side of its border: 32 here), m wherever its two
+    terms have one sign (where they cancel, what fp32 loses is more than two of its steps)."""
+    import torch
+    import mixture_experts_layer_router_amd as lm
+    n, dev = 1 << 26, device()
+    say("adamw, codes in 64 bits")
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(17)
+    g = (1e-3 * torch.randn(n, generator=gen, device=dev)).to(torch.bfloat16)
+    opt = lm.AdamW([torch.zeros(n, dtype=torch.bfloat16, device=dev)], [g], state_bits=8)
+    b1, b2 = float(np.float32(0.9)), float(np.float32(0.95))
+    opt.step(1e-3, beta1=b1, beta2=b2, eps=1e-8, step=1, seed=1)
+    g.copy_(1e-3 * torch.randn(n, generator=gen, device=dev))
+    half = lambda codes, scales: codes.view(torch.float8_e4m3fn).double() * torch.exp2(scales.double() - 127).repeat_interleave(128)  # noqa: E731
+    m0, r0 = half(opt.m[0], opt.m_scales[0]), half(opt.v[0], opt.v_scales[0])
+    opt.step(1e-3, beta1=b1, beta2=b2, eps=1e-8, step=2, seed=1)
+    key = int(ot.mix(np.uint64((1 + 0x9E3779B9 * 2) & 0xFFFFFFFF)))
+    key = int(ot.mix(np.uint64((key + 0x3C6EF373) & 0xFFFFFFFF)))
+    x = (torch.arange(n, device=dev) + key) & 0xFFFFFFFF
+    for shift, factor in ((16, 0x6A09E667), (15, 0xBB67AE85)):
+        x = ((x ^ (x >> shift)) * factor) & 0xFFFFFFFF
+    x = x ^ (x >> 16)
+    assert int(x[12345]) == int(ot.random_bits(1, 2, 0, np.array([12345]))[0])
+    a, b = b1 * m0, (1 - b1) * g.double()
+    m, r = a + b, (b2 * r0 ** 2 + (1 - b2) * g.double() ** 2).sqrt()
+    for name, val, bits, codes, scales, ask in (("m", m, x & 0xFFFF, opt.m[0], opt.m_scales[0], a * b >= 0),
+                                                ("r", r, x >> 16, opt.v[0], opt.v_scales[0], r > 0)):
+        y = (val * torch.exp2(127 - scales.double()).repeat_interleave(128)).abs()
+        step = torch.exp2(torch.floor(torch.log2(y.clamp(min=2.0 ** -6))) - 3)
+        q = torch.floor(y / step + (bits.double() + 0.5) / 65536) * step
+        got = codes.view(torch.float8_e4m3fn).double().abs()
+        if name == "r":
+            q = q.clamp(min=2.0 ** -9)
+        wrong = ask & (y >= 2.0 ** -6) & (got != q)
+        assert int(wrong.sum()) == 0, (name, int(wrong.sum()))
+
+
 HYPER = dict(beta1=0.9, beta2=0.95, eps=1e-8, seed=7)
 
 
