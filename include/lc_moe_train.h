@@ -196,9 +196,9 @@ typedef struct {
  * state_bits = 32: m and v are fp32, m_scale and v_scale are not read (may be NULL).
  * Tensors with n = 0 are skipped and their pointers not read.  What a call writes may overlap
  * nothing else of it; gradients may be shared.  count = 0 does nothing; count < 0, n out of range,
- * state_bits other than 8 and 32, step < 1 without step_dev, a beta outside [0, 1), eps < 0 or an eps between 0 and
- * 2^-126 (the quotient's reciprocal takes such numbers as 0): LC_MOE_E_SHAPE; an unknown
- * dtype: LC_MOE_E_DTYPE.  With eps = 0 an element whose v is 0 follows the formula: 0 / 0. */
+ * state_bits other than 8 and 32, step < 1 without step_dev, a beta outside [0, 1), eps < 0 or
+ * an eps between 0 and 2^-126 (the quotient's reciprocal takes such numbers as 0):
+ * LC_MOE_E_SHAPE; an unknown dtype: LC_MOE_E_DTYPE.  With eps = 0 an element whose v is 0 follows the formula: 0 / 0. */
 lc_moe_status lc_moe_adamw(const lc_moe_adamw_tensor* tensors, int32_t count,
                            const lc_moe_adamw_hyper* hyper, hipStream_t stream);
 

@@ -2,7 +2,7 @@
 // include/lc_moe_train.h).  A step reads and writes every byte of the weights and states
 // once: it is bound by HBM.  403M bf16 weights with fp32 masters and 32-bit states (28 bytes a
 // weight) take 2.13 ms, 5.3 TB/s, where a copy reaches 4.9.  With 8-bit states and no masters (10
-// bytes) 0.75-0.77 ms, 5.3 TB/s: there the arithmetic (the hash, two random roundings, a root)
+// bytes) 0.77 ms, 5.2 TB/s: there the arithmetic (the hash, two random roundings, a root)
 // counts beside the bytes.  Steps: 1.25 ms with codes decoded in integer arithmetic and
 // 1 - beta^step by expm1 in every thread, 0.84 without, 0.795 with strips typed by what the
 // tensors hold, 0.78 with the hardware's random rounding, which also takes the registers from 94

@@ -11,25 +11,26 @@
 // What bounds it.  T = 16384, d = 6144, E = 768, bf16: 0.91 ms.  dW's three products of
 // 155 GFLOP take 0.37-0.40 ms, 1.15-1.25 PFLOP/s, the rate of a large library product (1.2
 // measured on this card); dx's three take 0.45 with 0.4 GB of dx_add and dx (one took 0.20-0.22);
-// the operands 0.045, W_r 0.01, the sum of dW's four pieces 0.016.  One 155 GFLOP product
+// the operands 0.045, W_r 0.011, the sum of dW's four pieces 0.018.  One 155 GFLOP product
 // each in fp32 (150 TFLOP/s) would take 1.0 ms.  Steps that got it there: 8.0 ms on plain fp32
-// tiles, 0.95 on bf16 parts, 0.77 with dx from fp16 rows, 0.71 with two workgroups a CU and dx
-// through LDS, 0.66 with constant waits, dx_add loaded early and lane offsets kept.
+// tiles, 0.95 on bf16 parts; dx from fp16 rows, of one part, 0.77, 0.71 with two workgroups a CU and
+// dx through LDS, 0.65 with constant waits, dx_add loaded early and lane offsets kept; with the
+// second part 0.97, 0.91 with both in one stage.
 // Few tokens and narrow pools are bound by their launches and by a few memory latencies
 // each: T = 64, d = 6144, E = 768 takes 22.1 us (operands 6, products 16), T = 4096, d = 2048,
-// E = 96 takes 34 (6.5, 24, sum 4), fp32 T = 1777, d = 1028, E = 77 takes 20.
+// E = 96 takes 34 (6, 25, sum 4), fp32 T = 1777, d = 1028, E = 77 takes 20.
 //
 // Precision.  dW is an fp32 output: dlogits is cut into three bf16 parts (24 bits), the tokens
 // are bf16 already (or cut the same way), every product of parts is exact and the matrix cores
 // add them in fp32.  dx is made the same way.  That of a bf16 layer is rounded to bf16, but the
 // rows of W_r may share a part that cancels in it (a row of the gates' dlogits sums to 0), so
 // digits that its operands lose can show many times as large (two bf16 parts each, 16 bits, took
-// 19.7 us at T = 64 and 31.1 at T = 4096).  The form for many
-// tokens takes two fp16 parts of each operand, a power of two taken out of every row, and three
-// products: an operand is off by at most 2^-23 of its value (2^-39 of its row's largest below
-// 2^-17 of that), a product by 2^-21, less than its sums in fp32.  (One fp16 part of each, 11 bits,
-// took 0.66 ms for the whole call; with rows of W_r that are ten parts shared to one part
-// different, dx was off by 3.4e-3, where bf16's rounding alone is 1.7e-3.)
+// 19.7 us at T = 64 and 31.1 at T = 4096).  The form for many tokens takes two fp16 parts of each
+// operand, a power of two taken out of every row, and three products: an operand is off by at most
+// 2^-23 of its value (2^-39 of its row's largest below 2^-17 of that), a product by 2^-21, less
+// than its sums in fp32.  (One fp16 part of each, 11 bits, took 0.65 ms for the whole call; with
+// rows of W_r that are ten parts shared to one part different, dx was off by 3.4e-3, where bf16's
+// rounding alone is 1.7e-3.)
 #include <type_traits>
 
 #include "train.h"
@@ -122,7 +123,8 @@ struct OperandArgs {
   const float* aux;
   float* out;        // dlogits in fp32, or NULL
   bf16_t* parts;     // [3][T][Ep]
-  bf16_t* dl16;      // [2][T][Ep] fp16 parts of 2^(wexp[e] + 14 - x) dlogits, x the row's exponent; or NULL
+  bf16_t* dl16;      // [2][T][Ep] fp16 parts of 2^(wexp[e] + 14 - x) dlogits, x the row's exponent;
+                     // or NULL
   float* rscale;     // [T] 2^(x - 28)
   const int32_t* wexp;
   int T, E, K, Ep;
@@ -622,7 +624,8 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
 
 // dx of at most 64 tokens: 32 columns a workgroup, every fourth 16-step of the reduction a
 // wave, the four sums added through LDS in wave order (T = 64, d = 6144, E = 768: 22.1 us for the
-// call).  W_r is read as it lies, once, and cut into NP parts in registers: lane (l32, half) holds column n0 + l32 of rows 8 half + 0..7.
+// call).  W_r is read as it lies, once, and cut into NP parts in registers: lane (l32, half) holds
+// column n0 + l32 of rows 8 half + 0..7.
 template <int NP, typename Tx>
 __device__ __forceinline__ void dx_few(const ProdArgs& p, const float* __restrict__ w, int E, unsigned block, float* sums) {
   const int n0 = block * 32;
@@ -652,7 +655,8 @@ __device__ __forceinline__ void dx_few(const ProdArgs& p, const float* __restric
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
-  constexpr int B = 3;  // steps whose loads are in flight together (T = 64, E = 768: 22.1 us; four 22.2, six 24.2)
+  // steps whose loads are in flight together (T = 64, E = 768: 22.1 us; four 22.2, six 24.2)
+  constexpr int B = 3;
   float wv[B][8];
   bf16x8 fa[B][NP][2];
   auto load = [&](int b, int k) {
@@ -716,7 +720,7 @@ __device__ __forceinline__ void dx_few(const ProdArgs& p, const float* __restric
 }
 
 // Both products in one grid: dW's workgroups first (their tiles are the longest), then dx's.
-// (Mixed one to three, so that both kinds share a CU, they take 1.6 ms instead of 0.64 at
+// (Mixed one to three, so that both kinds share a CU, they took 1.6 ms instead of 0.64 at
 // T = 16384, d = 6144, E = 768: their operands push each other out of the L2.)
 struct ProductsArgs {
   ProdArgs dw, dx;
@@ -729,7 +733,8 @@ template <int FORM, bool BF>
 __global__ __launch_bounds__(256, 2) void products_kernel(ProductsArgs a) {
   typedef typename std::conditional<BF, bf16_t, float>::type Tx;
   constexpr int X = BF ? 1 : 3, W = 3;  // parts of the tokens; of W_r (and dlogits for dx)
-  // ring: big 2 x 40 KB for dW, 3 x 24 KB for dx (16 steps each); else 2 x 40 KB (few bf16 tokens 2 x 32 KB)
+  // ring: big 2 x 40 KB for dW, 3 x 24 KB for dx (16 steps each); else 2 x 40 KB (few bf16 tokens
+  // 2 x 32 KB)
   constexpr int LDS = FORM == kRbFew && BF ? 65536 : 81920;
   __shared__ __attribute__((aligned(1024))) unsigned char smem[LDS];
   if (blockIdx.x < a.dw_blocks) {

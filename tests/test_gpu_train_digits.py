@@ -100,6 +100,28 @@ def test_router_dx_with_a_row_of_zeros():
     assert (np.abs(got - want) / tol).max() <= 1
 
 
+def test_router_dx_with_one_large_column():
+    """Many tokens: one column of W_r 2^16 times the others, so that most of the second fp16 parts
+    are below fp16's normal numbers: an operand is off by 2^-39 of its row's largest there, and
+    no more."""
+    import torch
+    import mixture_experts_layer_router_amd as lm
+    T, d, E = 2048, 6144, 3
+    say("router dx, one large column")
+    rng = np.random.default_rng(12)
+    aux = cancelling(rng, T)
+    w = (4096.0 * rng.standard_normal(d) + rng.standard_normal((E, d))).astype(np.float32)
+    w[:, 1:] *= np.float32(2.0 ** -16)
+    w[:, 0] = 4096.0 * 3.5
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device=device())
+    got = to_np(lm.router_backward(x, put(w), None, None, None, E, dlogits_aux=put(aux), need_dw=False)["dx"])
+    w64, a64 = w.astype(np.float64), aux.astype(np.float64)
+    want = a64 @ w64
+    tol = (6 * E + 8 + 8) * U * (np.abs(a64) @ np.abs(w64)) + 2.0 ** -39 * (np.abs(a64) @ np.abs(w64).max(1))[:, None]
+    tol += 2.0 ** -8 * (np.abs(want) + tol)
+    assert (np.abs(got - want) / tol).max() <= 1
+
+
 # ---- AdamW ------------------------------------------------------------------------------------
 
 def test_8bit_codes_at_the_border_of_the_random_rounding():
