@@ -400,3 +400,8 @@ def pack_weights(w_gate, w_up, w_down):
 # ---- training operators (include/lc_moe_train.h) ----------------------------------------
 from .train import (AdamW, adamw_state, balance_loss, forward_saved, gate_backward,  # noqa: E402,F401
                     layer_backward, router_backward)
+
+# ---- block operators (include/lc_moe_block.h) --------------------------------------------
+from .block import (Fp8Matrix, Gating, block_norm, block_norm_backward, forward_picks,  # noqa: E402,F401
+                    linear_fp8, linear_fp8_backward, matmul_fp8, quantize_matrix, route_select, select,
+                    select_backward)

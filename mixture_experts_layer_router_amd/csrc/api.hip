@@ -4,6 +4,7 @@
 
 #include "checks.h"
 #include "common.h"
+#include "lc_moe_block.h"
 
 using namespace lcm;
 
@@ -57,6 +58,58 @@ lc_moe_status permute_core(const lc_moe_shape& s, const int32_t* idx, const WsPl
   LCM_LAUNCH(launch_scan(s, bc, p.nblocks, load, offsets, bb, at<MTile>(ws, p.mtiles),
                          at<int32_t>(ws, p.n_mtiles), p.bm, st));
   LCM_LAUNCH(launch_scatter(s, idx, bb, p.nblocks, slot_row, perm_token, st));
+  return LC_MOE_OK;
+}
+
+// The expert weights that the FFN reads, in the form given.
+lc_moe_status check_expert_weights(const lc_moe_shape& s, const lc_moe_weights& w) {
+  if (w.fp8 && w.packed) return LC_MOE_E_DTYPE;  // one weight format
+  if (w.fp8_act && !w.fp8) return LC_MOE_E_DTYPE;
+  if (w.fp8) {
+    LCM_CHECK(check_ptr(w.fp8));
+    if (s.dtype != LC_MOE_BF16) return LC_MOE_E_DTYPE;
+    if (plan_fp8(s).total == 0) return LC_MOE_E_SHAPE;
+    if (w.fp8_act && !fp8_mfma_ok(s)) return LC_MOE_E_SHAPE;
+  } else if (w.packed) {
+    LCM_CHECK(check_ptr(w.packed));
+    if (s.dtype != LC_MOE_BF16) return LC_MOE_E_DTYPE;
+    if (plan_packed(s).total == 0) return LC_MOE_E_SHAPE;
+  } else {
+    LCM_CHECK(check_ptr(w.w_gate));
+    LCM_CHECK(check_ptr(w.w_up));
+    LCM_CHECK(check_ptr(w.w_down));
+  }
+  return LC_MOE_OK;
+}
+
+// Grouped FFN and combine over a permutation in the workspace.  mark(i): after stage i - 1.
+template <typename Mark>
+lc_moe_status ffn_and_combine(const lc_moe_shape& s, const WsPlan& p, void* workspace, const void* x,
+                              const lc_moe_weights& w, const float* gate, void* y, hipStream_t stream, Mark mark) {
+  const int32_t* offsets = at<int32_t>(workspace, p.offsets);
+  const int32_t* perm_token = at<int32_t>(workspace, p.perm_token);
+  const int32_t* slot_row = at<int32_t>(workspace, p.slot_row);
+  const MTile* mtiles = at<MTile>(workspace, p.mtiles);
+  const int32_t* n_mtiles = at<int32_t>(workspace, p.n_mtiles);
+  void* hbuf = at<char>(workspace, p.hbuf);
+  void* ybuf = at<char>(workspace, p.ybuf);
+  if (w.fp8_act) {  // x quantized, then the FP8 MFMA gate/up (H quantized in it)
+    LCM_LAUNCH(launch_quantize_act(x, s.T, s.d, at<unsigned char>(workspace, p.xq),
+                                   at<unsigned char>(workspace, p.xs), stream));
+    LCM_LAUNCH(launch_ffn_fp8_mfma(s, p, workspace, w.fp8, 0, stream));
+  } else {
+    LCM_LAUNCH(launch_ffn_gate_up(s, x, perm_token, w.w_gate, w.w_up, w.fp8,
+                                  w.packed, hbuf, mtiles, offsets, n_mtiles, p.mt_max, stream));
+  }
+  if (!mark(3)) return LC_MOE_E_DEVICE;
+  if (w.fp8_act)
+    LCM_LAUNCH(launch_ffn_fp8_mfma(s, p, workspace, w.fp8, 1, stream));
+  else
+    LCM_LAUNCH(launch_ffn_down(s, hbuf, w.w_down, w.fp8, w.packed, ybuf, mtiles, offsets,
+                               n_mtiles, p.mt_max, stream));
+  if (!mark(4)) return LC_MOE_E_DEVICE;
+  LCM_LAUNCH(launch_combine(s, x, ybuf, slot_row, gate, y, stream));
+  if (!mark(5)) return LC_MOE_E_DEVICE;
   return LC_MOE_OK;
 }
 
@@ -153,22 +206,7 @@ lc_moe_status lc_moe_forward_staged(const lc_moe_shape* shape, const void* x,
   LCM_CHECK(check_ptr(x));
   LCM_CHECK(check_ptr(weights->w_router));
   LCM_CHECK(check_ptr(weights->bias));
-  if (weights->fp8 && weights->packed) return LC_MOE_E_DTYPE;  // one weight format
-  if (weights->fp8_act && !weights->fp8) return LC_MOE_E_DTYPE;
-  if (weights->fp8) {
-    LCM_CHECK(check_ptr(weights->fp8));
-    if (shape->dtype != LC_MOE_BF16) return LC_MOE_E_DTYPE;
-    if (plan_fp8(*shape).total == 0) return LC_MOE_E_SHAPE;
-    if (weights->fp8_act && !fp8_mfma_ok(*shape)) return LC_MOE_E_SHAPE;
-  } else if (weights->packed) {
-    LCM_CHECK(check_ptr(weights->packed));
-    if (shape->dtype != LC_MOE_BF16) return LC_MOE_E_DTYPE;
-    if (plan_packed(*shape).total == 0) return LC_MOE_E_SHAPE;
-  } else {
-    LCM_CHECK(check_ptr(weights->w_gate));
-    LCM_CHECK(check_ptr(weights->w_up));
-    LCM_CHECK(check_ptr(weights->w_down));
-  }
+  LCM_CHECK(check_expert_weights(*shape, *weights));
   LCM_CHECK(check_ptr(y));
   LCM_CHECK(check_ptr(topk_idx, true));
   LCM_CHECK(check_ptr(topk_gate, true));
@@ -189,10 +227,6 @@ lc_moe_status lc_moe_forward_staged(const lc_moe_shape* shape, const void* x,
   int32_t* offsets = at<int32_t>(workspace, p.offsets);
   int32_t* perm_token = at<int32_t>(workspace, p.perm_token);
   int32_t* slot_row = at<int32_t>(workspace, p.slot_row);
-  const MTile* mtiles = at<MTile>(workspace, p.mtiles);
-  const int32_t* n_mtiles = at<int32_t>(workspace, p.n_mtiles);
-  void* hbuf = at<char>(workspace, p.hbuf);
-  void* ybuf = at<char>(workspace, p.ybuf);
 
   // A layer of one token block runs top-K and permutation as one kernel (counted in the
   // route stage; the permute stage's span is then empty).
@@ -211,24 +245,26 @@ lc_moe_status lc_moe_forward_staged(const lc_moe_shape* shape, const void* x,
   if (!mark(1)) return LC_MOE_E_DEVICE;
   if (!fused) LCM_CHECK(permute_core(s, idx, p, workspace, ld, offsets, slot_row, perm_token, nullptr, stream));
   if (!mark(2)) return LC_MOE_E_DEVICE;
-  if (weights->fp8_act) {  // x quantized, then the FP8 MFMA gate/up (H quantized in it)
-    LCM_LAUNCH(launch_quantize_act(x, s.T, s.d, at<unsigned char>(workspace, p.xq),
-                                   at<unsigned char>(workspace, p.xs), stream));
-    LCM_LAUNCH(launch_ffn_fp8_mfma(s, p, workspace, weights->fp8, 0, stream));
-  } else {
-    LCM_LAUNCH(launch_ffn_gate_up(s, x, perm_token, weights->w_gate, weights->w_up, weights->fp8,
-                                  weights->packed, hbuf, mtiles, offsets, n_mtiles, p.mt_max, stream));
-  }
-  if (!mark(3)) return LC_MOE_E_DEVICE;
-  if (weights->fp8_act)
-    LCM_LAUNCH(launch_ffn_fp8_mfma(s, p, workspace, weights->fp8, 1, stream));
-  else
-    LCM_LAUNCH(launch_ffn_down(s, hbuf, weights->w_down, weights->fp8, weights->packed, ybuf, mtiles, offsets,
-                               n_mtiles, p.mt_max, stream));
-  if (!mark(4)) return LC_MOE_E_DEVICE;
-  LCM_LAUNCH(launch_combine(s, x, ybuf, slot_row, gate, y, stream));
-  if (!mark(5)) return LC_MOE_E_DEVICE;
-  return LC_MOE_OK;
+  return ffn_and_combine(s, p, workspace, x, *weights, gate, y, stream, mark);
+}
+
+lc_moe_status lc_moe_forward_picks(const lc_moe_shape* shape, const void* x, const lc_moe_weights* weights,
+                                   const int32_t* topk_idx, const float* topk_gate, void* y, int32_t* load,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  LCM_CHECK(check_shape(shape));
+  if (!weights) return LC_MOE_E_NULLPTR;
+  LCM_CHECK(check_ptr(x));
+  LCM_CHECK(check_expert_weights(*shape, *weights));
+  LCM_CHECK(check_ptr(topk_idx));
+  LCM_CHECK(check_ptr(topk_gate));
+  LCM_CHECK(check_ptr(y));
+  LCM_CHECK(check_ptr(load, true));
+  WsPlan p;
+  LCM_CHECK(check_ws(shape, workspace, workspace_bytes, p));
+  LCM_CHECK(permute_core(*shape, topk_idx, p, workspace, load ? load : at<int32_t>(workspace, p.load),
+                         at<int32_t>(workspace, p.offsets), at<int32_t>(workspace, p.slot_row),
+                         at<int32_t>(workspace, p.perm_token), nullptr, stream));
+  return ffn_and_combine(*shape, p, workspace, x, *weights, topk_gate, y, stream, [](int) { return true; });
 }
 
 size_t lc_moe_fp8_weights_size(const lc_moe_shape* shape) {

@@ -1,0 +1,66 @@
+// Internal definitions of the block operators (include/lc_moe_block.h).
+#pragma once
+
+#include "common.h"
+#include "lc_moe_block.h"
+
+namespace lcm {
+
+// ---- choice of experts -----------------------------------------------------------------
+constexpr int kMaxPicks = 64;   // one lane of a wavefront for each pick
+constexpr int kMaxGroups = 64;  // and for each group
+hipError_t launch_select(const lc_moe_shape& s, const lc_moe_gating& g, const float* logits, const float* bias,
+                         const uint8_t* mask, int32_t* idx, float* gate, hipStream_t st);
+hipError_t launch_select_backward(const lc_moe_shape& s, const lc_moe_gating& g, const float* logits,
+                                  const int32_t* idx, const float* dgate, const float* aux, float* dlogits,
+                                  hipStream_t st);
+
+// ---- norms around a block ----------------------------------------------------------------
+constexpr int kNormMaxD = 16384;
+hipError_t launch_block_norm(int T, int d, int dtype, const lc_moe_norm& n, const void* x, const void* y,
+                             const float* gate, const float* w_post, const float* w_pre, void* h, void* z,
+                             hipStream_t st);
+// Backward: `wgs` workgroups take the rows in turn and leave a row of partial sums each
+// (part [wgs][3][d]: dw_pre, dw_post, dgate), added in order by a second kernel.
+struct NormBwPlan {
+  size_t part, total;
+  int wgs;
+};
+NormBwPlan plan_norm_backward(int T, int d, int dtype);
+hipError_t launch_block_norm_backward(int T, int d, int dtype, const lc_moe_norm& n, const NormBwPlan& p, void* ws,
+                                      const void* h, const void* dh, const void* dz, const void* y,
+                                      const float* gate, const float* w_post, const float* w_pre, void* dx, void* dy,
+                                      float* dw_pre, float* dw_post, float* dgate, hipStream_t st);
+
+// ---- block FP8 ---------------------------------------------------------------------------
+struct Fp8Mat {
+  size_t scales, total;  // byte offsets: codes at 0
+  size_t ldc, lds;       // bytes from one row of codes, one run of scales, to the next
+  int nkb;               // runs of 128 columns
+};
+inline Fp8Mat plan_fp8_mat(int rows, int cols) {
+  Fp8Mat m{};
+  m.nkb = (cols + 127) / 128;
+  m.ldc = size_t(m.nkb) * 128;
+  m.lds = (size_t(rows) + 255) / 256 * 256;
+  m.scales = align256(size_t(rows) * m.ldc);
+  m.total = m.scales + m.nkb * m.lds + 256;
+  return m;
+}
+// Place of row r's exponent byte in its run.
+__host__ __device__ __forceinline__ size_t fp8_scale_at(size_t r) {
+  return (r & ~size_t(127)) + 4 * (r & 31) + (r >> 5 & 3);
+}
+hipError_t launch_quantize_matrix(const void* x, int rows, int cols, int block_rows, void* out, void* out_t,
+                                  hipStream_t st);
+
+struct MatmulPlan {
+  size_t part, total;
+  int splits, chunk;  // pieces of the reduction, runs of 128 of each
+  int form;
+};
+MatmulPlan plan_matmul_fp8(int M, int N, int K);
+hipError_t launch_matmul_fp8(int M, int N, int K, const MatmulPlan& p, void* ws, const void* a, const void* b,
+                             const void* add, void* out, hipStream_t st);
+
+}  // namespace lcm

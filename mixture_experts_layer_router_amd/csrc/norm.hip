@@ -1,0 +1,367 @@
+// Norms before and after a block with its gate and the scaled residual, and their gradient
+// (include/lc_moe_block.h).
+//
+// A workgroup holds a row in registers, NV vectors of 16 bytes a thread, so every array of
+// tokens is read and written once; the row's sums go through one barrier each.  It takes
+// rows in turn, and keeps the weights (and, backward, its sums over tokens) in registers.
+#include "block.h"
+#include "topk.h"
+#include "train.h"
+
+namespace lcm {
+
+template <typename E>
+struct Vec;  // 16 bytes of a row
+template <>
+struct Vec<bf16_t> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void open(const uint4& q, float (&v)[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 close(const float (&v)[8]) {
+    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  }
+};
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void open(const uint4& q, float (&v)[4]) {
+    v[0] = __uint_as_float(q.x), v[1] = __uint_as_float(q.y), v[2] = __uint_as_float(q.z), v[3] = __uint_as_float(q.w);
+  }
+  static __device__ __forceinline__ uint4 close(const float (&v)[4]) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+};
+
+constexpr int kNormMaxThreads = 1024;
+
+// Sums of C values over the workgroup, the same bits in every thread.  lds: two rooms used in
+// turn, so that one barrier is enough: a room is written again only behind the next sum's
+// barrier, which every thread reaches after it has read this one.
+template <int C>
+__device__ __forceinline__ void block_sums(float (&v)[C], float (*lds)[C][kNormMaxThreads / 64], int& turn) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) v[c] = __ockl_wfred_add_f32(v[c]);
+  if (blockDim.x == 64) return;
+  const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  float(*room)[kNormMaxThreads / 64] = lds[turn];
+  turn ^= 1;
+  if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) room[c][wave] = v[c];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    float s = 0.f;
+    for (int w = 0; w < waves; ++w) s += room[c][w];
+    v[c] = s;
+  }
+}
+
+template <typename E, int NV>
+__device__ __forceinline__ void load_weights(const float* w, int d, float other, float (&out)[NV][Vec<E>::N]) {
+  constexpr int N = Vec<E>::N;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (int(threadIdx.x) + j * int(blockDim.x)) * N;
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      float4 q = make_float4(other, other, other, other);
+      if (w && c < d) q = *reinterpret_cast<const float4*>(w + c + i);
+      out[j][i] = q.x, out[j][i + 1] = q.y, out[j][i + 2] = q.z, out[j][i + 3] = q.w;
+    }
+  }
+}
+
+template <typename E, int NV>
+__device__ __forceinline__ void load_rows(const void* p, size_t t, int d, uint4 (&out)[NV]) {
+  constexpr int N = Vec<E>::N;
+  const E* row = static_cast<const E*>(p) + t * d;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (int(threadIdx.x) + j * int(blockDim.x)) * N;
+    out[j] = p && c < d ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
+  }
+}
+
+struct NormArgs {
+  const void *x, *y;
+  const float *gate, *w_post, *w_pre;
+  void *h, *z;
+  int T, d, gate_kind;
+  float a, b, eps, rd;  // rd: 1 / d
+};
+
+template <typename E, int NV>
+__global__ __launch_bounds__(kNormMaxThreads) void block_norm_kernel(NormArgs p) {
+  constexpr int N = Vec<E>::N;
+  __shared__ float lds[2][1][kNormMaxThreads / 64];
+  int turn = 0;
+  float wpost[NV][N], wpre[NV][N], gc[NV][N];
+  load_weights<E, NV>(p.w_post, p.d, 1.f, wpost);
+  load_weights<E, NV>(p.w_pre, p.d, 0.f, wpre);
+  load_weights<E, NV>(p.gate_kind == LC_MOE_GATE_CHANNEL ? p.gate : nullptr, p.d, 1.f, gc);
+  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+    uint4 qx[NV], qy[NV];
+    load_rows<E, NV>(p.x, t, p.d, qx);
+    load_rows<E, NV>(p.y, t, p.d, qy);
+    float g = p.b;
+    if (p.gate_kind == LC_MOE_GATE_TOKEN) g *= p.gate[t];
+    float h[NV][N], s[1] = {0.f};
+    if (p.w_post) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        Vec<E>::open(qy[j], h[j]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[0] = fmaf(h[j][i], h[j][i], s[0]);
+      }
+      block_sums<1>(s, lds, turn);
+      g *= 1.f / sqrtf(fmaf(s[0], p.rd, p.eps));
+    }
+    s[0] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float x[N], y[N];
+      Vec<E>::open(qx[j], x);
+      Vec<E>::open(qy[j], y);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        h[j][i] = fmaf(p.a, x[i], g * (y[i] * (wpost[j][i] * gc[j][i])));
+        s[0] = fmaf(h[j][i], h[j][i], s[0]);
+      }
+    }
+    if (p.z) {
+      block_sums<1>(s, lds, turn);
+      s[0] = 1.f / sqrtf(fmaf(s[0], p.rd, p.eps));
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (int(threadIdx.x) + j * int(blockDim.x)) * N;
+      if (c >= p.d) continue;
+      const size_t at = size_t(t) * p.d + c;
+      if (p.h) *reinterpret_cast<uint4*>(static_cast<E*>(p.h) + at) = Vec<E>::close(h[j]);
+      if (p.z) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) h[j][i] *= s[0] * wpre[j][i];
+        *reinterpret_cast<uint4*>(static_cast<E*>(p.z) + at) = Vec<E>::close(h[j]);
+      }
+    }
+  }
+}
+
+// Threads of a row and vectors a thread: as few threads idle as may be.
+static void norm_shape(int d, int vec, int& threads, int& nv) {
+  const int n = (d + vec - 1) / vec;
+  nv = 1;
+  while ((n + nv - 1) / nv > kNormMaxThreads) ++nv;
+  threads = ((n + nv - 1) / nv + 63) / 64 * 64;
+}
+
+template <typename E>
+static hipError_t norm_forward(const NormArgs& p, hipStream_t st) {
+  int threads, nv;
+  norm_shape(p.d, Vec<E>::N, threads, nv);
+  const int wgs = 256 * (2048 / threads);
+  const dim3 grid(p.T < wgs ? p.T : wgs), block(threads);
+  switch (nv) {
+    case 1: block_norm_kernel<E, 1><<<grid, block, 0, st>>>(p); break;
+    case 2: block_norm_kernel<E, 2><<<grid, block, 0, st>>>(p); break;
+    case 3: block_norm_kernel<E, 3><<<grid, block, 0, st>>>(p); break;
+    default: block_norm_kernel<E, 4><<<grid, block, 0, st>>>(p); break;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_block_norm(int T, int d, int dtype, const lc_moe_norm& n, const void* x, const void* y,
+                             const float* gate, const float* w_post, const float* w_pre, void* h, void* z,
+                             hipStream_t st) {
+  const NormArgs p{x, y, gate, w_post, w_pre, h, z, T, d, n.gate_kind, n.residual_scale, n.block_scale, n.eps,
+                   1.f / float(d)};
+  return dtype == LC_MOE_BF16 ? norm_forward<bf16_t>(p, st) : norm_forward<float>(p, st);
+}
+
+// ---- gradient ----------------------------------------------------------------------------
+
+struct NormBwArgs {
+  const void *h, *dh, *dz, *y;
+  const float *gate, *w_post, *w_pre;
+  void *dx, *dy;
+  float *part, *dgate_token;
+  int T, d, gate_kind;
+  float a, b, eps, rd;
+};
+
+template <typename E, int NV>
+__global__ __launch_bounds__(kNormMaxThreads) void block_norm_backward_kernel(NormBwArgs p) {
+  constexpr int N = Vec<E>::N;
+  __shared__ float lds[2][3][kNormMaxThreads / 64];
+  int turn = 0;
+  float wpost[NV][N], wpre[NV][N], gc[NV][N];
+  load_weights<E, NV>(p.w_post, p.d, 1.f, wpost);
+  load_weights<E, NV>(p.w_pre, p.d, 0.f, wpre);
+  load_weights<E, NV>(p.gate_kind == LC_MOE_GATE_CHANNEL ? p.gate : nullptr, p.d, 1.f, gc);
+  float s_pre[NV][N], s_post[NV][N], s_gate[NV][N];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < N; ++i) s_pre[j][i] = s_post[j][i] = s_gate[j][i] = 0.f;
+  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+    uint4 qh[NV], qd[NV], qz[NV], qy[NV];
+    load_rows<E, NV>(p.h, t, p.d, qh);
+    load_rows<E, NV>(p.dz, t, p.d, qz);
+    load_rows<E, NV>(p.y, t, p.d, qy);
+    load_rows<E, NV>(p.dh, t, p.d, qd);
+    float g = p.b;
+    if (p.gate_kind == LC_MOE_GATE_TOKEN) g *= p.gate[t];
+    float s[3] = {0.f, 0.f, 0.f};  // h^2, w_pre dz h, y^2
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float h[N], z[N], y[N];
+      Vec<E>::open(qh[j], h);
+      Vec<E>::open(qz[j], z);
+      Vec<E>::open(qy[j], y);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        s[0] = fmaf(h[i], h[i], s[0]);
+        s[1] = fmaf(wpre[j][i] * z[i], h[i], s[1]);
+        s[2] = fmaf(y[i], y[i], s[2]);
+      }
+    }
+    block_sums<3>(s, lds, turn);
+    const float r = 1.f / sqrtf(fmaf(s[0], p.rd, p.eps));
+    const float q = p.w_post ? 1.f / sqrtf(fmaf(s[2], p.rd, p.eps)) : 1.f;
+    const float back = s[1] * p.rd * r * r;
+    float dH[NV][N];
+    s[0] = s[1] = s[2] = 0.f;  // w_post gate y dH (without the token's gate), w_post y dH
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float h[N], z[N], y[N], d[N];
+      Vec<E>::open(qh[j], h);
+      Vec<E>::open(qz[j], z);
+      Vec<E>::open(qy[j], y);
+      Vec<E>::open(qd[j], d);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        s_pre[j][i] = fmaf(z[i], h[i] * r, s_pre[j][i]);
+        dH[j][i] = fmaf(r, wpre[j][i] * z[i] - h[i] * back, d[i]);
+        const float yq = y[i] * q, wy = wpost[j][i] * yq;
+        s_post[j][i] = fmaf(g * gc[j][i] * dH[j][i], yq, s_post[j][i]);
+        s_gate[j][i] = fmaf(p.b * wy, dH[j][i], s_gate[j][i]);
+        s[0] = fmaf(wy * gc[j][i], dH[j][i], s[0]);
+      }
+    }
+    if (p.w_post || p.dgate_token) block_sums<3>(s, lds, turn);
+    if (p.dgate_token && threadIdx.x == 0) p.dgate_token[t] = p.b * s[0];
+    const float mean = g * s[0] * p.rd;  // of w_post du times y q
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (int(threadIdx.x) + j * int(blockDim.x)) * N;
+      if (c >= p.d) continue;
+      const size_t at = size_t(t) * p.d + c;
+      if (p.dy) {
+        float y[N];
+        Vec<E>::open(qy[j], y);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float du = g * gc[j][i] * dH[j][i];
+          y[i] = p.w_post ? q * (wpost[j][i] * du - y[i] * q * mean) : du;
+        }
+        *reinterpret_cast<uint4*>(static_cast<E*>(p.dy) + at) = Vec<E>::close(y);
+      }
+      if (p.dx) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) dH[j][i] *= p.a;
+        *reinterpret_cast<uint4*>(static_cast<E*>(p.dx) + at) = Vec<E>::close(dH[j]);
+      }
+    }
+  }
+  float* part = p.part + size_t(blockIdx.x) * 3 * p.d;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (int(threadIdx.x) + j * int(blockDim.x)) * N;
+    if (c >= p.d) continue;
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      *reinterpret_cast<float4*>(part + c + i) = make_float4(s_pre[j][i], s_pre[j][i + 1], s_pre[j][i + 2], s_pre[j][i + 3]);
+      *reinterpret_cast<float4*>(part + p.d + c + i) =
+          make_float4(s_post[j][i], s_post[j][i + 1], s_post[j][i + 2], s_post[j][i + 3]);
+      *reinterpret_cast<float4*>(part + 2 * p.d + c + i) =
+          make_float4(s_gate[j][i], s_gate[j][i + 1], s_gate[j][i + 2], s_gate[j][i + 3]);
+    }
+  }
+}
+
+// dst_k[c] = sum over the workgroups of part[w][k][c], in a fixed order: 64 columns a
+// workgroup, its 16 waves a sixteenth of the rows each.
+__global__ __launch_bounds__(1024) void norm_sums_kernel(const float* __restrict__ part, int wgs, int d,
+                                                         float* d0, float* d1, float* d2) {
+  __shared__ float lds[16][64];
+  float* dst = blockIdx.y == 0 ? d0 : blockIdx.y == 1 ? d1 : d2;
+  if (!dst) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
+  float s = 0.f;
+  if (c < d) {
+#pragma unroll 8
+    for (int w = wave; w < wgs; w += 16) s += part[(size_t(w) * 3 + blockIdx.y) * d + c];
+  }
+  lds[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < d) {
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) s += lds[w][lane];
+    dst[c] = s;
+  }
+}
+
+NormBwPlan plan_norm_backward(int T, int d, int dtype) {
+  NormBwPlan p{};
+  int threads, nv;
+  norm_shape(d, dtype == LC_MOE_BF16 ? 8 : 4, threads, nv);
+  const int most = 256 * (threads > 512 ? 1 : 1024 / threads < 4 ? 1024 / threads : 4);
+  p.wgs = T < most ? T : most;
+  p.part = 0;
+  p.total = align256(size_t(p.wgs > 0 ? p.wgs : 1) * 3 * d * 4);
+  return p;
+}
+
+template <typename E>
+static void norm_backward(const NormBwArgs& p, int wgs, hipStream_t st) {
+  int threads, nv;
+  norm_shape(p.d, Vec<E>::N, threads, nv);
+  const dim3 grid(wgs), block(threads);
+  switch (nv) {
+    case 1: block_norm_backward_kernel<E, 1><<<grid, block, 0, st>>>(p); break;
+    case 2: block_norm_backward_kernel<E, 2><<<grid, block, 0, st>>>(p); break;
+    case 3: block_norm_backward_kernel<E, 3><<<grid, block, 0, st>>>(p); break;
+    default: block_norm_backward_kernel<E, 4><<<grid, block, 0, st>>>(p); break;
+  }
+}
+
+hipError_t launch_block_norm_backward(int T, int d, int dtype, const lc_moe_norm& n, const NormBwPlan& plan, void* ws,
+                                      const void* h, const void* dh, const void* dz, const void* y,
+                                      const float* gate, const float* w_post, const float* w_pre, void* dx, void* dy,
+                                      float* dw_pre, float* dw_post, float* dgate, hipStream_t st) {
+  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + plan.part);
+  const bool token = n.gate_kind == LC_MOE_GATE_TOKEN;
+  const NormBwArgs p{h, dh, dz, y, gate, w_post, w_pre, dx, dy, part, token ? dgate : nullptr, T, d, n.gate_kind,
+                     n.residual_scale, n.block_scale, n.eps, 1.f / float(d)};
+  if (plan.wgs > 0) {
+    if (dtype == LC_MOE_BF16) norm_backward<bf16_t>(p, plan.wgs, st);
+    else norm_backward<float>(p, plan.wgs, st);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  float* dg = token ? nullptr : dgate;
+  if (dw_pre || dw_post || dg)
+    norm_sums_kernel<<<dim3((d + 63) / 64, 3), dim3(1024), 0, st>>>(part, plan.wgs, d, dw_pre, dw_post, dg);
+  return hipGetLastError();
+}
+
+}  // namespace lcm
