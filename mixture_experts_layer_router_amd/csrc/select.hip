@@ -1,8 +1,8 @@
 // Choice of experts from the router's logits, and the gradient of its gates
 // (include/lc_moe_block.h): softmax or sigmoid scores, a bias for the choice, groups of experts,
-// top-K, renormalised gates.
+// top-K, renormalised gates.  One wavefront a token.
 #include "block.h"
-#include "topk.h"
+#include "logit_row.h"
 
 namespace lcm {
 
@@ -31,18 +31,29 @@ struct SelectArgs {
 // softmax's largest logit and sum over the pool (not read with renorm or sigmoid scores).
 __device__ __forceinline__ float pick_gate(const SelectArgs& a, bool valid, float x, float m, float sum) {
   if (a.renorm) {
-    // shares of the picks from the logarithms of their scores, so that none underflows
-    const float ls = a.score == LC_MOE_SOFTMAX ? x : fminf(x, 0.f) - log1pf(expf(-fabsf(x)));
-    const float top = __ockl_wfred_max_f32(valid ? ls : -INFINITY);
-    const float w = valid ? expf(ls - top) : 0.f;
-    return a.scale * (w / __ockl_wfred_add_f32(w));
+    // Shares of the picks, a power of e taken out of their scores so that none underflows: a softmax
+    // score is e^(x - top) of the largest, a sigmoid one e^min(x, 0) / (1 + e^-|x|).
+    const bool soft = a.score == LC_MOE_SOFTMAX;
+    const float l = soft ? x : fminf(x, 0.f);
+    const float top = __ockl_wfred_max_f32(valid ? l : -INFINITY);
+    float w = valid ? exp_neg(l - top) : 0.f;
+    if (!soft) w *= 1.f / (1.f + exp_neg(-fabsf(x)));
+    return w * (a.scale / __ockl_wfred_add_f32(w));
   }
   const float s = a.score == LC_MOE_SOFTMAX ? expf(x - m) / sum : 1.f / (1.f + expf(-x));
   return a.scale * s;
 }
 
+// Writes a token's places, pick k (-1: none) in lane k.
+__device__ __forceinline__ void put_picks(const SelectArgs& a, int t, int lane, int pick, float g) {
+  if (lane < a.K) {
+    a.idx[size_t(t) * a.K + lane] = pick;
+    a.gate[size_t(t) * a.K + lane] = pick >= 0 ? g : 0.f;
+  }
+}
+
 // One token by one wavefront, scores in fp64.  c: room for E values in LDS.
-__device__ void select_token_f64(const SelectArgs& a, int t, int lane, double* c) {
+__device__ __forceinline__ void select_token_f64(const SelectArgs& a, int t, int lane, double* c) {
   const float* row = a.logits + size_t(t) * a.E;
   double m = -INFINITY, sum = 0.0;
   if (a.score == LC_MOE_SOFTMAX) {
@@ -101,23 +112,279 @@ __device__ void select_token_f64(const SelectArgs& a, int t, int lane, double* c
     g = pick_gate(a, pick >= 0, x, 0.f, 1.f);
   else
     g = float(double(a.scale) * (exp(x - m) / sum));
-  if (lane < a.K) {
-    a.idx[size_t(t) * a.K + lane] = pick;
-    a.gate[size_t(t) * a.K + lane] = pick >= 0 ? g : 0.f;
-  }
+  put_picks(a, t, lane, pick, g);
 }
 
-__global__ __launch_bounds__(64) void select_kernel(SelectArgs a) {
-  extern __shared__ double c[];
-  const int t = blockIdx.x, lane = threadIdx.x;
-  if (a.mask && !a.mask[t]) {
-    if (lane < a.K) {
-      a.idx[size_t(t) * a.K + lane] = -1;
-      a.gate[size_t(t) * a.K + lane] = 0.f;
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(u), lane), hi = __builtin_amdgcn_readlane(uint32_t(u >> 32), lane);
+  return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+__device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
+// Of the n values c of lanes 0 .. n-1 (n <= 64; -infinity in the lanes behind): how many are ahead of
+// the lane's in descending order, equal ones in the order of their experts e (F = double), or of
+// their lanes (float: their order is then settled in fp64).
+template <typename F>
+__device__ __forceinline__ int place_of(F c, int e, int n, int lane) {
+  int place = 0;
+  if constexpr (sizeof(F) == 8) {
+    for (int j = 0; j < n; ++j) {
+      const double cj = lane_value(c, j);
+      const int ej = __builtin_amdgcn_readlane(e, j);
+      place += (cj > c || (cj == c && ej < e)) ? 1 : 0;
     }
+  } else {
+    for (int j = 0; j < n; j += 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float cj = lane_value(c, j + i);
+        place += (lane > j + i ? cj >= c : cj > c) ? 1 : 0;
+      }
+    }
+  }
+  return place;
+}
+
+// Scores in fp32, a lane's EPL experts in registers (logit_row.h).  What may be picked is little:
+// the K-th largest of the largest of 16 parts of the pool (64 for K above 16, and where 16 leave too
+// many) bounds the K-th largest of all from below, and about 25 of 768 scores are not below it (K =
+// 12); they are gathered one to a lane and sorted by counting.
+// Where two scores next to each other are within the error of their fp32 values, the gathered ones
+// are taken again in fp64; where two groups at the border are, or more than 64 scores are gathered
+// (equal logits, say), the whole token is (select_token_f64).
+template <int EPL, int V>
+__global__ __launch_bounds__(256) void select_kernel(SelectArgs a, int room) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = blockIdx.x * (blockDim.x >> 6) + wave;
+  if (t >= a.T) return;
+  if (a.mask && !a.mask[t]) {
+    put_picks(a, t, lane, -1, 0.f);
     return;
   }
-  select_token_f64(a, t, lane, c);
+  unsigned char* mine = lds + size_t(wave) * room;
+  float x[EPL], c[EPL];
+  load_row<EPL, V>(a.logits + size_t(t) * a.E, a.E, lane, -INFINITY, x);
+  if (a.bias) {
+    load_row<EPL, V>(a.bias, a.E, lane, 0.f, c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) c[i] = 0.f;
+  }
+  float m = -INFINITY;  // (of those that are numbers)
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) m = fmaxf(m, x[i]);
+  m = __ockl_wfred_max_f32(m);
+  if (m == -INFINITY) {  // every expert is off
+    put_picks(a, t, lane, -1, 0.f);
+    return;
+  }
+  // serr: bound of the error of a score.  Softmax: a score is off by its share of (|x - m| + 6 of
+  // exp and products, EPL + 10 of the sum) 2^-24, s |x - m| at most 0.37 of the largest; sigmoid: by
+  // (1 - s) (1.5 |x| + 2) + 3 of it, s (1 - s) |x| at most that of the largest logit if it is below -1.
+  float sum = 1.f, serr;
+  if (a.score == LC_MOE_SOFTMAX) {
+    float e[EPL];
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      e[i] = exp_neg(x[i] - m);
+      sum += e[i];
+    }
+    sum = __ockl_wfred_add_f32(sum);
+    const float rs = 1.f / sum;
+    serr = rs * (EPL + 17) * 0x1p-24f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) c[i] = x[i] > -INFINITY ? fmaxf(fmaf(e[i], rs, c[i]), -INFINITY) : -INFINITY;  // (NaN: off)
+  } else {
+    const float top = 1.f / (1.f + __builtin_amdgcn_exp2f(m * -1.44269504f));
+    serr = top * (8.f + 2.f * fmaxf(-m, 0.f)) * 0x1p-24f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x[i] * -1.44269504f));
+      c[i] = x[i] > -INFINITY ? fmaxf(s + c[i], -INFINITY) : -INFINITY;
+    }
+  }
+
+  bool whole = false;  // the token has to be taken in fp64
+  if (a.top_groups < a.groups) {
+    float* row = reinterpret_cast<float*>(mine);
+#pragma unroll
+    for (int j = 0; j < EPL / V; ++j) {
+      const int e = (j * 64 + lane) * V;
+      if (e < a.E) {
+        if constexpr (V == 4)
+          *reinterpret_cast<float4*>(row + e) = make_float4(c[4 * j], c[4 * j + 1], c[4 * j + 2], c[4 * j + 3]);
+        else
+          row[e] = c[j];
+      }
+    }
+    wave_fence();
+    // 64 / (groups rounded up to a power of two) lanes a group
+    const int sh = a.groups > 32 ? 0 : a.groups > 16 ? 1 : a.groups > 8 ? 2 : a.groups > 4 ? 3 : a.groups > 2 ? 4 : 5;
+    const int g = lane >> sh, part = 1 << sh;
+    float m1 = -INFINITY, m2 = -INFINITY;
+    if (g < a.groups) {
+      const float* run = row + g * a.size;
+      auto take = [&](float v) {
+        m2 = fmaxf(m2, fminf(m1, v));
+        m1 = fmaxf(m1, v);
+      };
+      if (a.size % 4 == 0) {
+        for (int e = (lane & (part - 1)) * 4; e < a.size; e += part * 4) {
+          const float4 q = *reinterpret_cast<const float4*>(run + e);
+          take(q.x), take(q.y), take(q.z), take(q.w);
+        }
+      } else {
+        for (int e = lane & (part - 1); e < a.size; e += part) take(run[e]);
+      }
+    }
+    for (int o = 1; o < part; o <<= 1) {
+      const float o1 = __shfl_xor(m1, o), o2 = __shfl_xor(m2, o);
+      m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+      m1 = fmaxf(m1, o1);
+    }
+    const bool two = a.rank == 2 && m2 > -INFINITY;
+    const float best = two ? m1 + m2 : m1;
+    int before = 0;  // groups ahead of the lane's
+    for (int j = 0; j < a.groups; ++j) {
+      const float bj = lane_value(best, j << sh);
+      before += (bj > best || (bj == best && j < g)) ? 1 : 0;
+    }
+    const bool kept = before < a.top_groups;
+    // half a step of every fp32 value that went into a group's score, and its scores' errors
+    const float err = m1 > -INFINITY ? (two ? 2.f * serr + (fabsf(m1) + fabsf(m2) + fabsf(best)) * 0x1.1p-24f
+                                            : serr + fabsf(m1) * 0x1.1p-24f) : 0.f;
+    const float least = -__ockl_wfred_max_f32(kept || g >= a.groups ? -(kept ? best - err : INFINITY) : -INFINITY);
+    const float most = __ockl_wfred_max_f32(kept || g >= a.groups ? -INFINITY : best + err);
+    wave_fence();
+    whole = most > -INFINITY && !(least > most);
+    const unsigned long long live = __ballot(kept);
+    const uint32_t magic = uint32_t((0x100000000ull + a.size - 1) / a.size);  // e / size, exact for e, size < 2^16
+    auto keep = [&](int e) {
+      const int ge = a.size == 1 ? e : int(__umulhi(uint32_t(e), magic));
+      return e < a.E && (live >> ((ge << sh) & 63) & 1);
+    };
+    if (V == 4 && a.size % 4 == 0) {  // four experts of a lane are of one group
+#pragma unroll
+      for (int j = 0; j < EPL / V; ++j) {
+        const bool in = keep((j * 64 + lane) * V);
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[j * V + i] = in ? c[j * V + i] : -INFINITY;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) c[i] = keep(((i / V) * 64 + lane) * V + i % V) ? c[i] : -INFINITY;
+    }
+  }
+
+  // ---- what may be picked ----
+  // A candidate is (c, expert, logit).
+  float* g_c = reinterpret_cast<float*>(mine);
+  int* g_e = reinterpret_cast<int*>(mine + 512);
+  float* g_x = reinterpret_cast<float*>(mine + 768);
+  float lm = c[0];  // the lane's largest
+#pragma unroll
+  for (int i = 1; i < EPL; ++i) lm = fmaxf(lm, c[i]);
+  int n = 65;
+  for (int parts = EPL == 1 ? 1 : a.K <= 16 ? 16 : 64; !whole; parts = 64) {
+    float kth = -INFINITY;
+    if constexpr (EPL > 1) {
+      int before = 0;
+      float pm = lm;  // largest of the lane's part
+      if (parts == 16) {
+        pm = fmaxf(pm, __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(pm), 0xB1, 0xF, 0xF, true)));  // lanes 1 0 3 2
+        pm = fmaxf(pm, __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(pm), 0x4E, 0xF, 0xF, true)));  // lanes 2 3 0 1
+#pragma unroll
+        for (int j = 0; j < 16; ++j) before += lane_value(pm, 4 * j) > pm ? 1 : 0;
+      } else {
+#pragma unroll 8
+        for (int j = 0; j < 64; ++j) before += lane_value(pm, j) > pm ? 1 : 0;
+      }
+      kth = -__ockl_wfred_max_f32(before < a.K ? -pm : -INFINITY);
+    }
+    // (what is off is below every bound)
+    const float bound = kth > -INFINITY ? kth - 2.f * serr - fabsf(kth) * 0x1p-22f : -__FLT_MAX__;
+    n = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const bool in = c[i] >= bound;
+      const unsigned long long at = __ballot(in);
+      // (places from 64 on come round again: they are then gathered anew)
+      const int place = __builtin_amdgcn_mbcnt_hi(uint32_t(at >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(at), n)) & 63;
+      if (in) {
+        g_c[place] = c[i];
+        g_e[place] = ((i / V) * 64 + lane) * V + i % V;
+        g_x[place] = x[i];
+      }
+      n += __popcll(at);
+    }
+    wave_fence();
+    if (n <= 64 || parts != 16) break;
+  }
+  if (n > 64) {
+    select_token_f64(a, t, lane, reinterpret_cast<double*>(mine));
+    return;
+  }
+  float vc = lane < n ? g_c[lane] : -INFINITY, vx = g_x[lane];
+  int ve = g_e[lane];
+  wave_fence();
+  // Sorted one k in lane k.
+  auto put = [&](int place) {
+    if (lane < n) {
+      g_e[place] = ve;
+      g_x[place] = vx;
+    }
+  };
+  auto get = [&]() {
+    wave_fence();
+    ve = g_e[lane];
+    vx = g_x[lane];
+    wave_fence();
+  };
+  int place = place_of(vc, ve, n, lane);
+  put(place);
+  if (lane < n) g_c[place] = vc;
+  get();
+  vc = g_c[lane];
+  // (the last lane has no next one; a place behind the last candidate does not count)
+  const float next = __shfl_down(vc, 1);
+  const bool near = lane < a.K && lane + 1 < n && vc - next <= 2.f * serr + (fabsf(vc) + fabsf(next)) * 0x1.1p-24f;
+  if (__ballot(near)) {
+    double sum64 = 1.0;
+    if (a.score == LC_MOE_SOFTMAX) {
+      sum64 = 0.0;
+#pragma unroll 1
+      for (int e = lane; e < a.E; e += 64) {
+        const float l = a.logits[size_t(t) * a.E + e];
+        sum64 += l > -INFINITY ? exp(l - double(m)) : 0.0;
+      }
+      sum64 = wave_sum(sum64);
+    }
+    double c64 = 0.0;
+    if (lane < n) {
+      const double s = a.score == LC_MOE_SOFTMAX ? exp(vx - double(m)) / sum64 : 1.0 / (1.0 + exp(-double(vx)));
+      c64 = s + (a.bias ? a.bias[ve] : 0.f);
+    }
+    put(place_of(c64, ve, n, lane));
+    get();
+  }
+  const bool valid = lane < n && lane < a.K;
+  const float g = pick_gate(a, valid, valid ? vx : 0.f, m, sum);
+  put_picks(a, t, lane, valid ? ve : -1, g);
+}
+
+template <int EPL, int V>
+static void select_launch(const SelectArgs& a, hipStream_t st) {
+  // a wave's room: E fp64 scores (a token that is taken in fp64), or 64 candidates
+  const int room = (a.E * 8 > 1024 ? a.E * 8 : 1024) + 15 & ~15;
+  int waves = 4;
+  while (waves > 1 && (waves * room > 32768 || (a.T + waves - 1) / waves < 256)) waves /= 2;
+  select_kernel<EPL, V><<<dim3((a.T + waves - 1) / waves), dim3(waves * 64), waves * room, st>>>(a, room);
 }
 
 hipError_t launch_select(const lc_moe_shape& s, const lc_moe_gating& g, const float* logits, const float* bias,
@@ -125,7 +392,22 @@ hipError_t launch_select(const lc_moe_shape& s, const lc_moe_gating& g, const fl
   const int E = s.N + s.Z;
   const SelectArgs a{logits, bias, mask, idx, gate, s.T, E, s.K, g.score, g.groups, E / g.groups, g.top_groups,
                      g.group_rank, g.renorm != 0, g.scale};
-  select_kernel<<<dim3(s.T), dim3(64), size_t(E) * 8, st>>>(a);
+  if (E % 4 == 0) {
+    if (E <= 256) select_launch<4, 4>(a, st);
+    else if (E <= 512) select_launch<8, 4>(a, st);
+    else if (E <= 768) select_launch<12, 4>(a, st);
+    else if (E <= 1024) select_launch<16, 4>(a, st);
+    else if (E <= 2048) select_launch<32, 4>(a, st);
+    else select_launch<64, 4>(a, st);
+  } else {
+    if (E <= 64) select_launch<1, 1>(a, st);
+    else if (E <= 128) select_launch<2, 1>(a, st);
+    else if (E <= 256) select_launch<4, 1>(a, st);
+    else if (E <= 512) select_launch<8, 1>(a, st);
+    else if (E <= 1024) select_launch<16, 1>(a, st);
+    else if (E <= 2048) select_launch<32, 1>(a, st);
+    else select_launch<64, 1>(a, st);
+  }
   return hipGetLastError();
 }
 
