@@ -125,26 +125,23 @@ __device__ __forceinline__ double lane_value(double v, int lane) {
 }
 __device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
-// Of the n values c of lanes 0 .. n-1 (n <= 64; -infinity in the lanes behind): how many are ahead of
-// the lane's in descending order, equal ones in the order of their experts e (F = double), or of
-// their lanes (float: their order is then settled in fp64).
-template <typename F>
-__device__ __forceinline__ int place_of(F c, int e, int n, int lane) {
+// Of the n values c of lanes 0 .. n-1 (n <= 64): how many are ahead of the lane's in descending order,
+// equal ones in the order of their experts e.
+__device__ __forceinline__ int place_of(double c, int e, int n) {
   int place = 0;
-  if constexpr (sizeof(F) == 8) {
-    for (int j = 0; j < n; ++j) {
-      const double cj = lane_value(c, j);
-      const int ej = __builtin_amdgcn_readlane(e, j);
-      place += (cj > c || (cj == c && ej < e)) ? 1 : 0;
-    }
-  } else {
-    for (int j = 0; j < n; j += 4) {
+  for (int j = 0; j < n; ++j) {
+    const double cj = lane_value(c, j);
+    const int ej = __builtin_amdgcn_readlane(e, j);
+    place += (cj > c || (cj == c && ej < e)) ? 1 : 0;
+  }
+  return place;
+}
+// The same in fp32 (-infinity in the lanes behind), but that equal ones get one place.
+__device__ __forceinline__ int place_of(float c, int n) {
+  int place = 0;
+  for (int j = 0; j < n; j += 4) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float cj = lane_value(c, j + i);
-        place += (lane > j + i ? cj >= c : cj > c) ? 1 : 0;
-      }
-    }
+    for (int i = 0; i < 4; ++i) place += lane_value(c, j + i) > c ? 1 : 0;
   }
   return place;
 }
@@ -186,6 +183,8 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a, int room) {
   // serr: bound of the error of a score.  Softmax: a score is off by its share of (|x - m| + 6 of
   // exp and products, EPL + 10 of the sum) 2^-24, s |x - m| at most 0.37 of the largest; sigmoid: by
   // (1 - s) (1.5 |x| + 2) + 3 of it, s (1 - s) |x| at most that of the largest logit if it is below -1.
+  // What is off becomes -infinity: x 0 is NaN for it, and so is a NaN bias, and the larger of NaN and
+  // -infinity is that.
   float sum = 1.f, serr;
   if (a.score == LC_MOE_SOFTMAX) {
     float e[EPL];
@@ -199,14 +198,14 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a, int room) {
     const float rs = 1.f / sum;
     serr = rs * (EPL + 17) * 0x1p-24f;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) c[i] = x[i] > -INFINITY ? fmaxf(fmaf(e[i], rs, c[i]), -INFINITY) : -INFINITY;  // (NaN: off)
+    for (int i = 0; i < EPL; ++i) c[i] = fmaxf(fmaf(x[i], 0.f, fmaf(e[i], rs, c[i])), -INFINITY);
   } else {
     const float top = 1.f / (1.f + __builtin_amdgcn_exp2f(m * -1.44269504f));
     serr = top * (8.f + 2.f * fmaxf(-m, 0.f)) * 0x1p-24f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x[i] * -1.44269504f));
-      c[i] = x[i] > -INFINITY ? fmaxf(s + c[i], -INFINITY) : -INFINITY;
+      c[i] = fmaxf(fmaf(x[i], 0.f, s + c[i]), -INFINITY);
     }
   }
 
@@ -253,7 +252,7 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a, int room) {
     int before = 0;  // groups ahead of the lane's
     for (int j = 0; j < a.groups; ++j) {
       const float bj = lane_value(best, j << sh);
-      before += (bj > best || (bj == best && j < g)) ? 1 : 0;
+      before += (g > j ? bj >= best : bj > best) ? 1 : 0;
     }
     const bool kept = before < a.top_groups;
     // half a step of every fp32 value that went into a group's score, and its scores' errors
@@ -289,7 +288,8 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a, int room) {
   float* g_x = reinterpret_cast<float*>(mine + 768);
   float lm = c[0];  // the lane's largest
 #pragma unroll
-  for (int i = 1; i < EPL; ++i) lm = fmaxf(lm, c[i]);
+  for (int i = 1; i + 1 < EPL; i += 2) lm = fmaxf(lm, fmaxf(c[i], c[i + 1]));
+  if constexpr (EPL % 2 == 0) lm = fmaxf(lm, c[EPL - 1]);
   int n = 65;
   for (int parts = EPL == 1 ? 1 : a.K <= 16 ? 16 : 64; !whole; parts = 64) {
     float kth = -INFINITY;
@@ -346,15 +346,20 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a, int room) {
     vx = g_x[lane];
     wave_fence();
   };
-  int place = place_of(vc, ve, n, lane);
+  const int place = place_of(vc, n);
+  const int was = ve;
   put(place);
   if (lane < n) g_c[place] = vc;
-  get();
-  vc = g_c[lane];
-  // (the last lane has no next one; a place behind the last candidate does not count)
-  const float next = __shfl_down(vc, 1);
-  const bool near = lane < a.K && lane + 1 < n && vc - next <= 2.f * serr + (fabsf(vc) + fabsf(next)) * 0x1.1p-24f;
-  if (__ballot(near)) {
+  wave_fence();
+  // Where two are as good as equal, or equal (one place for both: one finds the other there), fp64
+  // decides.  (The last lane has no next one; a place behind the last candidate does not count.)
+  const float next = g_c[lane < 63 ? lane + 1 : 63], mine_c = g_c[lane];
+  const bool near = lane < n && (g_e[place] != was || (lane < a.K && lane + 1 < n && mine_c - next <=
+                                 2.f * serr + (fabsf(mine_c) + fabsf(next)) * 0x1.1p-24f));
+  if (!__ballot(near)) {
+    get();
+  } else {
+    wave_fence();
     double sum64 = 1.0;
     if (a.score == LC_MOE_SOFTMAX) {
       sum64 = 0.0;
@@ -370,7 +375,7 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a, int room) {
       const double s = a.score == LC_MOE_SOFTMAX ? exp(vx - double(m)) / sum64 : 1.0 / (1.0 + exp(-double(vx)));
       c64 = s + (a.bias ? a.bias[ve] : 0.f);
     }
-    put(place_of(c64, ve, n, lane));
+    put(place_of(c64, ve, n));
     get();
   }
   const bool valid = lane < n && lane < a.K;
