@@ -187,7 +187,7 @@ lc_moe_status lc_moe_quantize_matrix(const void* x, int32_t rows, int32_t cols, 
  * NULL, or out itself); N a multiple of 8.  The products of codes are exact; the FP8 matrix cores
  * add 64 of them and the fp32 accumulator with about 12 bits below the largest addend (see
  * lc_moe_quantize_activations); add is added in fp32 and the sum rounded once.  M = 0 does
- * nothing. */
+ * nothing.  M, N and K are limited as a matrix's sizes are, M and N together too. */
 size_t lc_moe_matmul_fp8_workspace_size(int32_t M, int32_t N, int32_t K);
 lc_moe_status lc_moe_matmul_fp8(int32_t M, int32_t N, int32_t K, const void* a, const void* b,
                                 const void* add, void* out, void* workspace,

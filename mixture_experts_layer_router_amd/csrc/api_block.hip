@@ -46,13 +46,10 @@ bool matrix_ok(int rows, int cols) {
   const size_t rp = (size_t(rows) + 255) / 256 * 256, cp = (size_t(cols) + 127) / 128 * 128;
   return rp * cp <= size_t(1) << 37;
 }
-// The product's operands exist, and its grids fit the device's.
+// The product's operands exist, and its tiles can be counted.
 bool matmul_ok(int M, int N, int K) {
-  if (N < 8 || N % 8 != 0 || !matrix_ok(M < 1 ? 1 : M, K) || !matrix_ok(N, K)) return false;
-  const MatmulPlan p = plan_matmul_fp8(M < 1 ? 1 : M, N, K);
-  const size_t lim = 0xFFFFFFFFull, m = M;
-  const size_t tiles = ((m + 127) / 128) * ((size_t(N) + 127) / 128);
-  return tiles <= lim / 512 / p.splits && m * N / 8 + 256 <= lim;
+  const int m = M < 1 ? 1 : M;
+  return N >= 8 && N % 8 == 0 && matrix_ok(m, K) && matrix_ok(N, K) && matrix_ok(m, N);
 }
 lc_moe_status check_overlap(const void* a, const void* b) { return a && a == b ? LC_MOE_E_SHAPE : LC_MOE_OK; }
 
@@ -286,14 +283,17 @@ lc_moe_status lc_moe_linear_fp8_backward(int32_t T, int32_t k, int32_t n, const 
   LCM_CHECK(check_space(workspace, workspace_bytes, p.total));
   if (!dx && !dw) return LC_MOE_OK;
   void *dyq = at<void>(workspace, p.dy), *dyt = at<void>(workspace, p.dyt), *xt = at<void>(workspace, p.xt);
-  LCM_LAUNCH(launch_quantize_matrix(dy, T, n, 1, dx ? dyq : nullptr, dw ? dyt : nullptr, stream));
-  if (dw) LCM_LAUNCH(launch_quantize_matrix(x, T, k, 1, nullptr, xt, stream));
+  char* mm = at<char>(workspace, p.mm);
+  if (!dw) {
+    LCM_LAUNCH(launch_quantize_matrix(dy, T, n, 1, dyq, nullptr, stream));
+    LCM_LAUNCH(launch_matmul_fp8(T, k, n, plan_matmul_fp8(T, k, n), mm, dyq, w_t, dx_add, dx, stream));
+    return LC_MOE_OK;
+  }
+  LCM_LAUNCH(launch_quantize_gradients(dy, T, n, dx ? dyq : nullptr, dyt, x, k, xt, stream));
   if (dx)
-    LCM_LAUNCH(launch_matmul_fp8(T, k, n, plan_matmul_fp8(T, k, n), at<char>(workspace, p.mm), dyq, w_t, dx_add, dx,
-                                 stream));
-  if (dw)
-    LCM_LAUNCH(launch_matmul_fp8(n, k, T, plan_matmul_fp8(n, k, T), at<char>(workspace, p.mm), dyt, xt, nullptr, dw,
-                                 stream));
+    LCM_LAUNCH(launch_matmul_gradients(T, k, n, mm, dyq, w_t, dx_add, dx, dyt, xt, dw, stream));
+  else
+    LCM_LAUNCH(launch_matmul_fp8(n, k, T, plan_matmul_fp8(n, k, T), mm, dyt, xt, nullptr, dw, stream));
   return LC_MOE_OK;
 }
 

@@ -54,13 +54,22 @@ __host__ __device__ __forceinline__ size_t fp8_scale_at(size_t r) {
 hipError_t launch_quantize_matrix(const void* x, int rows, int cols, int block_rows, void* out, void* out_t,
                                   hipStream_t st);
 
+// dy [T][n] by its rows (dyq, may be null) and columns (dyt), x [T][k] by its columns (xt), in blocks of
+// 128 x 1.
+hipError_t launch_quantize_gradients(const void* dy, int T, int n, void* dyq, void* dyt, const void* x, int k, void* xt,
+                                     hipStream_t st);
+
 struct MatmulPlan {
   size_t part, total;
   int splits, chunk;  // pieces of the reduction, runs of 128 of each
-  int form;
+  int form;           // tile (fp8_matmul.hip)
 };
 MatmulPlan plan_matmul_fp8(int M, int N, int K);
 hipError_t launch_matmul_fp8(int M, int N, int K, const MatmulPlan& p, void* ws, const void* a, const void* b,
                              const void* add, void* out, hipStream_t st);
+// A linear layer's gradients: dx [T][k] = dyq w_t^T (+ add) and dw [n][k] = dyt xt^T, in one launch where both
+// take the same small tiles.  ws: room for either's plan.
+hipError_t launch_matmul_gradients(int T, int k, int n, void* ws, const void* dyq, const void* w_t, const void* add,
+                                   void* dx, const void* dyt, const void* xt, void* dw, hipStream_t st);
 
 }  // namespace lcm

@@ -21,14 +21,18 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-struct MatmulArgs {
+struct Product {
   const unsigned char *a, *b;  // codes
   const unsigned char *as, *bs;
   size_t lda, ldb, las, lbs;
   const bf16_t* add;
   bf16_t* out;
-  float* part;
   int M, N, nkb, chunk, splits, mt, nt;
+};
+struct MatmulArgs {
+  Product p, q;  // the units of q follow those of p
+  int units_p, units;
+  float* part;
 };
 
 // Keep a value out of the compiler's sight, in scalar or vector registers: what is made of it is made
@@ -61,17 +65,18 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int byte
 constexpr int kGroup = 4;  // tiles of rows that are taken together
 
 // 2 x 2 waves; a wave holds MB x NB blocks of 32 x 32, as the transposes of C's blocks: a lane then
-// has four neighbouring columns of one row.
-template <int MB, int NB, int MODE>
-__global__ __launch_bounds__(256, MB == 4 ? 1 : 2) void matmul_fp8_kernel(MatmulArgs p) {
+// has four neighbouring columns of one row.  TWO: the units of two products.
+template <int MB, int NB, int MODE, bool TWO>
+__global__ __launch_bounds__(256, MB == 4 ? 1 : 2) void matmul_fp8_kernel(MatmulArgs g) {
   constexpr int BM = MB * 64, BN = NB * 64;
   constexpr int ROWS = (BM + BN) * 128, STAGE = ROWS + 512;  // codes of A, of B, 256 scale bytes of each
   constexpr int LA = BM / 32, LB = BN / 32;                  // loads a wave and stage: 8 rows each
   constexpr int PER = LA + LB + 1;
   constexpr int NP = MB * NB;                                // products of a substep
-  // Room of a wave for results on their way out: 64 columns of 32 rows, of 16 where two workgroups
-  // have to fit a CU.
-  constexpr int OUT_ROWS = MB == 4 ? 32 : 16, OUT = OUT_ROWS * 128;
+  // Room of a wave for results on their way out: CB blocks of columns, 32 rows of them, or 16 where
+  // two workgroups have to fit a CU.
+  constexpr int CB = NB % 2 == 0 ? 2 : 1, OUT_ROWS = MB == 4 ? 32 : 16, OUT = OUT_ROWS * CB * 64;
+  constexpr bool WHOLE_RUNS = BM % 128 == 0 && BN % 128 == 0;  // tiles start at a run of 128 scales
   __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * STAGE + 4 * OUT];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -80,23 +85,26 @@ __global__ __launch_bounds__(256, MB == 4 ? 1 : 2) void matmul_fp8_kernel(Matmul
 
   // Every XCD takes a run of the units, in order: kGroup tiles of rows, then the columns, so that
   // the workgroups that run side by side on it share both operands in its L2.
-  const int tiles = p.mt * p.nt, units = tiles * p.splits, per_xcd = (units + 7) / 8;
-  const int first = (blockIdx.x & 7) * per_xcd, last = min(first + per_xcd, units);
+  const int per_xcd = (g.units + 7) / 8;
+  const int first = (blockIdx.x & 7) * per_xcd, last = min(first + per_xcd, g.units);
   const int step = int(gridDim.x >> 3);
 
+#define LCM_OF(unit, field) (TWO && (unit) >= g.units_p ? g.q.field : g.p.field)
   struct Unit {
     int split, m0, n0, k0, nk;
   };
-  auto unit_of = [&](int unit) {
+  auto unit_of = [&](int n) {
     Unit u;
-    u.split = unit / tiles;
-    const int tile = unit - u.split * tiles;
-    const int group = tile / (kGroup * p.nt), in = tile - group * (kGroup * p.nt);
-    const int high = min(kGroup, p.mt - group * kGroup);
+    const int mt = LCM_OF(n, mt), nt = LCM_OF(n, nt), chunk = LCM_OF(n, chunk);
+    const int in_product = TWO && n >= g.units_p ? n - g.units_p : n;
+    u.split = in_product / (mt * nt);
+    const int tile = in_product - u.split * (mt * nt);
+    const int group = tile / (kGroup * nt), in = tile - group * (kGroup * nt);
+    const int high = min(kGroup, mt - group * kGroup);
     u.n0 = in / high * BN;
     u.m0 = (group * kGroup + in % high) * BM;
-    u.k0 = u.split * p.chunk;
-    u.nk = min(p.chunk, p.nkb - u.k0);
+    u.k0 = u.split * chunk;
+    u.nk = min(chunk, LCM_OF(n, nkb) - u.k0);
     return u;
   };
   // The workgroup's stages are one stream through all its units; they are loaded two ahead.
@@ -104,21 +112,26 @@ __global__ __launch_bounds__(256, MB == 4 ? 1 : 2) void matmul_fp8_kernel(Matmul
   if (ahead >= last) return;
   int unit = ahead, to_load = 0;
   const unsigned char *pa, *pb, *ps;  // the stage's rows and scales
-  uint32_t off[LA + LB];              // the lane's pieces from there
+  size_t sstep = 0;
+  uint32_t off[LA + LB];  // the lane's pieces from there
+  int runs = 0;           // where the tile's scales start in their runs: row blocks of A, of B << 8
   auto open = [&]() {
     const Unit u = unit_of(ahead);
     to_load = u.nk;
-    pa = p.a + size_t(u.m0) * p.lda + size_t(u.k0) * 128;
-    pb = p.b + size_t(u.n0) * p.ldb + size_t(u.k0) * 128;
+    const size_t lda = LCM_OF(ahead, lda), ldb = LCM_OF(ahead, ldb), las = LCM_OF(ahead, las), lbs = LCM_OF(ahead, lbs);
+    pa = LCM_OF(ahead, a) + size_t(u.m0) * lda + size_t(u.k0) * 128;
+    pb = LCM_OF(ahead, b) + size_t(u.n0) * ldb + size_t(u.k0) * 128;
     // scales: two waves load A's, two B's (the same bytes: one count for all waves)
-    ps = (wave & 1) ? p.bs + size_t(u.k0) * p.lbs + u.n0 : p.as + size_t(u.k0) * p.las + u.m0;
-    const int lane = here(tid) & 63;
+    ps = (wave & 1) ? LCM_OF(ahead, bs) + size_t(u.k0) * lbs + (u.n0 & ~127)
+                    : LCM_OF(ahead, as) + size_t(u.k0) * las + (u.m0 & ~127);
+    sstep = (wave & 1) ? lbs : las;
+    if constexpr (!WHOLE_RUNS) runs = (u.m0 >> 5 & 3) | (u.n0 >> 5 & 3) << 8;
+    const int lane = here(tid) & 63, endA = LCM_OF(ahead, M) - u.m0 - 1, endB = LCM_OF(ahead, N) - u.n0 - 1;
 #pragma unroll
     for (int i = 0; i < LA + LB; ++i) {  // rows past the matrix read its last row and are not stored
       const bool isb = i >= LA;
       const int r = ((isb ? i - LA : i) * 4 + wave) * 8 + (lane >> 3);
-      const int end = (isb ? p.N - u.n0 : p.M - u.m0) - 1;
-      off[i] = uint32_t(min(r, end)) * uint32_t(isb ? p.ldb : p.lda) + (((lane & 7) ^ (r & 7)) << 4);
+      off[i] = uint32_t(min(r, isb ? endB : endA)) * uint32_t(isb ? ldb : lda) + (((lane & 7) ^ (r & 7)) << 4);
     }
   };
   auto load_one = [&](int i, unsigned char* st) {
@@ -133,7 +146,7 @@ __global__ __launch_bounds__(256, MB == 4 ? 1 : 2) void matmul_fp8_kernel(Matmul
   auto advance = [&](int by) {
     pa = here(pa + by * 128);
     pb = here(pb + by * 128);
-    ps = here(ps + by * ((wave & 1) ? p.lbs : p.las));
+    ps = here(ps + by * sstep);
   };
   // Behind the last stage of a unit: the next unit.  Behind the last of all it stays there: the loads
   // that nobody needs keep a wave's count of loads the same in every stage.
@@ -164,13 +177,21 @@ __global__ __launch_bounds__(256, MB == 4 ? 1 : 2) void matmul_fp8_kernel(Matmul
   i32x8 fa[2][MB], fb[2][NB];
   auto read_one = [&](const unsigned char* st, int ks, int i) {
     if (i < NB) fb[ks][i] = frag(st + (BM + (wn * NB + i) * 32) * 128, ks);
-    else fa[ks][i - NB] = frag(st + (wm * MB + i - NB) * 32 * 128, ks);
+    else if (i < MB + NB) fa[ks][i - NB] = frag(st + (wm * MB + i - NB) * 32 * 128, ks);
   };
-  // The scale bytes of the lane's rows in four row blocks of the tile: one word.  A wave of two
-  // blocks shifts its own down.
-  auto scales = [&](const unsigned char* sc, int block) {
-    const uint32_t w = __builtin_bit_cast(uint32_t, *reinterpret_cast<const bf16x2*>(sc + block / 4 * 128 + l32 * 4));
-    return int(w >> (block % 4 * 8));
+  // The scale bytes of the lane's rows in up to four row blocks from `block` of a run on: a word
+  // holds those of four row blocks from a multiple of four on.
+  auto scales = [&](const unsigned char* sc, int block, int count) {
+    const unsigned char* w = sc + block / 4 * 128 + l32 * 4;
+    const uint32_t lo = __builtin_bit_cast(uint32_t, *reinterpret_cast<const bf16x2*>(w));
+    if (count != 3) return int(lo >> (block % 4 * 8));
+    const uint32_t hi = __builtin_bit_cast(uint32_t, *reinterpret_cast<const bf16x2*>(w + 128));
+    return int(__builtin_amdgcn_alignbyte(hi, lo, block % 4));
+  };
+  int sa, sb;
+  auto read_scales = [&](const unsigned char* st, int runs) {
+    sa = scales(st + ROWS, wm * MB + (WHOLE_RUNS ? 0 : runs & 0xFF), MB);
+    sb = scales(st + ROWS + 256, wn * NB + (WHOLE_RUNS ? 0 : runs >> 8), NB);
   };
   f32x16 acc[MB][NB];
   auto product = [&](int ks, int k, int sa, int sb) {
@@ -199,9 +220,15 @@ __global__ __launch_bounds__(256, MB == 4 ? 1 : 2) void matmul_fp8_kernel(Matmul
 #pragma unroll
     for (int j = 0; j < NB; ++j) zero(acc[i][j]);
 
-  constexpr int HALF = NP / 2, EACH = (PER + NP - HALF - 1) / (NP - HALF);
+  // Products of the first substep before the barrier behind which its stage's place is free, and
+  // what goes beside each product: reads of operands, loads.
+  constexpr int HALF = NP > 1 ? NP / 2 : 1, REST = NP - HALF;
+  constexpr int READS = (MB + NB + HALF - 1) / HALF > 4 ? (MB + NB + HALF - 1) / HALF : 4;
+  constexpr int EACH = REST > 0 ? (PER + REST - 1) / REST : PER;
   open();
+  int runs0 = runs, runs1 = runs;  // of the stage at hand and the next
   for (int s = 0; s < 2; ++s) {
+    runs1 = runs;
 #pragma unroll
     for (int i = 0; i < PER; ++i) load_one(i, smem + s * STAGE);
     advance(by);
@@ -211,7 +238,7 @@ __global__ __launch_bounds__(256, MB == 4 ? 1 : 2) void matmul_fp8_kernel(Matmul
   block_barrier();
 #pragma unroll
   for (int i = 0; i < MB + NB; ++i) read_one(smem, 0, i);
-  int sa = scales(smem + ROWS, wm * MB), sb = scales(smem + ROWS + 256, wn * NB);
+  read_scales(smem, runs0);
   int slot = 0, left = unit_of(unit).nk;
   while (true) {
     // The stages up to the end of a unit, of this one or of the one that is being loaded.
@@ -230,17 +257,16 @@ __global__ __launch_bounds__(256, MB == 4 ? 1 : 2) void matmul_fp8_kernel(Matmul
       for (int k = 0; k < HALF; ++k) {
         product(0, k, sa, sb);
 #pragma unroll
-        for (int i = k * 4; i < k * 4 + 4; ++i)
-          if (i < MB + NB) read_one(st, 1, i);
+        for (int i = k * READS; i < k * READS + READS; ++i) read_one(st, 1, i);
         __builtin_amdgcn_sched_barrier(0);
       }
       wait_lds_reads();
       block_barrier();
 #pragma unroll
-      for (int k = HALF; k < NP; ++k) {
-        product(0, k, sa, sb);
+      for (int k = 0; k < (REST > 0 ? REST : 1); ++k) {
+        if (REST > 0) product(0, HALF + k, sa, sb);
 #pragma unroll
-        for (int i = (k - HALF) * EACH; i < (k - HALF) * EACH + EACH; ++i)
+        for (int i = k * EACH; i < k * EACH + EACH; ++i)
           if (i < PER) load_one(i, st);
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -252,12 +278,13 @@ __global__ __launch_bounds__(256, MB == 4 ? 1 : 2) void matmul_fp8_kernel(Matmul
 #pragma unroll
       for (int k = 0; k < NP; ++k) {  // (behind the last stage of all the reads find an old one: not used)
         product(1, k, ca, cb);
+        constexpr int NEXT = NP >= 4 ? 4 : MB + NB;
 #pragma unroll
-        for (int i = k * 4; i < k * 4 + 4; ++i)
-          if (i < MB + NB) read_one(sn, 0, i);
-        if (k == 2) sa = scales(sn + ROWS, wm * MB), sb = scales(sn + ROWS + 256, wn * NB);
+        for (int i = k * NEXT; i < k * NEXT + NEXT; ++i) read_one(sn, 0, i);
+        if (k == (NP > 2 ? 2 : 0)) read_scales(sn, runs1);
         __builtin_amdgcn_sched_barrier(0);
       }
+      if constexpr (!WHOLE_RUNS) runs1 = runs;
     }
     left -= n;
     to_load -= n;
@@ -265,15 +292,16 @@ __global__ __launch_bounds__(256, MB == 4 ? 1 : 2) void matmul_fp8_kernel(Matmul
     if (left > 0) continue;
     const Unit done = unit_of(unit);
     // Lane: row l32 of a block, columns 8 (r / 4) + 4 h + r % 4.  Rows and columns past the matrix
-    // are left out by the bounds of the buffer (32 rows of it), so that every unit stores as often.
+    // are left out by the bounds of the buffer (32 rows of it).
+    const int M = LCM_OF(unit, M), N = LCM_OF(unit, N);
     const int lane = here(tid) & 63, l32 = lane & 31, h = lane >> 5;
     unsigned char* room = smem + 2 * STAGE + wave * OUT;
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
-      const int row0 = done.m0 + (wm * MB + i) * 32, rows = max(min(p.M - row0, 32), 0);
-      const size_t first = size_t(rows ? row0 : 0) * p.N;
+      const int row0 = done.m0 + (wm * MB + i) * 32, rows = max(min(M - row0, 32), 0);
+      const size_t first = size_t(rows ? row0 : 0) * N;
       if constexpr (MODE == kPart) {
-        const auto dst = buffer(p.part + size_t(done.split) * p.M * p.N + first, rows * p.N * 4);
+        const auto dst = buffer(g.part + size_t(done.split) * M * N + first, rows * N * 4);
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
           hold(acc[i][j]);
@@ -282,25 +310,26 @@ __global__ __launch_bounds__(256, MB == 4 ? 1 : 2) void matmul_fp8_kernel(Matmul
             const int col = done.n0 + (wn * NB + j) * 32 + 8 * q + 4 * h;
             const f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
             __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), dst,
-                                                   col < p.N ? (l32 * p.N + col) * 4 : kNowhere, 0, 0);
+                                                   col < N ? (l32 * N + col) * 4 : kNowhere, 0, 0);
           }
           zero(acc[i][j]);
         }
         continue;
       }
-      // 64 columns at a time through the wave's room: out in whole lines.  16-byte piece c of row r is
-      // in slot c ^ (r & 7).
-      const auto dst = buffer(p.out + first, rows * p.N * 2);
-      const auto add = buffer(MODE == kAdd ? p.add + first : p.out, rows * p.N * 2);
+      // CB blocks of columns at a time through the wave's room: out in whole lines (CB = 2).  16-byte
+      // piece c of row r is in a slot that spreads eight rows (CB = 1: sixteen) over the banks.
+      auto slot_of = [](int r, int c) { return CB == 2 ? c ^ (r & 7) : c ^ (r >> 2 & 3); };
+      const auto dst = buffer(LCM_OF(unit, out) + first, rows * N * 2);
+      const auto add = buffer(MODE == kAdd ? LCM_OF(unit, add) + first : LCM_OF(unit, out), rows * N * 2);
 #pragma unroll
-      for (int jj = 0; jj < NB; jj += 2) {
+      for (int jj = 0; jj < NB; jj += CB) {
         const int col0 = done.n0 + (wn * NB + jj) * 32;
         __builtin_amdgcn_sched_barrier(0);
-        hold(acc[i][jj]);
-        hold(acc[i][jj + 1]);
-        uint2 w[2][4];
+        uint2 w[CB][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < CB; ++j) hold(acc[i][jj + j]);
+#pragma unroll
+        for (int j = 0; j < CB; ++j)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float v[4];
@@ -308,30 +337,32 @@ __global__ __launch_bounds__(256, MB == 4 ? 1 : 2) void matmul_fp8_kernel(Matmul
             for (int e = 0; e < 4; ++e) v[e] = acc[i][jj + j][4 * q + e];
             if constexpr (MODE == kAdd) {
               const int col = col0 + j * 32 + 8 * q + 4 * h;
-              const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(add, col < p.N ? (l32 * p.N + col) * 2 : kNowhere, 0, 0);
+              const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(add, col < N ? (l32 * N + col) * 2 : kNowhere, 0, 0);
               v[0] += __uint_as_float(w[0] << 16), v[1] += __uint_as_float(w[0] & 0xFFFF0000u);
               v[2] += __uint_as_float(w[1] << 16), v[3] += __uint_as_float(w[1] & 0xFFFF0000u);
             }
             w[j][q] = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
           }
-        zero(acc[i][jj]);
-        zero(acc[i][jj + 1]);
-        const int c = lane & 7, col = col0 + c * 8;
+#pragma unroll
+        for (int j = 0; j < CB; ++j) zero(acc[i][jj + j]);
+        constexpr int PIECES = CB * 4, AT_ONCE = 64 / PIECES;  // of a row; rows a store
+        const int c = lane % PIECES, col = col0 + c * 8;
 #pragma unroll
         for (int r0 = 0; r0 < 32; r0 += OUT_ROWS) {
           if (OUT_ROWS == 32 || l32 / OUT_ROWS * OUT_ROWS == r0) {
+            const int r = l32 % OUT_ROWS;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < CB; ++j)
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<uint2*>(room + l32 % OUT_ROWS * 128 + (((j * 4 + q) ^ (l32 & 7)) << 4) + h * 8) = w[j][q];
+                *reinterpret_cast<uint2*>(room + r * (CB * 64) + (slot_of(r, j * 4 + q) << 4) + h * 8) = w[j][q];
           }
           __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-          for (int it = 0; it < OUT_ROWS / 8; ++it) {
-            const int r = it * 8 + (lane >> 3);
-            const u32x4 w = *reinterpret_cast<const u32x4*>(room + r * 128 + ((c ^ (r & 7)) << 4));
-            __builtin_amdgcn_raw_buffer_store_b128(w, dst, col < p.N ? ((r0 + r) * p.N + col) * 2 : kNowhere, 0,
+          for (int it = 0; it < OUT_ROWS / AT_ONCE; ++it) {
+            const int r = it * AT_ONCE + lane / PIECES;
+            const u32x4 w = *reinterpret_cast<const u32x4*>(room + r * (CB * 64) + (slot_of(r, c) << 4));
+            __builtin_amdgcn_raw_buffer_store_b128(w, dst, col < N ? ((r0 + r) * N + col) * 2 : kNowhere, 0,
                                                    2);  // (streamed: nothing here reads it again)
           }
           __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -343,6 +374,7 @@ __global__ __launch_bounds__(256, MB == 4 ? 1 : 2) void matmul_fp8_kernel(Matmul
     left = unit_of(unit).nk;
   }
   LCM_WAIT_VMCNT(0);  // no load into this workgroup's LDS outlives it
+#undef LCM_OF
 }
 
 // out = sum of the pieces in order (+ add), 8 elements a thread.
@@ -369,49 +401,101 @@ __global__ __launch_bounds__(256) void matmul_join_kernel(const float* __restric
       make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
+// Tiles of mb x nb times 64 x 64, and what they take (us, measured): a stage with 1 .. fit workgroups
+// on a CU, and a unit's results.  M = 16384, N = K = 6144: 500 us in 256 x 256 tiles, 513 in 256 x 192;
+// M = 2048, N = 6144, K = 16384, 192 or 256 of them: 193 and 171; M = 1024, N = 4096, K = 1536: 23 us, 20,
+// 12.3 (128 x 128), 14.7 (64 x 64); M = N = K = 1000: 17.9, 16.0, 9.8, 6.8.
+struct Form {
+  int mb, nb, fit;
+  float stage[4], out;
+};
+constexpr Form kForms[] = {{4, 4, 1, {1.7f}, 1.5f},
+                           {4, 3, 1, {1.3f}, 1.2f},
+                           {2, 2, 2, {0.6f, 1.05f}, 0.5f},
+                           {1, 1, 4, {0.35f, 0.5f, 0.7f, 0.92f}, 0.2f}};
+
 MatmulPlan plan_matmul_fp8(int M, int N, int K) {
   MatmulPlan p{};
   const int nkb = (K + 127) / 128;
-  const size_t t256 = size_t((M + 255) / 256) * ((N + 255) / 256), t128 = size_t((M + 127) / 128) * ((N + 127) / 128);
-  p.form = t256 >= 192 ? 0 : 1;
-  const size_t tiles = p.form == 0 ? t256 : t128;
-  size_t want = p.form == 0 ? 1 : 512 / tiles;
-  if (want > size_t(nkb)) want = nkb;
-  if (want < 1) want = 1;
-  p.chunk = int((nkb + want - 1) / want);
+  // The form and the number of pieces of the reduction that take the least by these figures; pieces
+  // are joined by a second kernel (2.5 us, their bytes at 5 TB/s): M = 64, N = K = 6144 takes 14 us in
+  // four pieces, 20 in one.
+  double best = 1e30;
+  for (int f = 0; f < 4; ++f) {
+    const Form& o = kForms[f];
+    const size_t tiles = ((size_t(M) + o.mb * 64 - 1) / (o.mb * 64)) * ((size_t(N) + o.nb * 64 - 1) / (o.nb * 64));
+    for (int want : {1, 2, 3, 4, 6, 8, 12, 16, 24}) {
+      const int chunk = (nkb + want - 1) / want, splits = (nkb + chunk - 1) / chunk;
+      if (splits != want || (splits > 1 && tiles * splits > 1024)) continue;
+      const size_t each = (tiles * splits + 255) / 256;  // units of a CU
+      double t = double(each / o.fit) * o.stage[o.fit - 1];
+      if (each % o.fit) t += o.stage[each % o.fit - 1];
+      t = 4 + t * chunk + o.out * each;
+      if (splits > 1) t += 2.5 + double(splits) * M * N * 8 / 5e6;
+      if (t < best) best = t, p.form = f, p.chunk = chunk;
+    }
+  }
   p.splits = (nkb + p.chunk - 1) / p.chunk;
   p.part = 0;
   p.total = p.splits > 1 ? align256(size_t(p.splits) * M * N * 4) : 256;
   return p;
 }
 
-hipError_t launch_matmul_fp8(int M, int N, int K, const MatmulPlan& p, void* ws, const void* a, const void* b,
-                             const void* add, void* out, hipStream_t st) {
+static Product product_of(int M, int N, int K, const MatmulPlan& p, const void* a, const void* b, const void* add,
+                          void* out) {
   const Fp8Mat am = plan_fp8_mat(M, K), bm = plan_fp8_mat(N, K);
   const unsigned char *ac = static_cast<const unsigned char*>(a), *bc = static_cast<const unsigned char*>(b);
-  MatmulArgs g{ac, bc, ac + am.scales, bc + bm.scales, am.ldc, bm.ldc, am.lds, bm.lds,
-               static_cast<const bf16_t*>(add), static_cast<bf16_t*>(out), p.splits > 1 ? static_cast<float*>(ws) : nullptr,
-               M, N, am.nkb, p.chunk, p.splits, 0, 0};
-  const int bt = p.form == 0 ? 256 : 128;
-  g.mt = (M + bt - 1) / bt;
-  g.nt = (N + bt - 1) / bt;
+  const int tm = kForms[p.form].mb * 64, tn = kForms[p.form].nb * 64;
+  return Product{ac, bc, ac + am.scales, bc + bm.scales, am.ldc, bm.ldc, am.lds, bm.lds,
+                 static_cast<const bf16_t*>(add), static_cast<bf16_t*>(out), M, N, am.nkb, p.chunk, p.splits,
+                 (M + tm - 1) / tm, (N + tn - 1) / tn};
+}
+
+template <int MODE, bool TWO>
+static void launch_form(int form, const MatmulArgs& g, hipStream_t st) {
   // as many workgroups as run at once, in whole rounds of the XCDs
-  const size_t units = size_t(g.mt) * g.nt * p.splits, room = p.form == 0 ? 256 : 512;
-  const unsigned grid = unsigned((units < room ? (units + 7) / 8 * 8 : room));
-  const int mode = g.part ? kPart : add ? kAdd : kOut;
-#define LCM_FORM(B)                                                                                   \
-  do {                                                                                                \
-    if (mode == kPart) matmul_fp8_kernel<B, B, kPart><<<dim3(grid), dim3(256), 0, st>>>(g);         \
-    else if (mode == kAdd) matmul_fp8_kernel<B, B, kAdd><<<dim3(grid), dim3(256), 0, st>>>(g);      \
-    else matmul_fp8_kernel<B, B, kOut><<<dim3(grid), dim3(256), 0, st>>>(g);                        \
-  } while (0)
-  if (p.form == 0) LCM_FORM(4);
-  else LCM_FORM(2);
-#undef LCM_FORM
+  const int room = form <= 1 ? 256 : form == 2 ? 512 : 1024;
+  const dim3 grid(unsigned(g.units < room ? (g.units + 7) / 8 * 8 : room)), block(256);
+  switch (form) {
+    case 0: if constexpr (!TWO) matmul_fp8_kernel<4, 4, MODE, TWO><<<grid, block, 0, st>>>(g); break;
+    case 1: if constexpr (!TWO) matmul_fp8_kernel<4, 3, MODE, TWO><<<grid, block, 0, st>>>(g); break;
+    case 2: matmul_fp8_kernel<2, 2, MODE, TWO><<<grid, block, 0, st>>>(g); break;
+    default: matmul_fp8_kernel<1, 1, MODE, TWO><<<grid, block, 0, st>>>(g); break;
+  }
+}
+
+hipError_t launch_matmul_fp8(int M, int N, int K, const MatmulPlan& p, void* ws, const void* a, const void* b,
+                             const void* add, void* out, hipStream_t st) {
+  MatmulArgs g{};
+  g.p = product_of(M, N, K, p, a, b, add, out);
+  g.units = g.units_p = g.p.mt * g.p.nt * p.splits;
+  g.part = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
+  if (g.part) launch_form<kPart, false>(p.form, g, st);
+  else if (add) launch_form<kAdd, false>(p.form, g, st);
+  else launch_form<kOut, false>(p.form, g, st);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   const size_t n = size_t(M) * N;
-  matmul_join_kernel<<<dim3(unsigned((n / 8 + 255) / 256)), dim3(256), 0, st>>>(g.part, p.splits, n, g.add, g.out);
+  matmul_join_kernel<<<dim3(unsigned((n / 8 + 255) / 256)), dim3(256), 0, st>>>(g.part, p.splits, n, g.p.add, g.p.out);
+  return hipGetLastError();
+}
+
+hipError_t launch_matmul_gradients(int T, int k, int n, void* ws, const void* dyq, const void* w_t, const void* add,
+                                   void* dx, const void* dyt, const void* xt, void* dw, hipStream_t st) {
+  const MatmulPlan px = plan_matmul_fp8(T, k, n), pw = plan_matmul_fp8(n, k, T);
+  // One launch instead of two (4 us of the host's time, and the second's start) for products that
+  // leave the chip room: T = 777, k = 1032, n = 520.
+  const bool one = px.form == pw.form && px.form >= 2 && px.splits == 1 && pw.splits == 1 && !add;
+  if (!one) {
+    const hipError_t e = launch_matmul_fp8(T, k, n, px, ws, dyq, w_t, add, dx, st);
+    return e != hipSuccess ? e : launch_matmul_fp8(n, k, T, pw, ws, dyt, xt, nullptr, dw, st);
+  }
+  MatmulArgs g{};
+  g.p = product_of(n, k, T, pw, dyt, xt, nullptr, dw);
+  g.q = product_of(T, k, n, px, dyq, w_t, nullptr, dx);
+  g.units_p = g.p.mt * g.p.nt;
+  g.units = g.units_p + g.q.mt * g.q.nt;
+  launch_form<kOut, true>(px.form, g, st);
   return hipGetLastError();
 }
 

@@ -22,17 +22,27 @@ __device__ __forceinline__ uint32_t fp8_codes(float a, float b, float c, float d
   return uint32_t(q);
 }
 
-// BLOCK: one scale for the whole tile.  ROWS, COLS: the matrix, its transpose is written.
+struct QuantizeArgs {
+  const bf16_t* x;
+  int rows, cols;
+  Fp8Mat m, mt;
+  unsigned char *out, *out_t;
+  int tiles;
+};
+
+// Tile number `tile` of one matrix.  BLOCK: one scale for the whole tile.  ROWS, COLS: the matrix, its
+// transpose is written.
 template <bool BLOCK, bool ROWS, bool COLS>
-__global__ __launch_bounds__(256) void quantize_matrix_kernel(const bf16_t* __restrict__ x, int rows, int cols,
-                                                              Fp8Mat m, Fp8Mat mt,
-                                                              unsigned char* __restrict__ out,
-                                                              unsigned char* __restrict__ out_t) {
+__device__ __forceinline__ void quantize_tile(const QuantizeArgs& q, int tile_index) {
+  const bf16_t* __restrict__ x = q.x;
+  const int rows = q.rows, cols = q.cols;
+  const Fp8Mat m = q.m, mt = q.mt;
+  unsigned char *__restrict__ out = q.out, *__restrict__ out_t = q.out_t;
   __shared__ float colmax[16][128];
   __shared__ float wmax[4];
   // row stride 144: 16-byte pieces of eight rows in turn fall on different banks
   __shared__ __attribute__((aligned(16))) unsigned char tile[COLS ? 128 * 144 : 16];
-  const int cb = blockIdx.x % m.nkb, rb = blockIdx.x / m.nkb;
+  const int cb = tile_index % m.nkb, rb = tile_index / m.nkb;
   const int tid = threadIdx.x, rg = tid >> 4, cg = tid & 15;
   const int r0 = rb * 128 + rg * 8, c0 = cb * 128 + cg * 8;
   float v[8][8];
@@ -138,12 +148,30 @@ __global__ __launch_bounds__(256) void quantize_matrix_kernel(const bf16_t* __re
   }
 }
 
+template <bool BLOCK, bool ROWS, bool COLS>
+__global__ __launch_bounds__(256) void quantize_matrix_kernel(QuantizeArgs q) {
+  quantize_tile<BLOCK, ROWS, COLS>(q, blockIdx.x);
+}
+
+// A product's gradients in one launch: dy both ways, x by its columns (Q'(x) of dw).
+template <bool ROWS, bool COLS>
+__global__ __launch_bounds__(256) void quantize_gradients_kernel(QuantizeArgs dy, QuantizeArgs x) {
+  const int t = blockIdx.x;
+  if (t < dy.tiles) quantize_tile<false, ROWS, COLS>(dy, t);
+  else quantize_tile<false, false, true>(x, t - dy.tiles);
+}
+
+static QuantizeArgs quantize_args(const void* x, int rows, int cols, void* out, void* out_t) {
+  return QuantizeArgs{static_cast<const bf16_t*>(x), rows, cols, plan_fp8_mat(rows, cols), plan_fp8_mat(cols, rows),
+                      static_cast<unsigned char*>(out), static_cast<unsigned char*>(out_t),
+                      int(size_t((rows + 127) / 128) * ((cols + 127) / 128))};
+}
+
 hipError_t launch_quantize_matrix(const void* x, int rows, int cols, int block_rows, void* out, void* out_t,
                                   hipStream_t st) {
-  const dim3 grid(unsigned(size_t((rows + 127) / 128) * ((cols + 127) / 128))), block(256);
-  const bf16_t* in = static_cast<const bf16_t*>(x);
-  unsigned char *o = static_cast<unsigned char*>(out), *ot = static_cast<unsigned char*>(out_t);
-#define LCM_Q(B, R, C) quantize_matrix_kernel<B, R, C><<<grid, block, 0, st>>>(in, rows, cols, plan_fp8_mat(rows, cols), plan_fp8_mat(cols, rows), o, ot)
+  const QuantizeArgs q = quantize_args(x, rows, cols, out, out_t);
+  const dim3 grid(q.tiles), block(256);
+#define LCM_Q(B, R, C) quantize_matrix_kernel<B, R, C><<<grid, block, 0, st>>>(q)
   if (block_rows == 128) {
     if (out && out_t) LCM_Q(true, true, true);
     else if (out) LCM_Q(true, true, false);
@@ -154,6 +182,15 @@ hipError_t launch_quantize_matrix(const void* x, int rows, int cols, int block_r
     else if (out_t) LCM_Q(false, false, true);
   }
 #undef LCM_Q
+  return hipGetLastError();
+}
+
+hipError_t launch_quantize_gradients(const void* dy, int T, int n, void* dyq, void* dyt, const void* x, int k, void* xt,
+                                     hipStream_t st) {
+  const QuantizeArgs a = quantize_args(dy, T, n, dyq, dyt), b = quantize_args(x, T, k, nullptr, xt);
+  const dim3 grid(a.tiles + b.tiles), block(256);
+  if (dyq) quantize_gradients_kernel<true, true><<<grid, block, 0, st>>>(a, b);
+  else quantize_gradients_kernel<false, true><<<grid, block, 0, st>>>(a, b);
   return hipGetLastError();
 }
 
