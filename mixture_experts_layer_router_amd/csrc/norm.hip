@@ -42,14 +42,22 @@ constexpr int kNormMaxThreads = 1024;
 
 // Sums of C values over the workgroup, the same bits in every thread.  lds: two rooms used in
 // turn, so that one barrier is enough: a room is written again only behind the next sum's
-// barrier, which every thread reaches after it has read this one.
+// barrier, which every thread reaches after it has read this one.  Waves that are not there have
+// zeros in it (clear_sums).
+constexpr int kMaxWaves = kNormMaxThreads / 64;
+typedef float SumRoom[3][kMaxWaves];
+__device__ __forceinline__ void clear_sums(SumRoom (&lds)[2]) {
+  if (threadIdx.x < 2 * 3 * kMaxWaves) (&lds[0][0][0])[threadIdx.x] = 0.f;  // (a workgroup has 64 threads at least)
+  if (threadIdx.x < 2 * 3 * kMaxWaves - 64) (&lds[0][0][0])[threadIdx.x + 64] = 0.f;
+  __syncthreads();
+}
 template <int C>
-__device__ __forceinline__ void block_sums(float (&v)[C], float (*lds)[C][kNormMaxThreads / 64], int& turn) {
+__device__ __forceinline__ void block_sums(float (&v)[C], SumRoom (&lds)[2], int& turn) {
 #pragma unroll
   for (int c = 0; c < C; ++c) v[c] = __ockl_wfred_add_f32(v[c]);
   if (blockDim.x == 64) return;
   const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-  float(*room)[kNormMaxThreads / 64] = lds[turn];
+  SumRoom& room = lds[turn];
   turn ^= 1;
   if ((threadIdx.x & 63) == 0) {
 #pragma unroll
@@ -58,9 +66,11 @@ __device__ __forceinline__ void block_sums(float (&v)[C], float (*lds)[C][kNormM
   __syncthreads();
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    float s = 0.f;
-    for (int w = 0; w < waves; ++w) s += room[c][w];
-    v[c] = s;
+    v[c] = 0.f;
+    for (int w = 0; w < waves; w += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(&room[c][w]);
+      v[c] += (q.x + q.y) + (q.z + q.w);
+    }
   }
 }
 
@@ -101,8 +111,9 @@ struct NormArgs {
 template <typename E, int NV>
 __global__ __launch_bounds__(kNormMaxThreads) void block_norm_kernel(NormArgs p) {
   constexpr int N = Vec<E>::N;
-  __shared__ float lds[2][1][kNormMaxThreads / 64];
+  __shared__ __attribute__((aligned(16))) SumRoom lds[2];
   int turn = 0;
+  clear_sums(lds);
   float wpost[NV][N], wpre[NV][N], gc[NV][N];
   load_weights<E, NV>(p.w_post, p.d, 1.f, wpost);
   load_weights<E, NV>(p.w_pre, p.d, 0.f, wpre);
@@ -169,11 +180,11 @@ static hipError_t norm_forward(const NormArgs& p, hipStream_t st) {
   norm_shape(p.d, Vec<E>::N, threads, nv);
   const int wgs = 256 * (2048 / threads);
   const dim3 grid(p.T < wgs ? p.T : wgs), block(threads);
-  switch (nv) {
-    case 1: block_norm_kernel<E, 1><<<grid, block, 0, st>>>(p); break;
-    case 2: block_norm_kernel<E, 2><<<grid, block, 0, st>>>(p); break;
-    case 3: block_norm_kernel<E, 3><<<grid, block, 0, st>>>(p); break;
-    default: block_norm_kernel<E, 4><<<grid, block, 0, st>>>(p); break;
+  if (nv == 1) block_norm_kernel<E, 1><<<grid, block, 0, st>>>(p);
+  else if (nv == 2) block_norm_kernel<E, 2><<<grid, block, 0, st>>>(p);
+  else if constexpr (Vec<E>::N == 4) {  // (8 elements a vector: never more than two)
+    if (nv == 3) block_norm_kernel<E, 3><<<grid, block, 0, st>>>(p);
+    else block_norm_kernel<E, 4><<<grid, block, 0, st>>>(p);
   }
   return hipGetLastError();
 }
@@ -197,26 +208,41 @@ struct NormBwArgs {
   float a, b, eps, rd;
 };
 
-template <typename E, int NV>
-__global__ __launch_bounds__(kNormMaxThreads) void block_norm_backward_kernel(NormBwArgs p) {
+// NEXT: the next row is loaded beside the present one's sums.  KEEP: the weights stay in registers
+// (else they are read again, from the L2, in every row).
+template <typename E, int NV, int THREADS, bool NEXT, bool KEEP>
+__global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(NormBwArgs p) {
   constexpr int N = Vec<E>::N;
-  __shared__ float lds[2][3][kNormMaxThreads / 64];
+  __shared__ __attribute__((aligned(16))) SumRoom lds[2];
   int turn = 0;
+  clear_sums(lds);
   float wpost[NV][N], wpre[NV][N], gc[NV][N];
-  load_weights<E, NV>(p.w_post, p.d, 1.f, wpost);
-  load_weights<E, NV>(p.w_pre, p.d, 0.f, wpre);
-  load_weights<E, NV>(p.gate_kind == LC_MOE_GATE_CHANNEL ? p.gate : nullptr, p.d, 1.f, gc);
+  auto weights = [&]() {
+    load_weights<E, NV>(p.w_post, p.d, 1.f, wpost);
+    load_weights<E, NV>(p.w_pre, p.d, 0.f, wpre);
+    load_weights<E, NV>(p.gate_kind == LC_MOE_GATE_CHANNEL ? p.gate : nullptr, p.d, 1.f, gc);
+  };
+  if (KEEP) weights();
   float s_pre[NV][N], s_post[NV][N], s_gate[NV][N];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int i = 0; i < N; ++i) s_pre[j][i] = s_post[j][i] = s_gate[j][i] = 0.f;
+  uint4 nh[NV], nd[NV], nz[NV], ny[NV];
+  auto load = [&](int t) {
+    load_rows<E, NV>(p.h, t, p.d, nh);
+    load_rows<E, NV>(p.dz, t, p.d, nz);
+    load_rows<E, NV>(p.y, t, p.d, ny);
+    load_rows<E, NV>(p.dh, t, p.d, nd);
+  };
+  if (NEXT && blockIdx.x < p.T) load(blockIdx.x);
   for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+    if (!NEXT) load(t);
+    if (!KEEP) weights();
     uint4 qh[NV], qd[NV], qz[NV], qy[NV];
-    load_rows<E, NV>(p.h, t, p.d, qh);
-    load_rows<E, NV>(p.dz, t, p.d, qz);
-    load_rows<E, NV>(p.y, t, p.d, qy);
-    load_rows<E, NV>(p.dh, t, p.d, qd);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) qh[j] = nh[j], qd[j] = nd[j], qz[j] = nz[j], qy[j] = ny[j];
+    if (NEXT && p.T - t > int(gridDim.x)) load(t + gridDim.x);
     float g = p.b;
     if (p.gate_kind == LC_MOE_GATE_TOKEN) g *= p.gate[t];
     float s[3] = {0.f, 0.f, 0.f};  // h^2, w_pre dz h, y^2
@@ -238,7 +264,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void block_norm_backward_kernel(No
     const float q = p.w_post ? 1.f / sqrtf(fmaf(s[2], p.rd, p.eps)) : 1.f;
     const float back = s[1] * p.rd * r * r;
     float dH[NV][N];
-    s[0] = s[1] = s[2] = 0.f;  // w_post gate y dH (without the token's gate), w_post y dH
+    float u[1] = {0.f};  // w_post y q gate dH, the token's gate left out
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float h[N], z[N], y[N], d[N];
@@ -253,12 +279,12 @@ __global__ __launch_bounds__(kNormMaxThreads) void block_norm_backward_kernel(No
         const float yq = y[i] * q, wy = wpost[j][i] * yq;
         s_post[j][i] = fmaf(g * gc[j][i] * dH[j][i], yq, s_post[j][i]);
         s_gate[j][i] = fmaf(p.b * wy, dH[j][i], s_gate[j][i]);
-        s[0] = fmaf(wy * gc[j][i], dH[j][i], s[0]);
+        u[0] = fmaf(wy * gc[j][i], dH[j][i], u[0]);
       }
     }
-    if (p.w_post || p.dgate_token) block_sums<3>(s, lds, turn);
-    if (p.dgate_token && threadIdx.x == 0) p.dgate_token[t] = p.b * s[0];
-    const float mean = g * s[0] * p.rd;  // of w_post du times y q
+    if (p.w_post || p.dgate_token) block_sums<1>(u, lds, turn);
+    if (p.dgate_token && threadIdx.x == 0) p.dgate_token[t] = p.b * u[0];
+    const float mean = g * u[0] * p.rd;  // of w_post du times y q
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (int(threadIdx.x) + j * int(blockDim.x)) * N;
@@ -320,11 +346,26 @@ __global__ __launch_bounds__(1024) void norm_sums_kernel(const float* __restrict
   }
 }
 
+// One workgroup a CU takes rows in turn: at T = 16384, d = 6144 237 us with the next row on its way
+// (5.1 TB/s), 270 without, 276 with two workgroups for each CU, which do not fit it at once.
+// 8 elements a thread (4 of fp32) in up to 12 waves leave 168 registers, 16 in up to 8 waves 256, 16
+// in 16 waves 128: no room for the next row and the weights.
+struct NormBwShape {
+  int threads, nv, per_cu;
+};
+static NormBwShape norm_backward_shape(int d, int vec) {
+  const int n = (d + vec - 1) / vec, most = 16 / vec;  // vectors of a row, of a thread
+  NormBwShape s{};
+  s.nv = n <= 768 ? 1 : 2;
+  while (s.nv < most && (n + s.nv - 1) / s.nv > 512) s.nv *= 2;
+  s.threads = ((n + s.nv - 1) / s.nv + 63) / 64 * 64;
+  s.per_cu = s.threads > 256 ? 1 : s.threads > 128 ? 2 : 4;
+  return s;
+}
+
 NormBwPlan plan_norm_backward(int T, int d, int dtype) {
   NormBwPlan p{};
-  int threads, nv;
-  norm_shape(d, dtype == LC_MOE_BF16 ? 8 : 4, threads, nv);
-  const int most = 256 * (threads > 512 ? 1 : 1024 / threads < 4 ? 1024 / threads : 4);
+  const int most = 256 * norm_backward_shape(d, dtype == LC_MOE_BF16 ? 8 : 4).per_cu;
   p.wgs = T < most ? T : most;
   p.part = 0;
   p.total = align256(size_t(p.wgs > 0 ? p.wgs : 1) * 3 * d * 4);
@@ -333,15 +374,13 @@ NormBwPlan plan_norm_backward(int T, int d, int dtype) {
 
 template <typename E>
 static void norm_backward(const NormBwArgs& p, int wgs, hipStream_t st) {
-  int threads, nv;
-  norm_shape(p.d, Vec<E>::N, threads, nv);
-  const dim3 grid(wgs), block(threads);
-  switch (nv) {
-    case 1: block_norm_backward_kernel<E, 1><<<grid, block, 0, st>>>(p); break;
-    case 2: block_norm_backward_kernel<E, 2><<<grid, block, 0, st>>>(p); break;
-    case 3: block_norm_backward_kernel<E, 3><<<grid, block, 0, st>>>(p); break;
-    default: block_norm_backward_kernel<E, 4><<<grid, block, 0, st>>>(p); break;
-  }
+  const NormBwShape s = norm_backward_shape(p.d, Vec<E>::N);
+  const dim3 grid(wgs), block(s.threads);
+  constexpr int MOST = 16 / Vec<E>::N;
+  if (s.nv == 1) block_norm_backward_kernel<E, 1, 768, true, true><<<grid, block, 0, st>>>(p);
+  else if (s.threads > 512) block_norm_backward_kernel<E, MOST, 1024, false, false><<<grid, block, 0, st>>>(p);
+  else if (s.nv == MOST) block_norm_backward_kernel<E, MOST, 512, true, MOST == 2><<<grid, block, 0, st>>>(p);
+  else if constexpr (MOST > 2) block_norm_backward_kernel<E, 2, 512, true, true><<<grid, block, 0, st>>>(p);
 }
 
 hipError_t launch_block_norm_backward(int T, int d, int dtype, const lc_moe_norm& n, const NormBwPlan& plan, void* ws,
