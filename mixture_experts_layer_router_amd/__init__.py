@@ -304,16 +304,28 @@ def permute(x, topk_idx, N, E, with_x_perm=True, workspace=None):
 
 
 def forward(x, w_router, bias, w_gate, w_up, w_down, K, workspace=None, stage_events=None, fp8=None,
-            packed=None, fp8_act=False):
+            packed=None, fp8_act=False, gating=None, token_mask=None):
     """dict(y, topk_idx, topk_gate, load); x [T,d]; w_gate/w_up [N,I,d]; w_down [N,d,I];
     fp8: optional block-FP8 weights from quantize_weights (then used instead);
     packed: optional packed bf16 weights from pack_weights (then read instead);
-    fp8_act: with fp8, quantize x and H to block FP8 too (FP8 matrix cores)."""
+    fp8_act: with fp8, quantize x and H to block FP8 too (FP8 matrix cores);
+    gating: optional Gating: the experts are chosen by lc_moe_select's rule (sigmoid scores,
+    groups, renormalised gates; bias may be None) instead of lc_moe_route's;
+    token_mask: with gating, uint8 [T]: tokens left out (padding) have index -1, gate 0 and y 0."""
     import torch
     N, I, _ = w_gate.shape
     E = w_router.shape[0]
     shape = _shape_of(x, N, E - N, K, I)
     ws = workspace if workspace is not None else workspace_for(shape, x.device)
+    if gating is not None:
+        if stage_events is not None:
+            raise ValueError("stage_events: the stages of a layer with gating are two calls")
+        idx, gate = route_select(x, w_router, bias, K, N, gating, token_mask=token_mask, workspace=ws)
+        out = forward_picks(x, idx, gate, w_gate, w_up, w_down, E - N, workspace=ws, fp8=fp8, packed=packed,
+                            fp8_act=fp8_act)
+        return dict(y=out["y"], topk_idx=idx, topk_gate=gate, load=out["load"])
+    if token_mask is not None:
+        raise ValueError("token_mask needs gating")
     T, dev = x.shape[0], x.device
     y = torch.empty_like(x)
     idx = torch.empty((T, K), dtype=torch.int32, device=dev)

@@ -383,6 +383,27 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a, int room) {
   put_picks(a, t, lane, valid ? ve : -1, g);
 }
 
+// go(EPL, V) for a pool of E experts: how many of them a lane holds, and how many next to each other.
+#define LCM_BY_POOL(E, go)        \
+  do {                            \
+    if ((E) % 4 == 0) {           \
+      if ((E) <= 256) go(4, 4);   \
+      else if ((E) <= 512) go(8, 4);   \
+      else if ((E) <= 768) go(12, 4);  \
+      else if ((E) <= 1024) go(16, 4); \
+      else if ((E) <= 2048) go(32, 4); \
+      else go(64, 4);             \
+    } else {                      \
+      if ((E) <= 64) go(1, 1);    \
+      else if ((E) <= 128) go(2, 1);   \
+      else if ((E) <= 256) go(4, 1);   \
+      else if ((E) <= 512) go(8, 1);   \
+      else if ((E) <= 1024) go(16, 1); \
+      else if ((E) <= 2048) go(32, 1); \
+      else go(64, 1);             \
+    }                             \
+  } while (0)
+
 template <int EPL, int V>
 static void select_launch(const SelectArgs& a, hipStream_t st) {
   // a wave's room: E fp64 scores (a token that is taken in fp64), or 64 candidates
@@ -397,87 +418,130 @@ hipError_t launch_select(const lc_moe_shape& s, const lc_moe_gating& g, const fl
   const int E = s.N + s.Z;
   const SelectArgs a{logits, bias, mask, idx, gate, s.T, E, s.K, g.score, g.groups, E / g.groups, g.top_groups,
                      g.group_rank, g.renorm != 0, g.scale};
-  if (E % 4 == 0) {
-    if (E <= 256) select_launch<4, 4>(a, st);
-    else if (E <= 512) select_launch<8, 4>(a, st);
-    else if (E <= 768) select_launch<12, 4>(a, st);
-    else if (E <= 1024) select_launch<16, 4>(a, st);
-    else if (E <= 2048) select_launch<32, 4>(a, st);
-    else select_launch<64, 4>(a, st);
-  } else {
-    if (E <= 64) select_launch<1, 1>(a, st);
-    else if (E <= 128) select_launch<2, 1>(a, st);
-    else if (E <= 256) select_launch<4, 1>(a, st);
-    else if (E <= 512) select_launch<8, 1>(a, st);
-    else if (E <= 1024) select_launch<16, 1>(a, st);
-    else if (E <= 2048) select_launch<32, 1>(a, st);
-    else select_launch<64, 1>(a, st);
-  }
+#define LCM_GO(EPL, V) select_launch<EPL, V>(a, st)
+  LCM_BY_POOL(E, LCM_GO);
+#undef LCM_GO
   return hipGetLastError();
 }
 
 // ---- gradient ----------------------------------------------------------------------------
 
-// One token by one wavefront; pick k in lane k.
-__global__ __launch_bounds__(64) void select_backward_kernel(const float* __restrict__ logits,
-                                                             const int32_t* __restrict__ idx,
-                                                             const float* __restrict__ dgate, const float* aux,
-                                                             float* dlogits, int T, int E, int K, int score,
-                                                             int renorm, float scale) {
-  extern __shared__ float dp[];
-  const int t = blockIdx.x, lane = threadIdx.x;
-  const float* row = logits + size_t(t) * E;
-  const int e = lane < K ? idx[size_t(t) * K + lane] : -1;
-  const bool ok = static_cast<unsigned>(e) < static_cast<unsigned>(E);
-  const float dg = ok ? dgate[size_t(t) * K + lane] : 0.f;
+struct SelectBwArgs {
+  const float* logits;
+  const int32_t* idx;
+  const float* dgate;
+  const float* aux;
+  float* dlogits;
+  int T, E, K, score, renorm;
+  float scale;
+};
+
+// One token by one wavefront, pick k in lane k, the row of logits or of dlogits_aux in registers
+// (logit_row.h).  The picks' terms are put into a row of zeros in LDS.  Only the softmax without
+// renorm needs every logit; the other forms read those of the picks, and what they take is the
+// writing of dlogits and the reading of dlogits_aux.
+template <int EPL, int V>
+__global__ __launch_bounds__(256) void select_backward_kernel(SelectBwArgs a) {
+  extern __shared__ __attribute__((aligned(16))) float rows[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = blockIdx.x * (blockDim.x >> 6) + wave;
+  if (t >= a.T) return;
+  float* dp = rows + size_t(wave) * ((a.E + 3) & ~3);
+  const float* row = a.logits + size_t(t) * a.E;
+  const int e = lane < a.K ? a.idx[size_t(t) * a.K + lane] : -1;
+  float d[EPL];
+  if (a.aux) {
+    load_row<EPL, V>(a.aux + size_t(t) * a.E, a.E, lane, 0.f, d);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) d[i] = 0.f;
+  }
+  const bool ok = static_cast<unsigned>(e) < static_cast<unsigned>(a.E);
+  const float dg = ok ? a.dgate[size_t(t) * a.K + lane] : 0.f;
   const float x = ok ? row[e] : 0.f;
-  const bool whole = score == LC_MOE_SOFTMAX && !renorm;
-  float v;  // pick's own term
-  if (renorm) {
-    const float ls = score == LC_MOE_SOFTMAX ? x : fminf(x, 0.f) - log1pf(expf(-fabsf(x)));
-    const bool on = ok && ls > -INFINITY;
-    const float top = __ockl_wfred_max_f32(on ? ls : -INFINITY);
-    const float u = on ? expf(ls - top) : 0.f;
+  if (!__ballot(ok)) {  // no pick, no gradient: the row is not read
+    store_row<EPL, V>(a.dlogits + size_t(t) * a.E, a.E, lane, d);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < EPL / V; ++j) {
+    const int at = (j * 64 + lane) * V;
+    if (at >= a.E) continue;
+    if constexpr (V == 4) *reinterpret_cast<float4*>(dp + at) = make_float4(0.f, 0.f, 0.f, 0.f);
+    else dp[at] = 0.f;
+  }
+  const bool whole = a.score == LC_MOE_SOFTMAX && !a.renorm;
+  float v;  // the pick's own term
+  if (a.renorm) {
+    // the picks' shares, as in the forward
+    const bool soft = a.score == LC_MOE_SOFTMAX, on = ok && x > -INFINITY;
+    const float l = soft ? x : fminf(x, 0.f);
+    const float top = __ockl_wfred_max_f32(on ? l : -INFINITY);
+    float u = on ? exp_neg(l - top) : 0.f;
+    const float s = 1.f / (1.f + exp_neg(-fabsf(x)));  // of the larger of s and 1 - s
+    if (!soft) u *= s;
     const float sum = __ockl_wfred_add_f32(u);
     const float w = sum > 0.f ? u / sum : 0.f;
-    const float mean = __ockl_wfred_add_f32(w * dg);
-    v = scale * (w * (dg - mean));
-    if (score == LC_MOE_SIGMOID) v *= 1.f / (1.f + expf(x));
-  } else if (score == LC_MOE_SIGMOID) {
-    const float s = 1.f / (1.f + expf(-x)), r = 1.f / (1.f + expf(x));
-    v = scale * dg * (s * r);
+    v = a.scale * (w * (dg - __ockl_wfred_add_f32(w * dg)));
+    if (!soft) v *= x > 0.f ? exp_neg(-x) * s : s;  // 1 - s
+  } else if (a.score == LC_MOE_SIGMOID) {
+    const float q = exp_neg(-fabsf(x)), s = 1.f / (1.f + q);
+    v = a.scale * dg * (s * (q * s));
   } else {
-    v = scale * dg;
+    v = a.scale * dg;
   }
-  for (int i = lane; i < E; i += 64) dp[i] = 0.f;
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  for (int k = 0; k < K; ++k)  // in pick order: an index may repeat
-    if (lane == k && ok) dp[e] += v;
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  float m = -INFINITY, sum = 0.f, mean = 0.f;
+  // an index that repeats: its terms are added, in the order of the picks, and put once
+  float sum_v = 0.f;
+  bool again = false;
+  for (int k = 0; k < a.K; ++k) {
+    const int ek = __builtin_amdgcn_readlane(e, k);
+    const float vk = lane_value(v, k);
+    sum_v += ek == e ? vk : 0.f;
+    again |= k < lane && ek == e;
+  }
+  wave_fence();
+  if (ok && !again) dp[e] = sum_v;
+  wave_fence();
+  float m = 0.f, rs = 0.f, mean = 0.f;
+  float p[EPL];
   if (whole) {
-    for (int i = lane; i < E; i += 64) m = fmaxf(m, row[i]);
-    m = __ockl_wfred_max_f32(m);
-    m = m > -INFINITY ? m : 0.f;
-    for (int i = lane; i < E; i += 64) sum += expf(row[i] - m);
-    sum = __ockl_wfred_add_f32(sum);
-    const float p = sum > 0.f ? expf(x - m) / sum : 0.f;
-    mean = __ockl_wfred_add_f32(ok ? p * v : 0.f);
+    load_row<EPL, V>(row, a.E, lane, -INFINITY, p);
+    const RowSum r = softmax_row(p);
+    m = r.m > -INFINITY ? r.m : 0.f;
+    rs = r.sum > 0.f ? 1.f / r.sum : 0.f;
+    mean = __ockl_wfred_add_f32(ok ? exp_neg(x - m) * rs * v : 0.f);
   }
-  for (int i = lane; i < E; i += 64) {
-    float d = dp[i];
-    if (whole) d = sum > 0.f ? expf(row[i] - m) / sum * (d - mean) : 0.f;
-    if (aux) d += aux[size_t(t) * E + i];
-    dlogits[size_t(t) * E + i] = d;
+#pragma unroll
+  for (int j = 0; j < EPL / V; ++j) {
+    const int at = (j * 64 + lane) * V;
+    if (at >= a.E) continue;
+    float q[V];
+    if constexpr (V == 4) {
+      const float4 f = *reinterpret_cast<const float4*>(dp + at);
+      q[0] = f.x, q[1] = f.y, q[2] = f.z, q[3] = f.w;
+    } else {
+      q[0] = dp[at];
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) d[j * V + i] += whole ? p[j * V + i] * rs * (q[i] - mean) : q[i];
   }
+  store_row<EPL, V>(a.dlogits + size_t(t) * a.E, a.E, lane, d);
+}
+
+template <int EPL, int V>
+static void select_backward_launch(const SelectBwArgs& a, hipStream_t st) {
+  const int room = ((a.E + 3) & ~3) * 4, waves = a.E <= 1024 ? 4 : 1;
+  select_backward_kernel<EPL, V><<<dim3((a.T + waves - 1) / waves), dim3(waves * 64), waves * room, st>>>(a);
 }
 
 hipError_t launch_select_backward(const lc_moe_shape& s, const lc_moe_gating& g, const float* logits,
                                   const int32_t* idx, const float* dgate, const float* aux, float* dlogits,
                                   hipStream_t st) {
   const int E = s.N + s.Z;
-  select_backward_kernel<<<dim3(s.T), dim3(64), size_t(E) * 4, st>>>(logits, idx, dgate, aux, dlogits, s.T, E, s.K,
-                                                                     g.score, g.renorm != 0, g.scale);
+  const SelectBwArgs a{logits, idx, dgate, aux, dlogits, s.T, E, s.K, g.score, g.renorm != 0, g.scale};
+#define LCM_GO(EPL, V) select_backward_launch<EPL, V>(a, st)
+  LCM_BY_POOL(E, LCM_GO);
+#undef LCM_GO
   return hipGetLastError();
 }
 

@@ -284,11 +284,12 @@ def router_backward(x, w_router, logits, topk_idx, dgate, N, dlogits_aux=None, d
 
 
 def layer_backward(x, w_router, w_gate, w_up, w_down, out, dy, workspace, balance_coef=0.0, z_coef=0.0,
-                   seq_offsets=None, token_mask=None):
+                   seq_offsets=None, token_mask=None, gating=None):
     """The gradient of a whole layer, sum <dy, y> + balance loss + z loss: dict(dx, dw_router,
     dw_gate, dw_up, dw_down, dgate, loss, load, prob).  ``out`` and ``workspace`` are those of
     ``forward(x, ..., workspace=workspace)`` on bf16 tensors; the workspace is read and not
-    written.  The losses are left out (loss None) if both coefficients are 0."""
+    written.  The losses are left out (loss None) if both coefficients are 0.  gating: that of the
+    forward, if it had one (the losses stay those of the softmax of the logits)."""
     T, _ = x.shape
     N, I, _ = w_gate.shape
     E, K = w_router.shape[0], out["topk_idx"].shape[1]
@@ -298,8 +299,13 @@ def layer_backward(x, w_router, w_gate, w_up, w_down, out, dy, workspace, balanc
         bal = balance_loss(saved["logits"], out["topk_idx"], N, balance_coef, z_coef, seq_offsets, token_mask)
     dgate = gate_backward(x, saved["ffn_rows"], saved["slot_row"], dy)
     grads = _on(x.device, ffn_backward, x, w_gate, w_up, w_down, out["topk_idx"], out["topk_gate"], dy, E - N)
-    r = router_backward(x, w_router, saved["logits"], out["topk_idx"], dgate, N, dlogits_aux=bal["dlogits"],
-                        dx_add=grads["dx"], dx=grads["dx"])
+    if gating is None:
+        r = router_backward(x, w_router, saved["logits"], out["topk_idx"], dgate, N, dlogits_aux=bal["dlogits"],
+                            dx_add=grads["dx"], dx=grads["dx"])
+    else:
+        from .block import select_backward
+        dlogits = select_backward(saved["logits"], out["topk_idx"], dgate, gating, dlogits_aux=bal["dlogits"])
+        r = router_backward(x, w_router, None, None, None, N, dlogits_aux=dlogits, dx_add=grads["dx"], dx=grads["dx"])
     return dict(grads, dw_router=r["dw_router"], dgate=dgate, loss=bal["loss"], load=bal["load"], prob=bal["prob"])
 
 
