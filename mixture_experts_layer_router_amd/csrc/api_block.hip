@@ -59,6 +59,10 @@ struct LinearPlan {
 LinearPlan plan_linear(int T, int k, int n) {
   LinearPlan p{};
   p.x = 0;
+  if (linear_few(T, k, n)) {
+    p.total = plan_linear_few(T, k, n).total;
+    return p;
+  }
   p.mm = align256(plan_fp8_mat(T, k).total);
   p.total = p.mm + plan_matmul_fp8(T, n, k).total;
   return p;
@@ -252,6 +256,11 @@ lc_moe_status lc_moe_linear_fp8(int32_t T, int32_t k, int32_t n, const void* x, 
   LCM_CHECK(check_ptr(y));
   const LinearPlan p = plan_linear(T, k, n);
   LCM_CHECK(check_space(workspace, workspace_bytes, p.total));
+  LCM_CHECK(check_overlap(x, y));
+  if (linear_few(T, k, n)) {
+    LCM_LAUNCH(launch_linear_few(T, k, n, plan_linear_few(T, k, n), workspace, x, w, add, y, stream));
+    return LC_MOE_OK;
+  }
   void* xq = at<void>(workspace, p.x);
   LCM_LAUNCH(launch_quantize_matrix(x, T, k, 1, xq, nullptr, stream));
   LCM_LAUNCH(launch_matmul_fp8(T, n, k, plan_matmul_fp8(T, n, k), at<char>(workspace, p.mm), xq, w, add, y, stream));

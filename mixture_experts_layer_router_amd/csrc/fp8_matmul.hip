@@ -464,6 +464,11 @@ static void launch_form(int form, const MatmulArgs& g, hipStream_t st) {
   }
 }
 
+hipError_t launch_matmul_join(const float* part, int splits, size_t n, const bf16_t* add, bf16_t* out, hipStream_t st) {
+  matmul_join_kernel<<<dim3(unsigned((n / 8 + 255) / 256)), dim3(256), 0, st>>>(part, splits, n, add, out);
+  return hipGetLastError();
+}
+
 hipError_t launch_matmul_fp8(int M, int N, int K, const MatmulPlan& p, void* ws, const void* a, const void* b,
                              const void* add, void* out, hipStream_t st) {
   MatmulArgs g{};
@@ -475,9 +480,7 @@ hipError_t launch_matmul_fp8(int M, int N, int K, const MatmulPlan& p, void* ws,
   else launch_form<kOut, false>(p.form, g, st);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  const size_t n = size_t(M) * N;
-  matmul_join_kernel<<<dim3(unsigned((n / 8 + 255) / 256)), dim3(256), 0, st>>>(g.part, p.splits, n, g.p.add, g.p.out);
-  return hipGetLastError();
+  return launch_matmul_join(g.part, p.splits, size_t(M) * N, g.p.add, g.p.out, st);
 }
 
 hipError_t launch_matmul_gradients(int T, int k, int n, void* ws, const void* dyq, const void* w_t, const void* add,

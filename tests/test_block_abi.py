@@ -218,6 +218,7 @@ def test_linear_refusals():
     for k in ("x", "w", "add", "y", "ws"):
         assert fw(**{k: MIS}) == ALIGN, k
     assert fw(nb=n - 1) == WORKSPACE and fw(T=0, x=None, w=None, y=None, ws=None, nb=0) == OK
+    assert fw() == SHAPE and fw(add=None) == SHAPE  # y is x
 
     def bw(T=64, dy=P, x=P, w=P, add=P, dx=P, dw=P, ws=P, nb=nb_):
         return lib.lc_moe_linear_fp8_backward(T, 256, 128, dy, x, w, add, dx, dw, ws, nb, None)

@@ -510,7 +510,8 @@ def test_linear(T, k, n):
     q = ob.quantized(wv, 128, 128)
     y = lm().linear_fp8(x, wq)
     check_product(y, *product(ob.quantized(xv, 1, 128), q))
-    assert torch.equal(y, lm().matmul_fp8(lm().quantize_matrix(x, block_rows=1), wq))
+    if T > 64:  # fewer tokens may be summed up in another order
+        assert torch.equal(y, lm().matmul_fp8(lm().quantize_matrix(x, block_rows=1), wq))
     out = lm().linear_fp8_backward(dy, x, wq)
     check_product(out["dx"], *product(ob.quantized(dv, 1, 128), q.T))
     check_product(out["dw"], *product(ob.quantized(dv.T, 1, 128), ob.quantized(xv.T, 1, 128)))
@@ -520,6 +521,63 @@ def test_linear(T, k, n):
     check_product(over, *product(ob.quantized(dv, 1, 128), q.T, dav))
     r = lm().linear_fp8_backward(dy, x, wq, need_dx=False)
     assert "dx" not in r and torch.equal(r["dw"], out["dw"])
+
+
+FEW = [(1, 8, 8), (1, 128, 40), (3, 1032, 72), (15, 2048, 264), (16, 6144, 136), (17, 264, 1032), (32, 4104, 24),
+       (33, 136, 520), (63, 2056, 40), (64, 16384, 8), (65, 1032, 72), (64, 2048, 6144), (64, 2048, 5344)]
+
+
+@pytest.mark.parametrize("T,k,n", FEW)
+def test_linear_few_tokens(T, k, n):
+    """Few tokens: around the blocks of 16 of them, odd runs, reductions split and not; the addend, and the
+    same workspace for both."""
+    import torch
+    say(f"linear of few tokens {T} {k} {n}")
+    rng = np.random.default_rng(T + k + n)
+    x, xv = stored(rng.standard_normal((T, k)) * np.exp2(rng.integers(-8, 9, (T, 1))), "bf16")
+    w, wv = stored(rng.standard_normal((n, k)) / np.sqrt(k) * np.exp2(rng.integers(-3, 4, (n, 1))), "bf16")
+    e, ev = stored(rng.standard_normal((T, n)), "bf16")
+    wq, qx, qw = lm().quantize_matrix(w), ob.quantized(xv, 1, 128), ob.quantized(wv, 128, 128)
+    y = lm().linear_fp8(x, wq)
+    check_product(y, *product(qx, qw))
+    assert torch.equal(y, lm().linear_fp8(x, wq))
+    over = e.clone()
+    assert lm().linear_fp8(x, wq, add=over, out=over) is over
+    check_product(over, *product(qx, qw, ev))
+    assert torch.equal(over, lm().linear_fp8(x, wq, add=e))
+    # a token's result does not depend on the others
+    if T > 1:
+        assert torch.equal(lm().linear_fp8(torch.cat((x[1:], x[:1])), wq), torch.cat((y[1:], y[:1])))
+
+
+def test_linear_few_tokens_every_bf16_value():
+    """One-hot weights give the tokens' codes themselves: every finite bf16 value up to its run's 448, and the
+    values of the smallest scale."""
+    import torch
+    say("linear of every value")
+    vals = (torch.arange(65536, dtype=torch.int32) << 16).view(torch.float32)
+    vals = vals[torch.isfinite(vals) & (vals.abs() <= 448)]
+    n = -(-len(vals) // 64) * 64
+    v = torch.zeros(n)
+    v[:len(vals)] = vals
+    x = torch.cat((torch.full((n // 64, 64), 448.0), v.view(-1, 64)), 1).to(torch.bfloat16)
+    tiny = (torch.arange(256, dtype=torch.int32) << 16).view(torch.float32).view(2, 128).to(torch.bfloat16)
+    big = (torch.arange(0x7F00, 0x7F80, dtype=torch.int32) << 16).view(torch.float32).view(1, 128).to(torch.bfloat16)
+    for rows, unit in ((x, 1.0), (tiny, 2.0 ** 120), (big, 2.0 ** -20), (-big, 2.0 ** -20)):
+        wq = lm().quantize_matrix((unit * torch.eye(128)).to(torch.bfloat16).to(device()))
+        want = torch.from_numpy(ob.quantized(rows.double().numpy(), 1, 128) * unit)
+        for i in range(0, len(rows), 64):
+            got = lm().linear_fp8(rows[i:i + 64].to(device()), wq).double().cpu()
+            assert torch.equal(got, want[i:i + 64]), (i, unit)
+
+
+def test_linear_few_tokens_refuses_its_input_as_output():
+    import torch
+    say("linear over its input")
+    x = put(np.ones((4, 16), np.float32), torch.bfloat16)
+    wq = lm().quantize_matrix(put(np.ones((16, 16), np.float32), torch.bfloat16))
+    with pytest.raises(Exception):
+        lm().linear_fp8(x, wq, out=x)
 
 
 def test_no_rows():
