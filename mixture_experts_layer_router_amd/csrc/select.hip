@@ -182,7 +182,8 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a, int room) {
   }
   // serr: bound of the error of a score.  Softmax: a score is off by its share of (|x - m| + 6 of
   // exp and products, EPL + 10 of the sum) 2^-24, s |x - m| at most 0.37 of the largest; sigmoid: by
-  // (1 - s) (1.5 |x| + 2) + 3 of it, s (1 - s) |x| at most that of the largest logit if it is below -1.
+  // (1 - s) (1.5 |x| + 2) + 3 of it, s (1 - s) |x| at most that of the largest logit if it is below -1, and
+  // by all of it below 2^-126 (from |x| = 89 on: |x| of -128 and less does not matter, and may overflow).
   // What is off becomes -infinity: x 0 is NaN for it, and so is a NaN bias, and the larger of NaN and
   // -infinity is that.
   float sum = 1.f, serr;
@@ -201,7 +202,7 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a, int room) {
     for (int i = 0; i < EPL; ++i) c[i] = fmaxf(fmaf(x[i], 0.f, fmaf(e[i], rs, c[i])), -INFINITY);
   } else {
     const float top = 1.f / (1.f + __builtin_amdgcn_exp2f(m * -1.44269504f));
-    serr = top * (8.f + 2.f * fmaxf(-m, 0.f)) * 0x1p-24f;
+    serr = top * (8.f + 2.f * fminf(fmaxf(-m, 0.f), 128.f)) * 0x1p-24f + 0x1p-125f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x[i] * -1.44269504f));
@@ -261,7 +262,8 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a, int room) {
     const float least = -__ockl_wfred_max_f32(kept || g >= a.groups ? -(kept ? best - err : INFINITY) : -INFINITY);
     const float most = __ockl_wfred_max_f32(kept || g >= a.groups ? -INFINITY : best + err);
     wave_fence();
-    whole = most > -INFINITY && !(least > most);
+    // (two biases near the largest float may overflow: fp64 then tells the groups apart)
+    whole = (most > -INFINITY && !(least > most)) || __ballot(m1 > -INFINITY && !(fabsf(best) < INFINITY));
     const unsigned long long live = __ballot(kept);
     const uint32_t magic = uint32_t((0x100000000ull + a.size - 1) / a.size);  // e / size, exact for e, size < 2^16
     auto keep = [&](int e) {
@@ -307,7 +309,8 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a, int room) {
       }
       kth = -__ockl_wfred_max_f32(before < a.K ? -pm : -INFINITY);
     }
-    // (what is off is below every bound)
+    // (what is off is below every bound but one that overflows, of a bias near the lowest float: then all
+    // 64 EPL places count, and the token is taken in fp64)
     const float bound = kth > -INFINITY ? kth - 2.f * serr - fabsf(kth) * 0x1p-22f : -__FLT_MAX__;
     n = 0;
 #pragma unroll

@@ -159,6 +159,51 @@ def test_select_next_to_a_border(score, groups):
     check_select(kw, lg, b, None, got)
 
 
+LOWEST = np.finfo(np.float32).min
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,rank", [(1, 1), (4, 1), (4, 2), (8, 2)])
+@pytest.mark.parametrize("E", [64, 96, 768])
+def test_select_lowest_values(score, groups, rank, E):
+    """Masks of fp32's lowest value, in logits and biases, rows of nothing else too: such an expert is on, after
+    all that are larger and ahead of those that are off."""
+    say(f"select lowest values {score} {groups} {rank} {E}")
+    rng = np.random.default_rng(17)
+    T, K, size = 24, 8, E // groups
+    lg = rng.standard_normal((T, E)).astype(np.float32)
+    lg[0] = LOWEST
+    lg[1, 3:] = LOWEST
+    lg[2, :E // 2] = LOWEST
+    lg[3, rng.random(E) < 0.9] = LOWEST
+    lg[4] = LOWEST
+    lg[4, ::2] = -np.inf
+    lg[5] = LOWEST / 2
+    lg[6] = -1e30
+    lg[7] = np.linspace(-95, -80, E)
+    lg[8, :size] = -np.inf
+    lg[9] = LOWEST
+    lg[9, E - size:] = -np.inf
+    kw = dict(K=K, score=score, groups=groups, top_groups=max(groups // 2, 1), group_rank=rank)
+    plain = (0.05 * rng.uniform(-1, 1, E)).astype(np.float32)
+    low, some, half, high = plain.copy(), plain.copy(), plain.copy(), plain.copy()
+    low[:] = LOWEST
+    some[size // 2:] = LOWEST
+    half[:E // 2], half[E // 2:] = LOWEST / 2, LOWEST
+    high[::3] = -LOWEST
+    off = low.copy()
+    off[:size] = -np.inf
+    for b in (None, plain, low, some, half, high, off):
+        for renorm in (False, True):
+            kw["renorm"] = renorm
+            got = lm().select(put(lg), None if b is None else put(b), K, lm().Gating(**gating_of(kw)))
+            idx, gate = ob.select(lg, b, **kw)
+            np.testing.assert_array_equal(to_np(got[0]), idx)
+            # logits of a token are equal, or within 100 of 0, or so far below its largest that their scores
+            # are less than 2^-126 of it
+            np.testing.assert_allclose(to_np(got[1]), gate, rtol=(8 * 150 + 80) * U, atol=2.0 ** -126)
+
+
 def test_select_far_logits():
     """Scores far below fp32's range still have shares, and large ones saturate without NaN."""
     say("select far logits")
