@@ -74,28 +74,44 @@ __device__ __forceinline__ void block_sums(float (&v)[C], SumRoom (&lds)[2], int
   }
 }
 
+// Keeps a value out of the compiler's sight: what is made of it (addresses, the floats of a row) is made
+// where it is used and not kept from one use for the next, nor ahead of the loop over rows.
+__device__ __forceinline__ int here(int v) {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("" : "+v"(v));
+#endif
+  return v;
+}
+__device__ __forceinline__ uint4 here(uint4 v) {
+  return make_uint4(here(int(v.x)), here(int(v.y)), here(int(v.z)), here(int(v.w)));
+}
+
+// The weights of vector j of thread tid, `other` without w and behind d.
+template <typename E>
+__device__ __forceinline__ void load_weight(const float* w, int tid, int j, int d, float other,
+                                            float (&out)[Vec<E>::N]) {
+  constexpr int N = Vec<E>::N;
+  const int c = (tid + j * int(blockDim.x)) * N;
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    float4 q = make_float4(other, other, other, other);
+    if (w && c < d) q = *reinterpret_cast<const float4*>(w + c + i);
+    out[i] = q.x, out[i + 1] = q.y, out[i + 2] = q.z, out[i + 3] = q.w;
+  }
+}
 template <typename E, int NV>
 __device__ __forceinline__ void load_weights(const float* w, int d, float other, float (&out)[NV][Vec<E>::N]) {
-  constexpr int N = Vec<E>::N;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (int(threadIdx.x) + j * int(blockDim.x)) * N;
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      float4 q = make_float4(other, other, other, other);
-      if (w && c < d) q = *reinterpret_cast<const float4*>(w + c + i);
-      out[j][i] = q.x, out[j][i + 1] = q.y, out[j][i + 2] = q.z, out[j][i + 3] = q.w;
-    }
-  }
+  for (int j = 0; j < NV; ++j) load_weight<E>(w, threadIdx.x, j, d, other, out[j]);
 }
 
 template <typename E, int NV>
-__device__ __forceinline__ void load_rows(const void* p, size_t t, int d, uint4 (&out)[NV]) {
+__device__ __forceinline__ void load_rows(const void* p, size_t t, int d, int tid, uint4 (&out)[NV]) {
   constexpr int N = Vec<E>::N;
   const E* row = static_cast<const E*>(p) + t * d;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = (int(threadIdx.x) + j * int(blockDim.x)) * N;
+    const int c = (tid + j * int(blockDim.x)) * N;
     out[j] = p && c < d ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
   }
 }
@@ -120,8 +136,8 @@ __global__ __launch_bounds__(kNormMaxThreads) void block_norm_kernel(NormArgs p)
   load_weights<E, NV>(p.gate_kind == LC_MOE_GATE_CHANNEL ? p.gate : nullptr, p.d, 1.f, gc);
   for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
     uint4 qx[NV], qy[NV];
-    load_rows<E, NV>(p.x, t, p.d, qx);
-    load_rows<E, NV>(p.y, t, p.d, qy);
+    load_rows<E, NV>(p.x, t, p.d, threadIdx.x, qx);
+    load_rows<E, NV>(p.y, t, p.d, threadIdx.x, qy);
     float g = p.b;
     if (p.gate_kind == LC_MOE_GATE_TOKEN) g *= p.gate[t];
     float h[NV][N], s[1] = {0.f};
@@ -208,37 +224,59 @@ struct NormBwArgs {
   float a, b, eps, rd;
 };
 
-// NEXT: the next row is loaded beside the present one's sums.  KEEP: the weights stay in registers
-// (else they are read again, from the L2, in every row).
+// NEXT: the next row is loaded beside the present one's sums.  KEEP: the weights and all sums over tokens
+// stay in registers; else the weights are read in every row again, from the L2, and two of the sums stay
+// in LDS.  (With everything in registers, and spilled, d = 16384 ran at 1.3 TB/s; with these 3.8, fp32 4.5.)
 template <typename E, int NV, int THREADS, bool NEXT, bool KEEP>
 __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(NormBwArgs p) {
   constexpr int N = Vec<E>::N;
   __shared__ __attribute__((aligned(16))) SumRoom lds[2];
+  __shared__ float4 room[!KEEP ? 2 : 1][!KEEP ? NV * N / 4 : 1][!KEEP ? THREADS : 1];
   int turn = 0;
   clear_sums(lds);
   float wpost[NV][N], wpre[NV][N], gc[NV][N];
-  auto weights = [&]() {
+  const float* wgate = p.gate_kind == LC_MOE_GATE_CHANNEL ? p.gate : nullptr;
+  if (KEEP) {
     load_weights<E, NV>(p.w_post, p.d, 1.f, wpost);
     load_weights<E, NV>(p.w_pre, p.d, 0.f, wpre);
-    load_weights<E, NV>(p.gate_kind == LC_MOE_GATE_CHANNEL ? p.gate : nullptr, p.d, 1.f, gc);
-  };
-  if (KEEP) weights();
+    load_weights<E, NV>(wgate, p.d, 1.f, gc);
+  }
   float s_pre[NV][N], s_post[NV][N], s_gate[NV][N];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int i = 0; i < N; ++i) s_pre[j][i] = s_post[j][i] = s_gate[j][i] = 0.f;
+    for (int i = 0; i < N; ++i) {
+      s_pre[j][i] = s_post[j][i] = s_gate[j][i] = 0.f;
+      if (!KEEP && i % 4 == 0)
+        room[0][(j * N + i) / 4][threadIdx.x] = room[1][(j * N + i) / 4][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  int tid = threadIdx.x;
+  auto from_room = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 f = room[0][(j * N + i) / 4][tid], g = room[1][(j * N + i) / 4][tid];
+      s_post[j][i] = f.x, s_post[j][i + 1] = f.y, s_post[j][i + 2] = f.z, s_post[j][i + 3] = f.w;
+      s_gate[j][i] = g.x, s_gate[j][i + 1] = g.y, s_gate[j][i + 2] = g.z, s_gate[j][i + 3] = g.w;
+    }
+  };
+  auto to_room = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      room[0][(j * N + i) / 4][tid] = make_float4(s_post[j][i], s_post[j][i + 1], s_post[j][i + 2], s_post[j][i + 3]);
+      room[1][(j * N + i) / 4][tid] = make_float4(s_gate[j][i], s_gate[j][i + 1], s_gate[j][i + 2], s_gate[j][i + 3]);
+    }
+  };
   uint4 nh[NV], nd[NV], nz[NV], ny[NV];
   auto load = [&](int t) {
-    load_rows<E, NV>(p.h, t, p.d, nh);
-    load_rows<E, NV>(p.dz, t, p.d, nz);
-    load_rows<E, NV>(p.y, t, p.d, ny);
-    load_rows<E, NV>(p.dh, t, p.d, nd);
+    if (!KEEP) tid = here(tid);
+    load_rows<E, NV>(p.h, t, p.d, tid, nh);
+    load_rows<E, NV>(p.dz, t, p.d, tid, nz);
+    load_rows<E, NV>(p.y, t, p.d, tid, ny);
+    load_rows<E, NV>(p.dh, t, p.d, tid, nd);
   };
   if (NEXT && blockIdx.x < p.T) load(blockIdx.x);
   for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
     if (!NEXT) load(t);
-    if (!KEEP) weights();
     uint4 qh[NV], qd[NV], qz[NV], qy[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) qh[j] = nh[j], qd[j] = nd[j], qz[j] = nz[j], qy[j] = ny[j];
@@ -249,15 +287,18 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(NormBwArgs
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float h[N], z[N], y[N];
+      if (!KEEP) tid = here(tid);
       Vec<E>::open(qh[j], h);
       Vec<E>::open(qz[j], z);
       Vec<E>::open(qy[j], y);
+      if (!KEEP) load_weight<E>(p.w_pre, tid, j, p.d, 0.f, wpre[j]);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         s[0] = fmaf(h[i], h[i], s[0]);
         s[1] = fmaf(wpre[j][i] * z[i], h[i], s[1]);
         s[2] = fmaf(y[i], y[i], s[2]);
       }
+      if (!KEEP) __builtin_amdgcn_sched_barrier(0);
     }
     block_sums<3>(s, lds, turn);
     const float r = 1.f / sqrtf(fmaf(s[0], p.rd, p.eps));
@@ -268,10 +309,17 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(NormBwArgs
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float h[N], z[N], y[N], d[N];
+      if (!KEEP) tid = here(tid), qh[j] = here(qh[j]), qz[j] = here(qz[j]), qy[j] = here(qy[j]);
       Vec<E>::open(qh[j], h);
       Vec<E>::open(qz[j], z);
       Vec<E>::open(qy[j], y);
       Vec<E>::open(qd[j], d);
+      if (!KEEP) {
+        load_weight<E>(p.w_pre, tid, j, p.d, 0.f, wpre[j]);
+        load_weight<E>(p.w_post, tid, j, p.d, 1.f, wpost[j]);
+        load_weight<E>(wgate, tid, j, p.d, 1.f, gc[j]);
+      }
+      if (!KEEP) from_room(j);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         s_pre[j][i] = fmaf(z[i], h[i] * r, s_pre[j][i]);
@@ -281,18 +329,25 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(NormBwArgs
         s_gate[j][i] = fmaf(p.b * wy, dH[j][i], s_gate[j][i]);
         u[0] = fmaf(wy * gc[j][i], dH[j][i], u[0]);
       }
+      if (!KEEP) to_room(j);
+      if (!KEEP) __builtin_amdgcn_sched_barrier(0);
     }
     if (p.w_post || p.dgate_token) block_sums<1>(u, lds, turn);
     if (p.dgate_token && threadIdx.x == 0) p.dgate_token[t] = p.b * u[0];
     const float mean = g * u[0] * p.rd;  // of w_post du times y q
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (int(threadIdx.x) + j * int(blockDim.x)) * N;
+      if (!KEEP) tid = here(tid), qy[j] = here(qy[j]);
+      const int c = (tid + j * int(blockDim.x)) * N;
       if (c >= p.d) continue;
       const size_t at = size_t(t) * p.d + c;
       if (p.dy) {
         float y[N];
         Vec<E>::open(qy[j], y);
+        if (!KEEP) {
+          load_weight<E>(p.w_post, tid, j, p.d, 1.f, wpost[j]);
+          load_weight<E>(wgate, tid, j, p.d, 1.f, gc[j]);
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const float du = g * gc[j][i] * dH[j][i];
@@ -305,6 +360,7 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(NormBwArgs
         for (int i = 0; i < N; ++i) dH[j][i] *= p.a;
         *reinterpret_cast<uint4*>(static_cast<E*>(p.dx) + at) = Vec<E>::close(dH[j]);
       }
+      if (!KEEP) __builtin_amdgcn_sched_barrier(0);
     }
   }
   float* part = p.part + size_t(blockIdx.x) * 3 * p.d;
@@ -312,6 +368,7 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(NormBwArgs
   for (int j = 0; j < NV; ++j) {
     const int c = (int(threadIdx.x) + j * int(blockDim.x)) * N;
     if (c >= p.d) continue;
+    if (!KEEP) from_room(j);
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
       *reinterpret_cast<float4*>(part + c + i) = make_float4(s_pre[j][i], s_pre[j][i + 1], s_pre[j][i + 2], s_pre[j][i + 3]);
@@ -346,10 +403,13 @@ __global__ __launch_bounds__(1024) void norm_sums_kernel(const float* __restrict
   }
 }
 
-// One workgroup a CU takes rows in turn: at T = 16384, d = 6144 237 us with the next row on its way
-// (5.1 TB/s), 270 without, 276 with two workgroups for each CU, which do not fit it at once.
-// 8 elements a thread (4 of fp32) in up to 12 waves leave 168 registers, 16 in up to 8 waves 256, 16
-// in 16 waves 128: no room for the next row and the weights.
+// One workgroup a CU takes rows in turn: at T = 16384, d = 6144 225 us with the next row on its way
+// (5.4 TB/s), 270 without, 276 with two workgroups for each CU, which do not fit it at once; of up to 6
+// waves two fit, of up to 3 four (T = 16384, d = 1032: 63 us with two of 3, 50 with four).  Beyond 256 of
+// them a workgroup has two rows at least, or its sums over them are as many bytes as the rows (T = 600,
+// d = 2048: 15.5 us with a row each, 13.6 with two).
+// 8 elements a thread in up to 12 waves leave 168 registers (fp32, d = 6144: 320 us for 10922 tokens, 361
+// with 16 elements in 6 waves), 16 in up to 8 waves 256, 16 in 16 waves 128: a row, and the sums in LDS.
 struct NormBwShape {
   int threads, nv, per_cu;
 };
@@ -357,15 +417,16 @@ static NormBwShape norm_backward_shape(int d, int vec) {
   const int n = (d + vec - 1) / vec, most = 16 / vec;  // vectors of a row, of a thread
   NormBwShape s{};
   s.nv = n <= 768 ? 1 : 2;
-  while (s.nv < most && (n + s.nv - 1) / s.nv > 512) s.nv *= 2;
+  while (s.nv < most && (n + s.nv - 1) / s.nv > 768) s.nv *= 2;
   s.threads = ((n + s.nv - 1) / s.nv + 63) / 64 * 64;
-  s.per_cu = s.threads > 256 ? 1 : s.threads > 128 ? 2 : 4;
+  s.per_cu = s.threads > 384 ? 1 : s.threads > 192 ? 2 : 4;
   return s;
 }
 
 NormBwPlan plan_norm_backward(int T, int d, int dtype) {
   NormBwPlan p{};
-  const int most = 256 * norm_backward_shape(d, dtype == LC_MOE_BF16 ? 8 : 4).per_cu;
+  int most = 256 * norm_backward_shape(d, dtype == LC_MOE_BF16 ? 8 : 4).per_cu;
+  if (T / 2 < most) most = T / 2 < 256 ? 256 : T / 2;
   p.wgs = T < most ? T : most;
   p.part = 0;
   p.total = align256(size_t(p.wgs > 0 ? p.wgs : 1) * 3 * d * 4);
@@ -378,9 +439,10 @@ static void norm_backward(const NormBwArgs& p, int wgs, hipStream_t st) {
   const dim3 grid(wgs), block(s.threads);
   constexpr int MOST = 16 / Vec<E>::N;
   if (s.nv == 1) block_norm_backward_kernel<E, 1, 768, true, true><<<grid, block, 0, st>>>(p);
-  else if (s.threads > 512) block_norm_backward_kernel<E, MOST, 1024, false, false><<<grid, block, 0, st>>>(p);
+  else if (s.nv == MOST && s.threads > 512)
+    block_norm_backward_kernel<E, MOST, 1024, false, false><<<grid, block, 0, st>>>(p);
   else if (s.nv == MOST) block_norm_backward_kernel<E, MOST, 512, true, MOST == 2><<<grid, block, 0, st>>>(p);
-  else if constexpr (MOST > 2) block_norm_backward_kernel<E, 2, 512, true, true><<<grid, block, 0, st>>>(p);
+  else if constexpr (MOST > 2) block_norm_backward_kernel<E, 2, 768, true, true><<<grid, block, 0, st>>>(p);
 }
 
 hipError_t launch_block_norm_backward(int T, int d, int dtype, const lc_moe_norm& n, const NormBwPlan& plan, void* ws,

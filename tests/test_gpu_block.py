@@ -290,7 +290,9 @@ def test_select_backward_against_differences(score, renorm):
 NORMS = [dict(T=1, d=8), dict(T=3, d=64, gate="channel"), dict(T=130, d=6144, post=True, gate="channel"),
          dict(T=33, d=1032, post=True, gate="token"), dict(T=9, d=16384, post=True, gate="channel"),
          dict(T=5, d=8200, gate="token"), dict(T=700, d=520, post=True), dict(T=1100, d=2048, post=True, gate="channel"),
-         dict(T=3000, d=128, post=True, gate="token"), dict(T=4, d=12296, noy=True), dict(T=66, d=256, noy=True)]
+         dict(T=3000, d=128, post=True, gate="token"), dict(T=4, d=12296, noy=True), dict(T=66, d=256, noy=True),
+         dict(T=600, d=8200, post=True, gate="channel"), dict(T=530, d=6144, post=True, gate="token"),
+         dict(T=515, d=5128, gate="channel"), dict(T=300, d=16384, post=True, gate="token")]
 
 
 def norm_inputs(kw, dt, seed=4):
