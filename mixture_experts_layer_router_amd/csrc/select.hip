@@ -129,6 +129,18 @@ __device__ __forceinline__ double lane_value(double v, int lane) {
 }
 __device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
+// Sums of v over the lanes up to this one: within runs of 16 lanes, then the last lane of a run to the
+// next run, and that of the lower half to the upper one.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // a lane's value to the next lane of its run
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);   // two on
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);   // four
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);   // eight
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // lanes 15 and 47 to the runs behind them
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // lane 31 to the upper half
+  return v;
+}
+
 // Of the n values c of lanes 0 .. n-1 (n <= 64): how many are ahead of the lane's in descending order,
 // equal ones in the order of their experts e.
 __device__ __forceinline__ int place_of(double c, int e, int n) {
@@ -296,7 +308,8 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a, int room) {
 #pragma unroll
   for (int i = 1; i + 1 < EPL; i += 2) lm = fmaxf(lm, fmaxf(c[i], c[i + 1]));
   if constexpr (EPL % 2 == 0) lm = fmaxf(lm, c[EPL - 1]);
-  int n = 65;
+  int n = 65, place = 0;  // how many may be, and the place of the lane's first
+  float bound = 0.f;
   for (int parts = EPL == 1 ? 1 : a.K <= 16 ? 16 : 64; !whole; parts = 64) {
     float kth = -INFINITY;
     if constexpr (EPL > 1) {
@@ -315,28 +328,29 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a, int room) {
     }
     // (what is off is below every bound but one that overflows, of a bias near the lowest float: then all
     // 64 EPL places count, and the token is taken in fp64)
-    const float bound = kth > -INFINITY ? kth - 2.f * serr - fabsf(kth) * 0x1p-22f : -__FLT_MAX__;
-    n = 0;
+    bound = kth > -INFINITY ? kth - 2.f * serr - fabsf(kth) * 0x1p-22f : -__FLT_MAX__;
+    int mine_n = 0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const bool in = c[i] >= bound;
-      const unsigned long long at = __ballot(in);
-      // (places from 64 on come round again: they are then gathered anew)
-      const int place = __builtin_amdgcn_mbcnt_hi(uint32_t(at >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(at), n)) & 63;
-      if (in) {
-        g_c[place] = c[i];
-        g_e[place] = ((i / V) * 64 + lane) * V + i % V;
-        g_x[place] = x[i];
-      }
-      n += __popcll(at);
-    }
-    wave_fence();
+    for (int i = 0; i < EPL; ++i) mine_n += c[i] >= bound ? 1 : 0;
+    place = wave_scan(mine_n);
+    n = __builtin_amdgcn_readlane(place, 63);
+    place -= mine_n;
     if (n <= 64 || parts != 16) break;
   }
   if (n > 64) {
     select_token_f64(a, t, lane, reinterpret_cast<double*>(mine));
     return;
   }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    if (c[i] >= bound) {
+      g_c[place] = c[i];
+      g_e[place] = ((i / V) * 64 + lane) * V + i % V;
+      g_x[place] = x[i];
+      ++place;
+    }
+  }
+  wave_fence();
   float vc = lane < n ? g_c[lane] : -INFINITY, vx = g_x[lane];
   int ve = g_e[lane];
   wave_fence();
@@ -353,7 +367,7 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a, int room) {
     vx = g_x[lane];
     wave_fence();
   };
-  const int place = place_of(vc, n);
+  place = place_of(vc, n);
   const int was = ve;
   put(place);
   if (lane < n) g_c[place] = vc;
