@@ -196,8 +196,9 @@ lc_moe_status lc_moe_matmul_fp8(int32_t M, int32_t N, int32_t K, const void* a, 
 /* y = Q(x) W^T + add: the tokens quantised in blocks of 1 x 128, W a block-FP8 weight [n][k].
  *   x [T][k] bf16, w the `out` of lc_moe_quantize_matrix(W, n, k, 128, ...), add and y [T][n]
  *   bf16 (add may be NULL, or y itself)
- * k and n multiples of 8; y == x: LC_MOE_E_SHAPE.  For few tokens the matrix cores add 128
- * products at a time, so that the last bits need not be those of lc_moe_matmul_fp8. */
+ * k and n multiples of 8; y == x: LC_MOE_E_SHAPE.  Few tokens or a small matrix are quantised and
+ * multiplied in one launch; the matrix cores then add 128 products at a time, so that the last
+ * bits need not be those of lc_moe_matmul_fp8. */
 size_t lc_moe_linear_fp8_workspace_size(int32_t T, int32_t k, int32_t n);
 lc_moe_status lc_moe_linear_fp8(int32_t T, int32_t k, int32_t n, const void* x, const void* w,
                                 const void* add, void* y, void* workspace, size_t workspace_bytes,
@@ -208,8 +209,9 @@ lc_moe_status lc_moe_linear_fp8(int32_t T, int32_t k, int32_t n, const void* x, 
  *                              lc_moe_quantize_matrix(W, n, k, 128, ...): the same values)
  *   dw = Q'(dy)^T Q'(x)        both in blocks of 128 tokens x 1 column
  *   dy [T][n], x [T][k], dx_add and dx [T][k] (dx_add may be NULL, or dx itself), dw [n][k], bf16
- * dx NULL: not computed (w_t is then not read); dw NULL: not computed (x is then not read).  T = 0
- * writes zeros to dw. */
+ * dx NULL: not computed (w_t is then not read); dw NULL: not computed (x is then not read; dx as
+ * lc_moe_linear_fp8 computes it, so that its last bits may differ).  dx == dy: LC_MOE_E_SHAPE.
+ * T = 0 writes zeros to dw. */
 size_t lc_moe_linear_fp8_backward_workspace_size(int32_t T, int32_t k, int32_t n);
 lc_moe_status lc_moe_linear_fp8_backward(int32_t T, int32_t k, int32_t n, const void* dy,
                                          const void* x, const void* w_t, const void* dx_add,

@@ -54,13 +54,15 @@ bool matmul_ok(int M, int N, int K) {
 lc_moe_status check_overlap(const void* a, const void* b) { return a && a == b ? LC_MOE_E_SHAPE : LC_MOE_OK; }
 
 struct LinearPlan {
-  size_t x, mm, total;
+  LinearFewPlan few;
+  size_t x, mm, total;  // mm 0: few
 };
 LinearPlan plan_linear(int T, int k, int n) {
   LinearPlan p{};
   p.x = 0;
-  if (linear_few(T, k, n)) {
-    p.total = plan_linear_few(T, k, n).total;
+  p.few = plan_linear_few(T, k, n);
+  if (linear_few(p.few, T, k, n)) {
+    p.total = p.few.total;
     return p;
   }
   p.mm = align256(plan_fp8_mat(T, k).total);
@@ -71,6 +73,7 @@ bool linear_ok(int T, int k, int n) {
   return T >= 0 && k >= 8 && k % 8 == 0 && matmul_ok(T, n, k);
 }
 struct LinearBwPlan {
+  LinearFewPlan few;  // total 0: not taken
   size_t dy, dyt, xt, mm, total;
 };
 LinearBwPlan plan_linear_backward(int T, int k, int n) {
@@ -82,6 +85,9 @@ LinearBwPlan plan_linear_backward(int T, int k, int n) {
   p.xt = take(plan_fp8_mat(k, T).total);
   const size_t a = plan_matmul_fp8(T, k, n).total, b = plan_matmul_fp8(n, k, T).total;
   p.mm = take(a > b ? a : b);
+  p.few = plan_linear_few(T, n, k);  // dx alone: the linear layer of the transpose
+  if (!linear_few(p.few, T, n, k)) p.few.total = 0;
+  if (p.few.total > o) o = p.few.total;
   p.total = o;
   return p;
 }
@@ -257,8 +263,8 @@ lc_moe_status lc_moe_linear_fp8(int32_t T, int32_t k, int32_t n, const void* x, 
   const LinearPlan p = plan_linear(T, k, n);
   LCM_CHECK(check_space(workspace, workspace_bytes, p.total));
   LCM_CHECK(check_overlap(x, y));
-  if (linear_few(T, k, n)) {
-    LCM_LAUNCH(launch_linear_few(T, k, n, plan_linear_few(T, k, n), workspace, x, w, add, y, stream));
+  if (p.mm == 0) {
+    LCM_LAUNCH(launch_linear_few(T, k, n, p.few, workspace, x, w, add, y, stream));
     return LC_MOE_OK;
   }
   void* xq = at<void>(workspace, p.x);
@@ -290,9 +296,14 @@ lc_moe_status lc_moe_linear_fp8_backward(int32_t T, int32_t k, int32_t n, const 
   LCM_CHECK(check_ptr(dx, true));
   const LinearBwPlan p = plan_linear_backward(T, k, n);
   LCM_CHECK(check_space(workspace, workspace_bytes, p.total));
+  LCM_CHECK(check_overlap(dy, dx));
   if (!dx && !dw) return LC_MOE_OK;
   void *dyq = at<void>(workspace, p.dy), *dyt = at<void>(workspace, p.dyt), *xt = at<void>(workspace, p.xt);
   char* mm = at<char>(workspace, p.mm);
+  if (!dw && p.few.total) {
+    LCM_LAUNCH(launch_linear_few(T, n, k, p.few, workspace, dy, w_t, dx_add, dx, stream));
+    return LC_MOE_OK;
+  }
   if (!dw) {
     LCM_LAUNCH(launch_quantize_matrix(dy, T, n, 1, dyq, nullptr, stream));
     LCM_LAUNCH(launch_matmul_fp8(T, k, n, plan_matmul_fp8(T, k, n), mm, dyq, w_t, dx_add, dx, stream));

@@ -63,19 +63,21 @@ struct MatmulPlan {
   size_t part, total;
   int splits, chunk;  // pieces of the reduction, runs of 128 of each
   int form;           // tile (fp8_matmul.hip)
+  float us;           // what it takes, by the model
 };
 MatmulPlan plan_matmul_fp8(int M, int N, int K);
 hipError_t launch_matmul_fp8(int M, int N, int K, const MatmulPlan& p, void* ws, const void* a, const void* b,
                              const void* add, void* out, hipStream_t st);
 // out [n] = sum of `splits` pieces of n fp32 sums in order (+ add).
 hipError_t launch_matmul_join(const float* part, int splits, size_t n, const bf16_t* add, bf16_t* out, hipStream_t st);
-// y [T][n] = Q(x) w^T (+ add) for few tokens, x quantised on the way, where linear_few says so.
-bool linear_few(int T, int k, int n);
+// y [T][n] = Q(x) w^T (+ add) for few tokens or small matrices, x quantised on the way, where linear_few says so.
 struct LinearFewPlan {
   size_t total;
-  int splits, chunk;  // pieces of the reduction, runs of 128 of each
+  int form, splits, chunk;  // blocks of tokens; pieces of the reduction, runs of 128 of each
+  float us;                 // what it takes, by the model
 };
 LinearFewPlan plan_linear_few(int T, int k, int n);
+bool linear_few(const LinearFewPlan& p, int T, int k, int n);
 hipError_t launch_linear_few(int T, int k, int n, const LinearFewPlan& p, void* ws, const void* x, const void* w,
                              const void* add, void* y, hipStream_t st);
 // A linear layer's gradients: dx [T][k] = dyq w_t^T (+ add) and dw [n][k] = dyt xt^T, in one launch where both

@@ -1,4 +1,4 @@
-// y = Q(x) W^T for few tokens, x quantised on the way (include/lc_moe_block.h).
+// y = Q(x) W^T for few tokens or small matrices, x quantised on the way (include/lc_moe_block.h).
 //
 // With few tokens the weight's bytes bound the product, and next to them every launch counts.  A wavefront
 // multiplies all tokens with 32 rows of W over whole runs of 128 columns by itself: it loads the codes
@@ -11,10 +11,11 @@
 // cache lines a load: 15.9 -> 14.1 us at T = 16, k = n = 6144).
 //
 // Measured, against one launch that quantises x and one or two that multiply (fp8_matmul.hip), us:
-//   k = n = 6144   T = 1: 10.1 (3.7 TB/s of W; 16.0)   16: 14.1 (17.6)   32: 20.1 (18.8)
-//   k = n = 1024   T = 1:  3.9 (9.0)                   16:  4.5 (9.5)    64:  7.9 (9.8)
-// Each workgroup reads x anew through its L2: about 6.5 us a 10^9 products of T n k.  Above 0.7 10^9 what
-// that costs passes what the launches cost, and linear_few says no.
+//   k = n = 6144   T = 1: 10.0 (3.8 TB/s of W; 15.5)   16: 13.9 (17.1)   32: 20.4 (18.4)
+//   k = n = 1024   T = 1:  4.0 (9.2)                   64:  4.8 (9.8)   400:  8.2 (10.2)   777: 14.6 (10.6)
+//   k = n =  520   T = 1:  3.8 (8.1)                   64:  4.0 (9.1)   777:  6.0 (9.7)   4000: 23.7 (12.8)
+// What bounds it is a CU's loads: a run of 32 rows of W and of 16 tokens is 8 KB, of 64 tokens 20 KB, and
+// every workgroup reads x anew.  linear_few weighs the two ways by kFewForms and the product's own figures.
 #include "block.h"
 #include "train.h"
 
@@ -47,6 +48,13 @@ __device__ __forceinline__ int fp8_exp_of_bf16(int bits) {
 }
 
 constexpr int kFewWaves = 8;  // wavefronts of a workgroup, among which its runs go in turn
+// Blocks of tokens, and what they take (us, measured): a run of 128 columns on a CU, and one more workgroup
+// on it.  (64, 1024, 1024): 4.7 us in blocks of 16 tokens, 5.7 of 32, 7.9 of 64; (777, 520, 520): 7.5, 6.8, 5.9.
+struct FewForm {
+  int tokens;
+  float run, next;
+};
+constexpr FewForm kFewForms[] = {{16, 0.2f, 0.5f}, {32, 0.33f, 0.8f}, {64, 0.6f, 1.3f}};
 
 // MB: blocks of 16 tokens.
 template <int MB>
@@ -56,7 +64,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void linear_few_kernel(FewArgs p) {
   __shared__ __attribute__((aligned(16))) float sums[WAVES][ROWS][COLS];
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int tile = blockIdx.x % p.tiles, split = blockIdx.x / p.tiles;
+  const int tile = blockIdx.x % p.tiles, split = blockIdx.x / p.tiles, t0 = blockIdx.y * ROWS;
   const int n0 = tile * COLS, k0 = split * p.chunk, k1 = min(k0 + p.chunk, p.nkb);
 
   const unsigned char* wrow[NB];  // rows past the matrix read its last row and are not stored
@@ -64,7 +72,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void linear_few_kernel(FewArgs p) {
   for (int j = 0; j < NB; ++j) wrow[j] = p.w + size_t(min(n0 + j * 16 + l16, p.n - 1)) * p.ldw + g * 16;
   const bf16_t* xrow[MB];
 #pragma unroll
-  for (int i = 0; i < MB; ++i) xrow[i] = p.x + size_t(min(i * 16 + l16, p.T - 1)) * p.k + g * 16;
+  for (int i = 0; i < MB; ++i) xrow[i] = p.x + size_t(min(t0 + i * 16 + l16, p.T - 1)) * p.k + g * 16;
 
   f32x4 acc[MB][NB];
 #pragma unroll
@@ -149,7 +157,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void linear_few_kernel(FewArgs p) {
   __syncthreads();
   for (int i = tid; i < ROWS * PIECES; i += WAVES * 64) {
     const int r = i / PIECES, c = i % PIECES, col = n0 + c * 4;
-    if (r >= p.T || col >= p.n) continue;
+    if (t0 + r >= p.T || col >= p.n) continue;
     const int slot = (c ^ (r % PIECES)) * 4;
     float4 f = *reinterpret_cast<const float4*>(&sums[0][r][slot]);
 #pragma unroll
@@ -157,7 +165,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void linear_few_kernel(FewArgs p) {
       const float4 v = *reinterpret_cast<const float4*>(&sums[w][r][slot]);
       f.x += v.x, f.y += v.y, f.z += v.z, f.w += v.w;
     }
-    const size_t at = size_t(r) * p.n + col;
+    const size_t at = size_t(t0 + r) * p.n + col;
     if (p.part) {
       *reinterpret_cast<float4*>(p.part + size_t(split) * p.T * p.n + at) = f;
       continue;
@@ -171,18 +179,33 @@ __global__ __launch_bounds__(kFewWaves * 64) void linear_few_kernel(FewArgs p) {
   }
 }
 
-bool linear_few(int T, int k, int n) { return T <= 64 && double(T) * n * k <= 0.7e9; }
-
-// Pieces of the columns: one while every wave has at most two runs of them (a piece more costs the launch that
-// joins them, 2 us), else as many as give each CU a workgroup and every wave of it a run.
+// The blocks of tokens and the number of pieces of the columns that take the least by these figures.  Every
+// wave of a piece has a run; pieces are joined by a second kernel.
 LinearFewPlan plan_linear_few(int T, int k, int n) {
   LinearFewPlan p{};
   const int nkb = (k + 127) / 128, tiles = (n + 31) / 32;
-  const int want = nkb <= 2 * kFewWaves ? 1 : max(1, min(256 / tiles, nkb / kFewWaves));
-  p.chunk = (nkb + want - 1) / want;
-  p.splits = (nkb + p.chunk - 1) / p.chunk;
+  p.us = 1e30f;
+  for (int f = 0; f < 3; ++f) {
+    const FewForm& o = kFewForms[f];
+    const int blocks = (T + o.tokens - 1) / o.tokens;
+    if (blocks > 65535 || (f > 0 && T <= kFewForms[f - 1].tokens)) continue;
+    for (int want : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (want > 1 && want * kFewWaves > nkb) break;
+      const int chunk = (nkb + want - 1) / want, splits = (nkb + chunk - 1) / chunk;
+      if (splits != want) continue;
+      const int64_t each = (int64_t(tiles) * blocks * splits + 255) / 256;  // workgroups of a CU
+      float t = 3.2f + float(each) * float(chunk) * o.run + float(each - 1) * o.next;
+      if (splits > 1) t += 2.f + float(splits) * float(T) * float(n) * 8 / 5e6f;
+      if (t < p.us) p.us = t, p.form = f, p.chunk = chunk, p.splits = splits;
+    }
+  }
   p.total = p.splits > 1 ? align256(size_t(p.splits) * T * n * 4) : 256;
   return p;
+}
+
+// Against a launch that quantises the tokens (2.5 us and their bytes) and the product's.
+bool linear_few(const LinearFewPlan& p, int T, int k, int n) {
+  return p.us < 2.5f + float(T) * float(k) * 3 / 5e6f + plan_matmul_fp8(T, n, k).us;
 }
 
 hipError_t launch_linear_few(int T, int k, int n, const LinearFewPlan& p, void* ws, const void* x, const void* w,
@@ -192,9 +215,10 @@ hipError_t launch_linear_few(int T, int k, int n, const LinearFewPlan& p, void* 
   const int tiles = (n + 31) / 32;
   const FewArgs a{static_cast<const bf16_t*>(x), wc, wc + m.scales, m.ldc, m.lds, static_cast<const bf16_t*>(add),
                   static_cast<bf16_t*>(y), p.splits > 1 ? static_cast<float*>(ws) : nullptr, T, k, n, m.nkb, p.chunk, tiles};
-  const dim3 grid(unsigned(tiles * p.splits)), block(kFewWaves * 64);
-  if (T <= 16) linear_few_kernel<1><<<grid, block, 0, st>>>(a);
-  else if (T <= 32) linear_few_kernel<2><<<grid, block, 0, st>>>(a);
+  const int tokens = kFewForms[p.form].tokens;
+  const dim3 grid(unsigned(tiles * p.splits), unsigned((T + tokens - 1) / tokens)), block(kFewWaves * 64);
+  if (p.form == 0) linear_few_kernel<1><<<grid, block, 0, st>>>(a);
+  else if (p.form == 1) linear_few_kernel<2><<<grid, block, 0, st>>>(a);
   else linear_few_kernel<4><<<grid, block, 0, st>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;

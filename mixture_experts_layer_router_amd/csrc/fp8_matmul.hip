@@ -442,6 +442,7 @@ MatmulPlan plan_matmul_fp8(int M, int N, int K) {
     }
   }
   p.splits = (nkb + p.chunk - 1) / p.chunk;
+  p.us = float(best);
   p.part = 0;
   p.total = p.splits > 1 ? align256(size_t(p.splits) * M * N * 4) : 256;
   return p;

@@ -227,6 +227,7 @@ def test_linear_refusals():
     for k in ("dy", "x", "w", "add", "dx", "dw", "ws"):
         assert bw(**{k: MIS}) == ALIGN, k
     assert bw(nb=nb_ - 1) == WORKSPACE and bw(T=0, dw=None) == OK and bw(dx=None, dw=None) == OK
+    assert bw() == SHAPE and bw(dw=None) == SHAPE  # dx is dy
 
 
 def test_wrappers_refuse_tensors_off_the_gpu():
