@@ -174,8 +174,8 @@ def select(logits, bias, K, gating, token_mask=None):
     if token_mask is not None:
         _need(token_mask, "token_mask", (T,), torch.uint8, dev)
     _on_gpu(dev)
-    idx = torch.empty((T, K), dtype=torch.int32, device=dev)
-    gate = torch.empty((T, K), dtype=torch.float32, device=dev)
+    idx = torch.empty(T, K, dtype=torch.int32, device=dev)
+    gate = torch.empty_like(idx, dtype=torch.float32)
     _on(dev, lc_moe_select, _select_shape(T, E, K), gating, logits, bias, token_mask, idx, gate)
     return idx, gate
 
@@ -194,8 +194,8 @@ def route_select(x, w_router, bias, K, N, gating, token_mask=None, workspace=Non
         _need(token_mask, "token_mask", (T,), torch.uint8, dev)
     shape = Shape(T, d, N, E - N, K, 8, _dtype_code(x, "x"))
     ws = _space(lc_moe_workspace_size(shape), workspace, dev, "lc_moe_workspace_size", (x, w_router, bias, token_mask))
-    idx = torch.empty((T, K), dtype=torch.int32, device=dev)
-    gate = torch.empty((T, K), dtype=torch.float32, device=dev)
+    idx = torch.empty(T, K, dtype=torch.int32, device=dev)
+    gate = torch.empty_like(idx, dtype=torch.float32)
     _on(dev, lc_moe_route_select, shape, gating, x, w_router, bias, token_mask, idx, gate, ws)
     return idx, gate
 
@@ -343,7 +343,7 @@ def _added(add, out, name, size, dev, others):
         same = add is not None and add.data_ptr() == out.data_ptr()
         _apart("out", out, (*others, None if same else add))
         return out
-    return torch.empty(size, dtype=torch.bfloat16, device=dev)
+    return torch.empty(*size, dtype=torch.bfloat16, device=dev)
 
 
 def matmul_fp8(a, b, add=None, out=None, workspace=None):
@@ -388,7 +388,7 @@ def linear_fp8_backward(dy, x, w, dx_add=None, dx=None, need_dx=True, need_dw=Tr
         _buffer(w.t, "w", k, n, dev)
         out["dx"] = _added(dx_add, dx, "dx_add", (T, k), dev, (x, dy, w.t))
     if need_dw:
-        out["dw"] = torch.empty((n, k), dtype=torch.bfloat16, device=dev)
+        out["dw"] = torch.empty(n, k, dtype=torch.bfloat16, device=dev)
     ws = _space(_lib().lc_moe_linear_fp8_backward_workspace_size(T, k, n), workspace, dev,
                 "lc_moe_linear_fp8_backward_workspace_size", (x, dy, w.t, dx_add, out.get("dx")))
     _on(dev, lc_moe_linear_fp8_backward, T, k, n, dy, x, w.t, dx_add, out.get("dx"), out.get("dw"), ws)
