@@ -266,12 +266,9 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a, int room) {
     }
     const bool two = a.rank == 2 && m2 > -INFINITY;
     const float best = two ? m1 + m2 : m1;
-    int before = 0;  // groups ahead of the lane's
-    for (int j = 0; j < a.groups; ++j) {
-      const float bj = lane_value(best, j << sh);
-      before += (g > j ? bj >= best : bj > best) ? 1 : 0;
-    }
-    const bool kept = before < a.top_groups;
+    int before = 0;  // groups ahead of the lane's, but for equal ones: if they make it too many, fp64 decides
+    for (int j = 0; j < a.groups; ++j) before += lane_value(best, j << sh) > best ? 1 : 0;
+    const bool kept = g < a.groups && before < a.top_groups;
     // half a step of every fp32 value that went into a group's score, and its scores' errors
     const float err = m1 > -INFINITY ? (two ? 2.f * serr + (fabsf(m1) + fabsf(m2) + fabsf(best)) * 0x1.1p-24f
                                             : serr + fabsf(m1) * 0x1.1p-24f) : 0.f;
@@ -279,7 +276,8 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a, int room) {
     const float most = __ockl_wfred_max_f32(kept || g >= a.groups ? -INFINITY : best + err);
     wave_fence();
     // (two biases near the largest float may overflow: fp64 then tells the groups apart)
-    whole = (most > -INFINITY && !(least > most)) || __ballot(m1 > -INFINITY && !(fabsf(best) < INFINITY));
+    whole = (most > -INFINITY && !(least > most)) || __ballot(m1 > -INFINITY && !(fabsf(best) < INFINITY)) ||
+            __popcll(__ballot(kept && m1 > -INFINITY)) > a.top_groups << sh;
     const unsigned long long live = __ballot(kept);
     const uint32_t magic = uint32_t((0x100000000ull + a.size - 1) / a.size);  // e / size, exact for e, size < 2^16
     auto keep = [&](int e) {
