@@ -1,6 +1,8 @@
 // Internal definitions of the block operators (include/lc_moe_block.h).
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 #include "lc_moe_block.h"
 
@@ -84,5 +86,23 @@ hipError_t launch_linear_few(int T, int k, int n, const LinearFewPlan& p, void* 
 // take the same small tiles.  ws: room for either's plan.
 hipError_t launch_matmul_gradients(int T, int k, int n, void* ws, const void* dyq, const void* w_t, const void* add,
                                    void* dx, const void* dyt, const void* xt, void* dw, hipStream_t st);
+
+// Largest over the 16 lanes of a row, and over the four rows of a wavefront (lanes l, l + 16, ...), in every
+// lane, without LDS.
+__device__ __forceinline__ float max_of_row(float v) {
+  const auto turned = [](float v, auto by) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), 0x120 + decltype(by)::value, 0xF, 0xF, true));
+  };
+  v = fmaxf(v, turned(v, std::integral_constant<int, 8>()));
+  v = fmaxf(v, turned(v, std::integral_constant<int, 4>()));
+  v = fmaxf(v, turned(v, std::integral_constant<int, 2>()));
+  return fmaxf(v, turned(v, std::integral_constant<int, 1>()));
+}
+__device__ __forceinline__ uint32_t max_of_rows(uint32_t v) {
+  const auto near = __builtin_amdgcn_permlane16_swap(v, v, false, false);  // rows 0 0 2 2 and 1 1 3 3
+  v = near[0] > near[1] ? near[0] : near[1];
+  const auto far = __builtin_amdgcn_permlane32_swap(v, v, false, false);  // the lower half twice, and the upper
+  return far[0] > far[1] ? far[0] : far[1];
+}
 
 }  // namespace lcm

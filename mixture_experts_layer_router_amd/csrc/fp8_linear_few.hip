@@ -126,9 +126,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void linear_few_kernel(FewArgs p) {
       for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int e = 0; e < 4; ++e) m = abs_max(m, nx[i][q][e]);
-      int bits = max(int(m[0]), int(m[1]));
-      bits = max(bits, __shfl_xor(bits, 16));
-      bits = max(bits, __shfl_xor(bits, 32));
+      const int bits = int(max_of_rows(max(uint32_t(m[0]), uint32_t(m[1]))));
       sa[i] = fp8_exp_of_bf16(bits) + 127;
       const float unit = __uint_as_float(uint32_t(sa[i]) << 23);  // the conversion reads the exponent alone
 #pragma unroll

@@ -4,8 +4,9 @@
 // A workgroup takes a tile of 128 x 128; thread (rg, cg) = (tid / 16, tid % 16) holds rows
 // 8 rg .. 8 rg + 7 and columns 8 cg .. 8 cg + 7 of it.  The codes of the transpose go through
 // LDS, so that they too leave in whole 128-byte rows.  Memory bounds it: 16384 x 6144 bf16 along the rows
-// takes 49-51 us (6 TB/s); dy both ways and x by its columns for a linear layer's gradient (n = 2048, k = 6144:
-// 436 MB) 93 us (4.7 TB/s; 99 before the transpose's codes went to all banks alike).
+// takes 49-51 us (6 TB/s), both forms 81 (5 TB/s); dy both ways and x by its columns for a linear layer's
+// gradient (n = 2048, k = 6144: 436 MB) 77 us (5.7 TB/s; 93 with the rows' maxima through LDS and those of
+// the columns from 16 rows of it, 99 with the transpose's codes on few banks too).
 #include "block.h"
 
 namespace lcm {
@@ -40,7 +41,7 @@ __device__ __forceinline__ void quantize_tile(const QuantizeArgs& q, int tile_in
   const int rows = q.rows, cols = q.cols;
   const Fp8Mat m = q.m, mt = q.mt;
   unsigned char *__restrict__ out = q.out, *__restrict__ out_t = q.out_t;
-  __shared__ float colmax[16][128];
+  __shared__ float colmax[4][128];
   __shared__ float wmax[4];
   // Codes of the transpose: row stride 144, 16-byte piece p of row c in slot p ^ (c / 16): the 16 x 4 threads
   // of a wave, 8 rows and half a piece apart, then write to all banks alike (without: 8 of them to one).
@@ -67,8 +68,7 @@ __device__ __forceinline__ void quantize_tile(const QuantizeArgs& q, int tile_in
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[i][j]));
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+    amax = __uint_as_float(max_of_rows(__float_as_uint(max_of_row(amax))));
     if ((tid & 63) == 0) wmax[tid >> 6] = amax;
     __syncthreads();
     const int k = fp8_exp(fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3])));
@@ -81,9 +81,7 @@ __device__ __forceinline__ void quantize_tile(const QuantizeArgs& q, int tile_in
         float amax = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[i][j]));
-#pragma unroll
-        for (int o = 8; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
-        kr[i] = fp8_exp(amax);
+        kr[i] = fp8_exp(max_of_row(amax));
       }
     }
     if constexpr (COLS) {
@@ -92,14 +90,15 @@ __device__ __forceinline__ void quantize_tile(const QuantizeArgs& q, int tile_in
         float amax = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i][j]));
-        colmax[rg][cg * 8 + j] = amax;
+        const uint32_t bits = max_of_rows(__float_as_uint(amax));  // (as numbers: not negative)
+        if ((tid & 48) == 0) colmax[tid >> 6][cg * 8 + j] = __uint_as_float(bits);
       }
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         float amax = 0.f;
 #pragma unroll
-        for (int g = 0; g < 16; ++g) amax = fmaxf(amax, colmax[g][cg * 8 + j]);
+        for (int g = 0; g < 4; ++g) amax = fmaxf(amax, colmax[g][cg * 8 + j]);
         kc[j] = fp8_exp(amax);
       }
     }

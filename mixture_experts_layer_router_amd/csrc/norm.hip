@@ -249,13 +249,13 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(NormBwArgs
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       s_pre[j][i] = s_post[j][i] = s_gate[j][i] = 0.f;
-      if (!KEEP && i % 4 == 0)
+      if constexpr (!KEEP)
         room[0][(j * N + i) / 4][threadIdx.x] = room[1][(j * N + i) / 4][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   int tid = threadIdx.x;
   auto from_room = [&](int j) {
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
+    for (int i = 0; i < N && !KEEP; i += 4) {
       const float4 f = room[0][(j * N + i) / 4][tid], g = room[1][(j * N + i) / 4][tid];
       s_post[j][i] = f.x, s_post[j][i + 1] = f.y, s_post[j][i + 2] = f.z, s_post[j][i + 3] = f.w;
       s_gate[j][i] = g.x, s_gate[j][i + 1] = g.y, s_gate[j][i + 2] = g.z, s_gate[j][i + 3] = g.w;
@@ -263,7 +263,7 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(NormBwArgs
   };
   auto to_room = [&](int j) {
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
+    for (int i = 0; i < N && !KEEP; i += 4) {
       room[0][(j * N + i) / 4][tid] = make_float4(s_post[j][i], s_post[j][i + 1], s_post[j][i + 2], s_post[j][i + 3]);
       room[1][(j * N + i) / 4][tid] = make_float4(s_gate[j][i], s_gate[j][i + 1], s_gate[j][i + 2], s_gate[j][i + 3]);
     }

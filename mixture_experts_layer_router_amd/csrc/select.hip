@@ -2,8 +2,8 @@
 // (include/lc_moe_block.h): softmax or sigmoid scores, a bias for the choice, groups of experts,
 // top-K, renormalised gates.  One wavefront a token.
 //
-// Measured at T = 16384, E = 768: the choice (K = 12, sigmoid, 8 groups) takes 28-29 us, its 50 MB read at
-// 1.8 TB/s; the vector units bound it: 850 instructions a token fill 55 of its 68 thousand cycles.  The
+// Measured at T = 16384, E = 768: the choice (K = 12, sigmoid, 8 groups) takes 27-28 us, its 50 MB read at
+// 1.8 TB/s; the vector units bound it: 820 instructions a token fill 53 of its 66 thousand cycles.  The
 // gradient takes 20 us (5 TB/s).
 #include "block.h"
 #include "logit_row.h"
