@@ -82,7 +82,7 @@ lc_moe_status lc_moe_route_select(const lc_moe_shape* shape, const lc_moe_gating
 
 /* Gradient of the gates with respect to the logits, the choice held fixed.  With dg the
  * gradient of a token's gates, w_k = s_k / sum of the picked s:
- *   renorm:      a_k = scale w_k (dg_k - sum_j w_j dg_j);  dlogits of pick k: a_k (softmax) or
+ *   renorm:      a_k = scale w_k sum_j w_j (dg_k - dg_j);  dlogits of pick k: a_k (softmax) or
  *                a_k (1 - s_k) (sigmoid); no other logit has a gradient
  *   else:        sigmoid: scale dg_k s_k (1 - s_k) at the picks;
  *                softmax: p_i (dp_i - sum_j p_j dp_j), dp_i = scale sum of dg_k over the picks of i

@@ -501,7 +501,11 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectBwArgs a) {
     if (!soft) u *= s;
     const float sum = __ockl_wfred_add_f32(u);
     const float w = sum > 0.f ? u / sum : 0.f;
-    v = a.scale * (w * (dg - __ockl_wfred_add_f32(w * dg)));
+    // The shares sum to 1, so dg_k - sum w_j dg_j is a sum of differences, in which nothing cancels that is
+    // not alike in dg itself: one pick, or gradients that are all the same, give 0.
+    float rest = 0.f;
+    for (int j = 0; j < a.K; ++j) rest = fmaf(lane_value(w, j), dg - lane_value(dg, j), rest);
+    v = a.scale * (w * rest);
     if (!soft) v *= x > 0.f ? exp_neg(-x) * s : s;  // 1 - s
   } else if (a.score == LC_MOE_SIGMOID) {
     const float q = exp_neg(-fabsf(x)), s = 1.f / (1.f + q);
