@@ -143,7 +143,8 @@ lc_moe_status lc_moe_expert_load(const lc_moe_shape* shape, const int32_t* topk_
  *   perm_token   [T*K] int32 (out)   token of each row; rows of expert e are
  *                                    ffn_offsets[e]..ffn_offsets[e+1]-1, in (token,
  *                                    pick) order; entries from nnz on are untouched
- *   slot_row     [T][K] int32 (out)  row of pick (t,k), -1 for a zero-computation pick
+ *   slot_row     [T][K] int32 (out)  row of pick (t,k), -1 for a zero-computation pick, -2 for
+ *                                    an index outside 0..N+Z-1 (no pick)
  *   x_perm       [T*K][d] dtype (out) x_perm[r] = x[perm_token[r]] for r < nnz; may be NULL
  *   load         [N+Z] int32 (out)   as lc_moe_expert_load; may be NULL */
 lc_moe_status lc_moe_permute(const lc_moe_shape* shape, const void* x, const int32_t* topk_idx,

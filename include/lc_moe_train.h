@@ -33,7 +33,8 @@ typedef struct {
   const float* logits;        /* [T][N+Z] router logits x W_r^T                              */
   const void* ffn_rows;       /* [T*K][d] dtype: output of every FFN pick, one row each;
                                  rows from ffn_offsets[N] on are unwritten                 */
-  const int32_t* slot_row;    /* [T][K] row of every pick, -1 for a zero-computation pick    */
+  const int32_t* slot_row;    /* [T][K] row of every pick, -1 for a zero-computation pick,
+                                 -2 for an index outside 0..N+Z-1                        */
   const int32_t* ffn_offsets; /* [N+1] first row of every FFN expert                        */
   const int32_t* perm_token;  /* [T*K] token of every row                                   */
 } lc_moe_saved;
@@ -95,9 +96,9 @@ lc_moe_status lc_moe_balance_loss(const lc_moe_shape* shape, const lc_moe_balanc
 
 /* Gradient of L = sum_t <dy_t, y_t> with respect to the gates: for an FFN pick (t, k)
  *   dgate[t][k] = <dy_t, ffn_rows[slot_row[t][k]]>,
- * for a zero-computation pick (slot_row < 0) dgate[t][k] = <dy_t, x_t>.  Products and sums
- * are fp32, added in a fixed order.  A row index of num_rows or more reads nothing and
- * gives 0.
+ * for a zero-computation pick (slot_row -1) dgate[t][k] = <dy_t, x_t>.  Products and sums
+ * are fp32, added in a fixed order.  A row index of num_rows or more, or below -1 (no pick),
+ * gives 0, whatever dy_t and x_t hold.
  *   x, dy      [T][d] dtype
  *   ffn_rows   [num_rows][d] dtype, 0 <= num_rows <= T*K (else LC_MOE_E_SHAPE); may be NULL if
  *              num_rows = 0

@@ -40,10 +40,10 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const Tp* __restrict
   bool none[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    // picks past the last repeat it; rows out of range read x and give 0
+    // picks past the last repeat it; rows out of range and places without a pick read x and give 0
     const int k = k0 + i < K ? k0 + i : K - 1;
     const int r = __builtin_amdgcn_readfirstlane(slot_row[size_t(t) * K + k]);
-    none[i] = r >= num_rows;
+    none[i] = r >= num_rows || r < -1;
     a[i] = r < 0 || r >= num_rows ? x + size_t(t) * d : rows + size_t(r) * d;
     acc[i] = 0.f;
   }

@@ -18,6 +18,12 @@
 
 namespace lcm {
 
+// slot_row of a pick that gets no row: -1 for a zero-computation expert, -2 for an index outside the pool,
+// which is no pick at all.
+__device__ __forceinline__ int no_row(int e, int E) {
+  return static_cast<unsigned>(e) < static_cast<unsigned>(E) ? -1 : -2;
+}
+
 __global__ __launch_bounds__(256) void histogram_kernel(const int32_t* __restrict__ idx,
                                                         int32_t* __restrict__ block_counts,
                                                         int32_t* __restrict__ ffn_cnt, int T,
@@ -119,13 +125,13 @@ __global__ __launch_bounds__(1024) void scan_kernel(const int32_t* __restrict__ 
 
 // Ranks the FFN picks of tokens t0..t1-1 one by one in (token, pick) order, run[e] holding
 // the next row of expert e; one thread, for token blocks with repeated picks.
-__device__ void scatter_serial(const int32_t* __restrict__ idx, int t0, int t1, int K, int N,
+__device__ void scatter_serial(const int32_t* __restrict__ idx, int t0, int t1, int K, int E, int N,
                                int* run, int32_t* __restrict__ slot_row,
                                int32_t* __restrict__ perm_token) {
   for (int t = t0; t < t1; ++t)
     for (int k = 0; k < K; ++k) {
       const int e = idx[size_t(t) * K + k];
-      int row = -1;
+      int row = no_row(e, E);
       if (static_cast<unsigned>(e) < static_cast<unsigned>(N)) {
         row = run[e]++;
         perm_token[row] = t;
@@ -139,7 +145,7 @@ __global__ __launch_bounds__(256) void scatter_kernel(const int32_t* __restrict_
                                                       const int32_t* __restrict__ block_base,
                                                       int32_t* __restrict__ slot_row,
                                                       int32_t* __restrict__ perm_token, int T,
-                                                      int K, int N) {
+                                                      int K, int E, int N) {
   extern __shared__ unsigned long long masks[];  // [4][N]; reused as int run[N]
   __shared__ int repeated;                       // a token of the block picks an expert twice
   const int tid = threadIdx.x, b = blockIdx.x;
@@ -162,14 +168,14 @@ __global__ __launch_bounds__(256) void scatter_kernel(const int32_t* __restrict_
     int* run = reinterpret_cast<int*>(masks);
     for (int e = tid; e < N; e += 256) run[e] = block_base[size_t(b) * N + e];
     __syncthreads();
-    if (tid == 0) scatter_serial(idx, b * kTokBlock, min(T, (b + 1) * kTokBlock), K, N, run, slot_row, perm_token);
+    if (tid == 0) scatter_serial(idx, b * kTokBlock, min(T, (b + 1) * kTokBlock), K, E, N, run, slot_row, perm_token);
     return;
   }
   if (t < T) {
     const unsigned long long below_lane = (1ull << lane) - 1ull;
     for (int k = 0; k < K; ++k) {
       const int e = idx[size_t(t) * K + k];
-      int row = -1;
+      int row = no_row(e, E);
       if (static_cast<unsigned>(e) < static_cast<unsigned>(N)) {
         int rank = __popcll(masks[w * N + e] & below_lane);
         for (int ww = 0; ww < w; ++ww) rank += __popcll(masks[ww * N + e]);
@@ -274,14 +280,14 @@ __device__ void permute_block(BlockLds& L, const int32_t* __restrict__ idx, int 
   }
   __syncthreads();
   if (L.repeated) {  // uniform over the workgroup
-    if (tid == 0) scatter_serial(idx, 0, T, K, N, L.off, slot_row, perm_token);
+    if (tid == 0) scatter_serial(idx, 0, T, K, E, N, L.off, slot_row, perm_token);
     return;
   }
   if (t < T) {
     const unsigned long long below_lane = (1ull << lane) - 1ull;
     for (int k = 0; k < K; ++k) {
       const int e = idx[size_t(t) * K + k];
-      int row = -1;
+      int row = no_row(e, E);
       if (static_cast<unsigned>(e) < static_cast<unsigned>(N)) {
         int rank = __popcll(L.masks[w * N + e] & below_lane);
         for (int ww = 0; ww < w; ++ww) rank += __popcll(L.masks[ww * N + e]);
@@ -402,7 +408,7 @@ hipError_t launch_scatter(const lc_moe_shape& s, const int32_t* idx, const int32
                           int nblocks, int32_t* slot_row, int32_t* perm_token, hipStream_t st) {
   const size_t lds = size_t(4) * s.N * sizeof(unsigned long long);
   hipLaunchKernelGGL(scatter_kernel, dim3(nblocks), dim3(256), lds, st, idx, block_base,
-                     slot_row, perm_token, s.T, s.K, s.N);
+                     slot_row, perm_token, s.T, s.K, s.N + s.Z, s.N);
   return hipGetLastError();
 }
 
