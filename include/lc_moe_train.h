@@ -121,6 +121,8 @@ lc_moe_status lc_moe_gate_backward(const lc_moe_shape* shape, const void* x, con
  * values below 2^-17 of their row's largest down to 2^-39 of it.  dx is rounded once.
  * A pick outside 0..N+Z-1 has no gradient.  A token whose logits are all -infinity has
  * dlogits = dlogits_aux.
+ * With dgate NULL a token whose row of dlogits_aux is all zero (padding) adds nothing to
+ * dw_router, whatever its row of x holds, NaN too.
  *   x            [T][d] dtype
  *   w_router     [N+Z][d] fp32
  *   logits       [T][N+Z] fp32, topk_idx [T][K] int32, dgate [T][K] fp32: all three, or dgate

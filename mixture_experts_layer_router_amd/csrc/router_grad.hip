@@ -127,6 +127,7 @@ struct OperandArgs {
                      // or NULL
   float* rscale;     // [T] 2^(x - 28)
   const int32_t* wexp;
+  unsigned char* live;  // [T] 1, or 0 for a token whose dlogits are all zero; or NULL: not asked for
   int T, E, K, Ep;
   uint4* zero;       // 16 zero bytes: the source of operand chunks past the data
 };
@@ -189,6 +190,13 @@ __global__ __launch_bounds__(256) void operands_kernel(OperandArgs a) {
     for (int i = 0; i < EPL; ++i) v[i] += ax[i];
   }
   if (a.out) store_row<EPL, V>(a.out + size_t(t) * E, E, lane, v);
+  if (a.live) {
+    uint32_t any = 0;  // bits: the smallest number is one too
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) any |= __float_as_uint(v[i]) << 1;
+    const bool live = __ballot(any != 0) != 0;
+    if (lane == 0) a.live[t] = live;
+  }
   auto put = [&](bf16_t* dst, int j, const bf16_t (&h)[V]) {
     const int e = (j * 64 + lane) * V;
     if (e >= a.Ep) return;
@@ -262,6 +270,10 @@ __global__ __launch_bounds__(256) void operands_kernel(OperandArgs a) {
 // read over the banks; fp32 chunk c of row r sits in c ^ 8 (r / 8 % 2), so that the two halves of
 // a wave, 8 rows apart, read different banks.  K-contiguous rows are 64 bytes, chunk c in slot
 // c ^ swz4(r), or 32 bytes, c ^ (r / 4 % 2).
+// LIVE (DW): tokens whose dlogits are all zero count for nothing, whatever their rows of B hold: zeros are
+// loaded in the place of those.  (The flags take 8 to 19 us of 900 at T = 16384, d = 6144, E = 768, 3 of 35 at
+// T = 4096, d = 2048, E = 96, 0 of 21 at T = 64; a copy of the tokens with those rows cleared would move 400 MB
+// at the first, 80 us.)
 // ---------------------------------------------------------------------------------------
 struct ProdArgs {
   const bf16_t* a;  // [NA][T][Ep]
@@ -271,13 +283,14 @@ struct ProdArgs {
   const void* add;
   void* c;
   const float* rscale;  // fp16: units of the rows' sums
+  const unsigned char* live;  // LIVE: of the tokens (whole stages, and room for two more)
   int M, N, Kdim, lda, ldb;
   int krows;            // rows of B: the reduction's steps behind them have zeros in A
   int chunk;            // reduction steps of a piece (a multiple of 32)
   int n_mt, n_nt, splits;
 };
 
-template <bool DX, bool F16, bool CUT, int BM, int BN, int NA, int NB, int BK, int NST, typename Tc>
+template <bool DX, bool F16, bool CUT, bool LIVE, int BM, int BN, int NA, int NB, int BK, int NST, typename Tc>
 __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, unsigned char* smem) {
   constexpr int WAVES = BM / 32, WN = 2, WC = BN / WN;  // wave tile: 64 x WC
   constexpr int NBL = WC / 32;                          // 32-wide column blocks of a wave
@@ -291,6 +304,7 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
   static_assert(A_OP % (1024 * WAVES) == 0 && B_OP % (1024 * WAVES) == 0, "whole loads");
   static_assert(!DX || BK == 32 || BK == 16, "K-contiguous rows are staged 64 or 32 bytes at a time");
   static_assert(NBL == 2 || NBL == 4, "wave tiles of 64 or 128 columns");
+  static_assert(!LIVE || (!DX && BK == 32 && NL == 1), "a stage's tokens in one word");
 
   // unit: pieces of the reduction, in them groups of 8 M-tiles, in a group column tiles, in them
   // its M-tiles; each XCD takes a contiguous eighth, so workgroups side by side share operand
@@ -311,6 +325,14 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
+  // The flags of the 32 tokens from k on, in scalar loads (the count of the direct ones stays as it is), two
+  // stages ahead.
+  typedef uint64_t u64x4 __attribute__((ext_vector_type(4)));
+  auto flags_from = [&](int k) {
+    return *reinterpret_cast<const __attribute__((address_space(4))) u64x4*>(reinterpret_cast<uintptr_t>(p.live + k));
+  };
+  u64x4 flags = {}, next_flags = {};
+  if constexpr (LIVE) flags = flags_from(kbeg), next_flags = flags_from(kbeg + BK);
 
   // A wave's load i of an operand with contiguous columns (BC of 2 bytes) fills bytes
   // 1024 (wave + WAVES i) of its part: 512 / BC rows of 2 BC bytes.
@@ -360,12 +382,32 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
     const bf16_t* a0 = DX ? p.a + size_t(m0) * p.lda + k0 : p.a + size_t(k0) * p.lda + m0;
     const char* b0 = static_cast<const char*>(p.b) + (size_t(k0) * p.ldb + n0) * EB;
     const size_t plane_b = size_t(p.krows) * p.ldb * EB;  // bytes of a part of B
+    uint32_t live = ~0u;  // bit i: token k0 + i counts
+    if constexpr (LIVE) {
+      constexpr uint64_t ONES = 0x0101010101010101ull;  // (bytes behind the last token hold anything)
+      if ((flags[0] & flags[1] & flags[2] & flags[3] & ONES) != ONES) {
+        live = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) live |= uint32_t((flags[j] & ONES) * 0x0102040810204080ull >> 56) << (8 * j);
+      }
+      flags = next_flags;
+      next_flags = flags_from(k0 + 2 * BK);
+    }
     if (near && k0 + BK <= krows) {
 #pragma unroll
       for (int q = 0; q < NA; ++q) {
         const char* g = reinterpret_cast<const char*>(a0 + q * p.plane_a);
 #pragma unroll
         for (int i = 0; i < LA; ++i) dma16(g + off_a[i], st + q * A_OP + (wave + WAVES * i) * 1024);
+      }
+      if (LIVE && live != ~0u) {
+#pragma unroll
+        for (int i = 0; i < LB; ++i) {
+          int kr, ch;
+          b_place(i, kr, ch);
+          dma16(live >> kr & 1 ? b0 + off_b[i] : reinterpret_cast<const char*>(p.zero), sb + (wave + WAVES * i) * 1024);
+        }
+        return;
       }
 #pragma unroll
       for (int q = 0; q < NL; ++q)
@@ -391,7 +433,7 @@ __device__ __forceinline__ void product_tile(const ProdArgs& p, unsigned block, 
       for (int i = 0; i < LB; ++i) {
         int kr, ch;
         b_place(i, kr, ch);
-        const bool in = k0 + kr < krows && n0 + ch * CC < p.ldb;
+        const bool in = k0 + kr < krows && n0 + ch * CC < p.ldb && (!LIVE || (live >> kr & 1));
         dma16(in ? b0 + q * plane_b + size_t(kr) * p.ldb * EB + ch * 16 : reinterpret_cast<const char*>(p.zero),
               sb + q * B_OP + (wave + WAVES * i) * 1024);
       }
@@ -729,7 +771,7 @@ struct ProductsArgs {
   int E;
 };
 
-template <int FORM, bool BF>
+template <int FORM, bool BF, bool LIVE>
 __global__ __launch_bounds__(256, 2) void products_kernel(ProductsArgs a) {
   typedef typename std::conditional<BF, bf16_t, float>::type Tx;
   constexpr int X = BF ? 1 : 3, W = 3;  // parts of the tokens; of W_r (and dlogits for dx)
@@ -738,13 +780,13 @@ __global__ __launch_bounds__(256, 2) void products_kernel(ProductsArgs a) {
   constexpr int LDS = FORM == kRbFew && BF ? 65536 : 81920;
   __shared__ __attribute__((aligned(1024))) unsigned char smem[LDS];
   if (blockIdx.x < a.dw_blocks) {
-    if constexpr (FORM == kRbBig) product_tile<false, false, false, 128, 256, 3, 1, 32, 2, float>(a.dw, blockIdx.x, smem);
-    else product_tile<false, false, !BF, 128, 128, 3, X, 32, 2, float>(a.dw, blockIdx.x, smem);
+    if constexpr (FORM == kRbBig) product_tile<false, false, false, LIVE, 128, 256, 3, 1, 32, 2, float>(a.dw, blockIdx.x, smem);
+    else product_tile<false, false, !BF, LIVE, 128, 128, 3, X, 32, 2, float>(a.dw, blockIdx.x, smem);
   } else {
     const unsigned b = blockIdx.x - a.dw_blocks;
     if constexpr (FORM == kRbFew) dx_few<W, Tx>(a.dx, a.w, a.E, b, reinterpret_cast<float*>(smem));
-    else if constexpr (FORM == kRbSmall) product_tile<true, false, true, 128, 128, W, W, 32, 2, Tx>(a.dx, b, smem);
-    else product_tile<true, true, false, 128, 256, 2, 2, 16, 3, Tx>(a.dx, b, smem);
+    else if constexpr (FORM == kRbSmall) product_tile<true, false, true, false, 128, 128, W, W, 32, 2, Tx>(a.dx, b, smem);
+    else product_tile<true, true, false, false, 128, 256, 2, 2, 16, 3, Tx>(a.dx, b, smem);
   }
 }
 
@@ -780,7 +822,9 @@ static void launch_products(ProductsArgs a, hipStream_t st) {
     a.dx.n_nt = (a.dx.N + BN - 1) / BN;
     dx_blocks = FORM == kRbFew ? size_t(a.dx.N + 31) / 32 : (size_t(a.dx.n_mt) * a.dx.n_nt + 7) / 8 * 8;
   }
-  hipLaunchKernelGGL((products_kernel<FORM, BF>), dim3(unsigned(a.dw_blocks + dx_blocks)), dim3(BM * 2), 0, st, a);
+  const dim3 grid(unsigned(a.dw_blocks + dx_blocks)), block(BM * 2);
+  if (a.dw.live) hipLaunchKernelGGL((products_kernel<FORM, BF, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((products_kernel<FORM, BF, false>), grid, block, 0, st, a);
 }
 
 hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, void* ws, const void* x,
@@ -799,6 +843,9 @@ hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, 
   o.out = dlogits;
   o.parts = reinterpret_cast<bf16_t*>(w + p.dl);
   o.zero = reinterpret_cast<uint4*>(w + p.zero);
+  // Without gradients of the gates a token may have none at all (padding); with them the softmax of its logits is
+  // part of its dlogits, and they and its row must be numbers.
+  if (!dgate && dw) o.live = reinterpret_cast<unsigned char*>(w + p.live);
   o.T = s.T;
   o.E = E;
   o.K = s.K;
@@ -855,6 +902,7 @@ hipError_t launch_router_backward(const lc_moe_shape& s, const RouterBwPlan& p, 
   a.dw.Kdim = s.T;
   a.dw.chunk = p.chunk;
   a.dw.splits = p.splits;
+  a.dw.live = o.live;
   float* part = reinterpret_cast<float*>(w + p.part);
   a.dw.c = !dw ? nullptr : p.splits > 1 ? part : dw;
   if (p.form == kRbBig) launch_products<kRbBig, true>(a, st);

@@ -62,7 +62,7 @@ hipError_t launch_gate_backward(const lc_moe_shape& s, const void* x, const void
 // Ep: E rounded up to whole operand rows (32 experts).
 enum RbForm { kRbFew, kRbSmall, kRbBig };
 struct RouterBwPlan {
-  size_t dl, dl16, rscale, wp, wexp, part, zero, total;
+  size_t dl, dl16, rscale, wp, wexp, part, zero, live, total;
   int Ep;
   RbForm form;
   int splits, chunk;  // dW: pieces of the reduction over the tokens, tokens of each (x 32)
@@ -99,6 +99,7 @@ inline RouterBwPlan plan_router_backward(const lc_moe_shape& s) {
   p.wexp = take(big ? size_t(p.Ep) * 4 : 0);
   p.part = take(p.splits > 1 ? size_t(p.splits) * E * s.d * 4 : 0);
   p.zero = take(16);
+  p.live = take((T + 31) / 32 * 32 + 64);  // a byte a token, whole stages and two behind the last
   p.total = o;
   return p;
 }

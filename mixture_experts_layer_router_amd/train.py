@@ -291,8 +291,8 @@ def layer_backward(x, w_router, w_gate, w_up, w_down, out, dy, workspace, balanc
     ``forward(x, ..., workspace=workspace)`` on bf16 tensors; the workspace is read and not
     written.  The losses are left out (loss None) if both coefficients are 0.  gating: that of the
     forward, if it had one (the losses stay those of the softmax of the logits).  Tokens that its
-    token_mask left out (token_mask here leaves them out of the losses) have no gradient; their
-    rows of x and dy must be finite all the same, since zeros multiply them."""
+    token_mask left out have no gradient, whatever their rows of x and dy hold; token_mask here
+    leaves them out of the losses, which count them else."""
     T, _ = x.shape
     N, I, _ = w_gate.shape
     E, K = w_router.shape[0], out["topk_idx"].shape[1]
