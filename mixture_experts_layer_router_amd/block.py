@@ -300,10 +300,11 @@ def block_norm_backward(h, w_pre, dz, dh=None, y=None, w_post=None, gate=None, r
 
 class Fp8Matrix:
     """A matrix in block FP8: `data` its buffer (codes and scales, see lc_moe_fp8_matrix_size), and
-    `t` the buffer of its transpose, either None if it was not asked for."""
+    `t` the buffer of its transpose, either None if it was not asked for.  block_rows: rows that
+    share a scale; with 128 both forms hold the same values, with 1 each has its own."""
 
-    def __init__(self, rows, cols, data, t):
-        self.rows, self.cols, self.data, self.t = rows, cols, data, t
+    def __init__(self, rows, cols, data, t, block_rows=128):
+        self.rows, self.cols, self.data, self.t, self.block_rows = rows, cols, data, t, block_rows
         self.device = (data if data is not None else t).device
 
 
@@ -324,7 +325,7 @@ def quantize_matrix(x, block_rows=128, rows=True, transposed=False):
             raise LcMoeError(2, "lc_moe_fp8_matrix_size")
         return torch.empty(size, dtype=torch.uint8, device=dev)
 
-    m = Fp8Matrix(R, C, room(R, C) if rows else None, room(C, R) if transposed else None)
+    m = Fp8Matrix(R, C, room(R, C) if rows else None, room(C, R) if transposed else None, block_rows)
     _on(dev, lc_moe_quantize_matrix, x, R, C, block_rows, m.data, m.t)
     return m
 
@@ -377,14 +378,16 @@ def linear_fp8(x, w, add=None, out=None, workspace=None):
 
 def linear_fp8_backward(dy, x, w, dx_add=None, dx=None, need_dx=True, need_dw=True, workspace=None):
     """The gradient of linear_fp8 with FP8 operands: dict(dx [T,k], dw [n,k]), bf16 (see
-    lc_moe_linear_fp8_backward).  w: quantize_matrix(weight, transposed=True).  dx: where to write
-    it (may be dx_add itself)."""
+    lc_moe_linear_fp8_backward).  w: quantize_matrix(weight, transposed=True), whose transpose holds the
+    values that linear_fp8 multiplied by.  dx: where to write it (may be dx_add itself)."""
     T, k = x.shape
     n, dev = w.rows, x.device
     _need(x, "x", (T, w.cols), torch.bfloat16, dev)
     _need(dy, "dy", (T, n), torch.bfloat16, dev)
     out = {}
     if need_dx:
+        if w.block_rows != 128:
+            raise ValueError(f"w: block_rows {w.block_rows}, expected 128: its transpose holds other values than w")
         _buffer(w.t, "w", k, n, dev)
         out["dx"] = _added(dx_add, dx, "dx_add", (T, k), dev, (x, dy, w.t))
     if need_dw:

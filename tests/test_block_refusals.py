@@ -120,3 +120,13 @@ def test_products():
     refused("out overlaps", lambda: back(dy=wide[:32].view(4, 8), dx=wide[:64].view(4, 16)))
     refused("x: torch", lambda: lm.quantize_matrix(zeros(4, 16, dtype=F)), TypeError)
     refused("x must be contiguous", lambda: lm.quantize_matrix(turned(4, 16)))
+
+
+def test_the_gradient_of_a_weight_with_a_scale_for_each_row():
+    """Its transpose has scales for its columns, so it holds other values than the weight that was multiplied by."""
+    x, dy, w = zeros(4, 16), zeros(4, 8), matrix(8, 16, transposed=True)
+    rows = lm.Fp8Matrix(8, 16, w.data, w.t, block_rows=1)
+    refused("block_rows 1", lambda: lm.linear_fp8_backward(dy, x, rows))
+    refused(OFF_GPU, lambda: lm.linear_fp8_backward(dy, x, rows, need_dx=False))  # dw does not read it
+    refused(OFF_GPU, lambda: lm.linear_fp8_backward(dy, x, w))
+    refused(OFF_GPU, lambda: lm.linear_fp8(x, rows))

@@ -39,3 +39,15 @@ def test_workspaces_over_other_tensors():
             lm().block_norm_backward(x, one, **{"dz": None, name: x[:3]})
     with pytest.raises(ValueError, match="rows or transposed"):
         lm().quantize_matrix(x, rows=False)
+
+
+def test_the_gradient_of_a_weight_with_a_scale_for_each_row():
+    import torch
+    say("gradient of a weight with a scale for each row")
+    w, x = torch.randn((16, 24), device=device()).bfloat16(), torch.randn((4, 24), device=device()).bfloat16()
+    dy = torch.randn((4, 16), device=device()).bfloat16()
+    m = lm().quantize_matrix(w, block_rows=1, transposed=True)
+    assert m.block_rows == 1 and lm().quantize_matrix(w).block_rows == 128
+    with pytest.raises(ValueError, match="block_rows 1"):
+        lm().linear_fp8_backward(dy, x, m)
+    assert "dx" not in lm().linear_fp8_backward(dy, x, m, need_dx=False)
