@@ -219,18 +219,23 @@ def select_backward(logits, topk_idx, dgate, gating, dlogits_aux=None):
 def forward_picks(x, topk_idx, topk_gate, w_gate, w_up, w_down, Z, workspace=None, fp8=None, packed=None,
                   fp8_act=False):
     """dict(y, load): the layer for the picks and gates given; Z zero-computation experts.  Weights
-    as ``forward`` takes them."""
+    as ``forward`` takes them: with fp8 or packed, w_gate, w_up and w_down are not read (tensors
+    without storage, of their sizes, will do)."""
     T, d = x.shape
     N, I, _ = w_gate.shape
     K, dev = topk_idx.shape[1], x.device
     _need(x, "x", (T, d), x.dtype, dev)
     _need(topk_idx, "topk_idx", (T, K), torch.int32, dev)
     _need(topk_gate, "topk_gate", (T, K), torch.float32, dev)
+    plain = fp8 is None and packed is None
     for name, w, size in (("w_gate", w_gate, (N, I, d)), ("w_up", w_up, (N, I, d)), ("w_down", w_down, (N, d, I))):
-        _need(w, name, size, x.dtype, dev)
+        if plain:
+            _need(w, name, size, x.dtype, dev)
+        elif w.shape != size:
+            raise ValueError(f"{name}: shape {tuple(w.shape)}, expected {size}")
     shape = Shape(T, d, N, Z, K, I, _dtype_code(x, "x"))
     ws = _space(lc_moe_workspace_size(shape), workspace, dev, "lc_moe_workspace_size",
-                (x, topk_idx, topk_gate, w_gate, w_up, w_down, fp8, packed))
+                (x, topk_idx, topk_gate, *((w_gate, w_up, w_down) if plain else (fp8, packed))))
     y = torch.empty_like(x)
     load = torch.empty(N + Z, dtype=torch.int32, device=dev)
     _on(dev, lc_moe_forward_picks, shape, x, _weights(None, None, w_gate, w_up, w_down, fp8, packed, fp8_act), topk_idx,

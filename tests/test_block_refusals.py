@@ -77,6 +77,17 @@ def test_forward_picks():
     refused("w_down must be contiguous", lambda: run(wd=zeros(3, 8, 16).transpose(1, 2)))
 
 
+def test_forward_picks_with_weights_in_another_form():
+    """The three matrices give the sizes then, and no more."""
+    x, idx, gate = zeros(4, 16), zeros(4, 2, dtype=torch.int32), zeros(4, 2, dtype=F)
+    wg, wd = zeros(3, 8, 16).to("meta"), zeros(3, 16, 8).to("meta")
+    for form in ("fp8", "packed"):
+        run = lambda wu=wg: lm.forward_picks(x, idx, gate, wg, wu, wd, 1, **{form: zeros(64, dtype=torch.uint8)})  # noqa: E731
+        refused(OFF_GPU, run)
+        refused("w_up: shape", lambda: run(wu=wd))
+    refused("w_gate is on meta", lambda: lm.forward_picks(x, idx, gate, wg, wg, wd, 1))
+
+
 def test_block_norm():
     x, w = zeros(4, 16), zeros(16, dtype=F)
     run = lambda x=x, w=w, **kw: lm.block_norm(x, w, **kw)  # noqa: E731
