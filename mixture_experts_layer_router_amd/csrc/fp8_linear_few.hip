@@ -10,10 +10,12 @@
 // neighbouring bytes, and the 16 x 16 x 128 product takes a run at once (32 x 32 x 64 touched twice as many
 // cache lines a load: 15.9 -> 14.1 us at T = 16, k = n = 6144).
 //
-// Measured, against one launch that quantises x and one or two that multiply (fp8_matmul.hip), us:
-//   k = n = 6144   T = 1: 10.0 (3.8 TB/s of W; 15.5)   16: 13.9 (17.1)   32: 20.4 (18.4)
-//   k = n = 1024   T = 1:  4.0 (9.2)                   64:  4.8 (9.8)   400:  8.2 (10.2)   777: 14.6 (10.6)
-//   k = n =  520   T = 1:  3.8 (8.1)                   64:  4.0 (9.1)   777:  6.0 (9.7)   4000: 23.7 (12.8)
+// Kernel times by trace, against those of the launch that quantises x and the one or two that multiply
+// (fp8_matmul.hip), us; (a call takes 9.5 us of the host's time unless a graph holds it):
+//   k = n = 6144   T = 1: 9.8 (3.9 TB/s of W; 15.5)   16: 13.6 (18.7)   32: 20.4 (20.1)
+//   k = n = 1024   T = 1: 3.9 (9.5)                   64:  4.8 (10.2)  400:  8.5 (10.6)   777: 14.6 (10.8)
+//   k = n =  520   T = 1: 3.7 (8.3)                   64:  4.0 (9.0)   400:  4.6 (10.0)   777:  6.2 (10.1)
+// (T = 32 and 777 of the wider ones go the other way, by the figures below.)
 // What bounds it is a CU's loads: a run of 32 rows of W and of 16 tokens is 8 KB, of 64 tokens 20 KB, and
 // every workgroup reads x anew.  linear_few weighs the two ways by kFewForms and the product's own figures.
 #include "block.h"

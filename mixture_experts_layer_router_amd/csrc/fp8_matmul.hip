@@ -3,20 +3,23 @@
 // v_mfma_scale_f32_32x32x64_f8f6f4 multiplies E4M3 codes and applies one E8M0 scale per row
 // of A and of B and 32 reduction elements, taken from the lane that holds them.  The products
 // are exact; the instruction adds its 64 products and the accumulator with about 12 bits below
-// the largest addend, which the result's rounding to bf16 (8 bits) covers.
+// the largest addend.  The result's rounding to bf16 (8 bits) covers that but where the sum is much
+// smaller than the root of its terms' squares: there the last bits of bf16 are the instruction's.
 //
 // A stage is 128 reduction columns, one scale block: BM + BN rows of 128 bytes, loaded into LDS
 // directly, 16-byte piece c of row r in slot c ^ (r & 7) (eight lanes of a fragment read then
 // fall on all banks), and the scale bytes of the tile's rows, laid out so that one word holds
 // those of a lane's rows in four row blocks.
 //
-// Measured: 16384 x 6144 x 6144 in 487-500 us, 2.5 PFLOP/s of a dense peak near 5 (a library's FP8
-// product with one scale a matrix, which has no scales to load: 504 us; this tiling without the
-// prefetched stream of stages 690), 16384 x 6144 x 2048 in 187, 2048 x 6144 x 16384 in 172.  The matrix
-// cores are busy 60% of the time.  A 256 x 256 tile is one wave per SIMD, so what a wave's reads of its
-// fragments from LDS (128 KB a stage, half the time of the stage's products) and the barrier between
+// Measured, products one after another (the card's clock moves with the length of the run: first 1 to 3 of
+// them, then 30, then 300): 16384 x 6144 x 6144 in 535-550, 560, 500 us, 2.1-2.5 PFLOP/s of a dense peak near
+// 5; 16384 x 6144 x 2048 in 196-216, 224, 190; 2048 x 6144 x 16384 in 189-201, 208, 179.  A library's FP8
+// product with one scale a matrix, which has no scales to load, in the same runs: 402-427, 463, 400; 170-184,
+// 187, 164; 159-178, 173, 151.  This tiling without the prefetched stream of stages took 690 where it took
+// 500.  The matrix cores are busy 60% of the time.  A 256 x 256 tile is one wave per SIMD, so what a wave's
+// reads of its fragments from LDS (128 KB a stage, half the time of the stage's products) and the barrier between
 // stages do not hide stays: of a stage's 1.7 us, 1.4-1.6 remain without the loads from memory, 0.8 with the
-// loads alone.  Four tiles of 128 x 128 read twice the bytes from the L2 and took 705 us.
+// loads alone.  Tiles of 128 x 128, two a CU, read twice the bytes from the L2 (720 us where these take 580).
 #include "block.h"
 #include "lds_dma.h"
 #include "train.h"
@@ -408,9 +411,10 @@ __global__ __launch_bounds__(256) void matmul_join_kernel(const float* __restric
 }
 
 // Tiles of mb x nb times 64 x 64, and what they take (us, measured): a stage with 1 .. fit workgroups
-// on a CU, and a unit's results.  M = 16384, N = K = 6144: 500 us in 256 x 256 tiles, 513 in 256 x 192;
-// M = 2048, N = 6144, K = 16384, 192 or 256 of them: 193 and 171; M = 1024, N = 4096, K = 1536: 23 us, 20,
-// 12.3 (128 x 128), 14.7 (64 x 64); M = N = K = 1000: 17.9, 16.0, 9.8, 6.8.
+// on a CU, and a unit's results.  In runs of 20, us in tiles of 256 x 256, 256 x 192, 128 x 128 and 64 x 64:
+// M = 16384, N = K = 6144: 582, 632, 720, 1356; M = 2048, N = 6144, K = 16384 (192 tiles of the first, 256 of the
+// second): 226, 205, 244, 386; M = 1024, N = 4096, K = 1536: 23.7, 20.8, 12.4, 15.7; M = N = K = 1000: 21.3, 15.6,
+// 9.4, 6.7; M = 64, N = K = 6144: 23.5, 21.5, 16.1, 14.1.
 struct Form {
   int mb, nb, fit;
   float stage[4], out;

@@ -228,7 +228,8 @@ struct NormBwArgs {
 
 // NEXT: the next row is loaded beside the present one's sums.  KEEP: the weights and all sums over tokens
 // stay in registers; else the weights are read in every row again, from the L2, and two of the sums stay
-// in LDS.  (With everything in registers, and spilled, d = 16384 ran at 1.3 TB/s; with these 3.8, fp32 4.5.)
+// in LDS.  (With everything in registers, and spilled, d = 16384 ran at 1.3 TB/s; with these 3.9, 8192 rows in
+// 410 us, fp32 4.8.)
 template <typename E, int NV, int THREADS, bool NEXT, bool KEEP>
 __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(NormBwArgs p) {
   constexpr int N = Vec<E>::N;
@@ -410,7 +411,7 @@ __global__ __launch_bounds__(1024) void norm_sums_kernel(const float* __restrict
 // waves two fit, of up to 3 four (T = 16384, d = 1032: 63 us with two of 3, 50 with four).  Beyond 256 of
 // them a workgroup has two rows at least, or its sums over them are as many bytes as the rows (T = 600,
 // d = 2048: 15.5 us with a row each, 13.6 with two).
-// 8 elements a thread in up to 12 waves leave 168 registers (fp32, d = 6144: 320 us for 10922 tokens, 361
+// 8 elements a thread in up to 12 waves leave 168 registers (fp32, d = 6144: 315 us for 10922 tokens, 361
 // with 16 elements in 6 waves), 16 in up to 8 waves 256, 16 in 16 waves 128: a row, and the sums in LDS.
 struct NormBwShape {
   int threads, nv, per_cu;

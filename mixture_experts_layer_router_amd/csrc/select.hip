@@ -2,9 +2,11 @@
 // (include/lc_moe_block.h): softmax or sigmoid scores, a bias for the choice, groups of experts,
 // top-K, renormalised gates.  One wavefront a token.
 //
-// Measured at T = 16384, E = 768: the choice (K = 12, sigmoid, 8 groups) takes 27-28 us, its 50 MB read at
-// 1.8 TB/s; the vector units bound it: 820 instructions a token fill 53 of its 66 thousand cycles.  The
-// gradient takes 20 us (5 TB/s).
+// Measured at T = 16384, E = 768: the choice (K = 12, sigmoid, 8 groups) takes 28-30 us by trace with the logits
+// in the last-level cache, 32 a call then and 37-39 with other logits in every call; the vector units bound it:
+// 820 instructions a token fill 53 of its 66 thousand cycles.  Softmax without groups 21 (call 22).  Where fp64
+// decides for every token it takes 120 (all scores equal), and 297 with K = 64, where more than 64 scores are
+// not below the bound (K above about 40).  The gradient takes 20-21 us (5 TB/s).
 #include "block.h"
 #include "logit_row.h"
 
