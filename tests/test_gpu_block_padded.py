@@ -125,3 +125,49 @@ def test_padded_rows_of_nan_have_a_gradient(T):
             if v is not None:
                 assert bool(torch.isfinite(a[k]).all()) and torch.equal(a[k], v), k
         assert not to_np(a["dx"])[~keep].any() and to_np(a["dx"])[keep].any() and to_np(a["dw_router"]).any()
+
+
+@pytest.mark.parametrize("T", [40, 700, 2100])
+def test_padded_batches_captured_and_replayed(T):
+    """A graph of forward and gradient, replayed on batches that are padded in other places, with eager work and waiting
+    between the replays: the eager calls' bits."""
+    import torch
+    say(f"padded batches captured T={T}")
+    c = layer(T=T) if T < 2000 else layer(T=T, d=6144, N=4, Z=2, K=2, I=64)
+    gt = lm().Gating("sigmoid", 2, 1, 2, True, 2.0)
+    ws, mask = workspace(c), torch.ones(T, dtype=torch.uint8, device=device())
+    x, dy = c["x"].clone(), c["dy"].clone()
+
+    def step(ws):
+        out = lm().forward(x, c["wr"], c["bias"], c["wg"], c["wu"], c["wd"], c["K"], workspace=ws, gating=gt, token_mask=mask)
+        return dict(lm().layer_backward(x, c["wr"], c["wg"], c["wu"], c["wd"], out, dy, ws, 0.1, 1e-3, token_mask=mask,
+                                        gating=gt), y=out["y"])
+
+    batches = [np.arange(T) % 3 != 1, np.ones(T, bool), np.arange(T) < T // 2, np.arange(T) % 64 >= 32]
+
+    def fill(keep):
+        x.copy_(without(c["x"], ~keep, float("nan")))
+        dy.copy_(without(c["dy"], ~keep, float("nan")))
+        mask.copy_(put(keep.astype(np.uint8)))
+
+    want = []
+    for keep in batches:
+        fill(keep)
+        want.append({k: v.clone() for k, v in step(workspace(c)).items() if v is not None})
+        assert all(bool(torch.isfinite(v).all()) for v in want[-1].values())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(ws)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step(ws)
+    for turn in range(2 * len(batches)):
+        i = turn % len(batches)
+        fill(batches[i])
+        g.replay()
+        torch.cuda.synchronize()
+        for k, v in want[i].items():
+            assert torch.equal(out[k], v), (turn, k)
+        step(workspace(c))  # eager work between
